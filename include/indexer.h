@@ -102,6 +102,9 @@ typedef enum {
 #define IDX_DEV_TIMEOUT 4u   /* a pipeline wait gave up; the kernel returned early */
 #define IDX_DEV_OVERFLOW 8u  /* more token rows than the output holds (flatten mode) */
 #define IDX_DEV_INTERNAL 16u /* the split-row selection's counts disagreed (a library bug) */
+#define IDX_DEV_BAD_ROW 32u  /* a block-table row index outside [0, num_rows) was skipped */
+#define IDX_DEV_NO_PAGE 64u  /* too few free pages: a child kept its parent's full pages only */
+#define IDX_DEV_BAD_REF 128u /* a held page without a reference (freed twice, or never counted) */
 
 #define IDX_NUM_HEADS 64
 #define IDX_HEAD_DIM 128
@@ -545,6 +548,153 @@ idx_status indexer_decode_topk_noalloc(const void* q, const float* weights,
                                        int32_t num_reqs, int32_t next_n, int32_t num_heads,
                                        int32_t head_dim, int32_t topk, int32_t* out_idx,
                                        uint32_t* dev_error, void* stream);
+
+/*
+ * Serving the selection: attention over a paged key/value cache
+ * --------------------------------------------------------------
+ * The step that consumes the indexer's selection, and the dense and windowed
+ * attention of the layers around it, over one paged cache. For query row t of
+ * head h and the keys s visible to it:
+ *
+ *     x_s = scale * q[t, h] . k_s     (kv head h / (num_heads / num_kv_heads))
+ *     lse[t, h] = log sum_s exp(x_s)
+ *     out[t, h] = sum_s exp(x_s - lse[t, h]) v_s
+ *
+ * and out = 0, lse = -inf when no key is visible. Request b's new tokens are
+ * rows query_start_loc[b] .. query_start_loc[b + 1] - 1; its key s lies in page
+ * block_table[b, s / 64], token s % 64. Rows in no request are left as they
+ * are. Products are of the 16-bit inputs with fp32 sums; scores, maxima and
+ * sums are fp32; the weights are rounded to the input type for the second
+ * product, and out once at the end.
+ *
+ * k and v: any strides (elements) over (page, token, kv head) that are
+ * multiples of 8, the head_dim values contiguous, 16-byte aligned (so a
+ * [pages, 64, kv heads, dim] cache, its head-major transpose, and K and V
+ * halves of one array are all views of this form). q: the same over (token,
+ * head). out contiguous [num_tokens, num_heads, head_dim].
+ *
+ * Token slots past a request's length, and pages past it, may hold anything:
+ * they are not read, or not used.
+ */
+enum { IDX_BF16 = 0, IDX_FP16 = 1 };
+
+typedef struct idx_attend {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* block_table;     /* [num_reqs, bt_width], row stride bt_stride */
+  const int32_t* seq_lens;        /* [num_reqs] keys, the new ones among them (paged form) */
+  const int32_t* query_start_loc; /* [num_reqs + 1], ascending, within [0, num_tokens] */
+  const int32_t* indices;         /* [num_tokens, topk], row stride indices_stride (selected form) */
+  void* out;
+  float* lse;                     /* nullable, [num_tokens, num_heads] */
+  void* workspace;                /* 256-byte aligned */
+  size_t workspace_bytes;
+  uint32_t* dev_error;            /* nullable */
+  int64_t q_stride_token, q_stride_head;
+  int64_t k_stride_page, k_stride_token, k_stride_head;
+  int64_t v_stride_page, v_stride_token, v_stride_head;
+  int64_t num_pages, bt_stride, indices_stride;
+  int32_t bt_width, num_reqs, num_tokens, num_heads, num_kv_heads;
+  int32_t head_dim;               /* 64 or 128 */
+  int32_t dtype;                  /* of q, k, v and out: IDX_BF16 or IDX_FP16 */
+  int32_t max_query_len;          /* longest request's new tokens (a hint; 0: unknown) */
+  int32_t window;                 /* 0: none (paged form) */
+  int32_t sinks;                  /* first keys a window leaves visible (paged form) */
+  int32_t topk;                   /* entries of a row's list (selected form) */
+  float scale;                    /* > 0 */
+} idx_attend;
+
+/* Bytes of workspace either attention call needs at most for these sizes, on
+ * the current CUDA device. */
+idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, int32_t num_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, size_t* bytes);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache: from single tokens
+ * (decode) over a few (speculative rows) to whole prompts, mixed freely in one
+ * batch. The new tokens' keys and values are in the cache already. Token i of
+ * a request with Q new tokens and L keys is at position p = L - Q + i and sees
+ * key s when s <= p and, with a window, p - s < window or s < sinks. (L < Q
+ * leaves rows of negative position, which see nothing.) Lengths outside the
+ * table set IDX_DEV_BAD_LEN and are clamped; a page that is read and lies
+ * outside the cache sets IDX_DEV_BAD_BLOCK.
+ */
+idx_status indexer_attend_paged(const idx_attend* a, void* stream);
+
+/*
+ * Attention of every token to the keys listed for it: indices[t] holds topk
+ * positions of t's request in any order, entries < 0 are empty (what
+ * indexer_decode_topk and indexer_prefill_topk write; every entry counts, so a
+ * position listed twice counts twice). seq_lens, max_query_len, window and
+ * sinks are not looked at. An entry outside the block table, or whose page
+ * lies outside the cache, sets IDX_DEV_BAD_BLOCK and is left out.
+ */
+idx_status indexer_attend_selected(const idx_attend* a, void* stream);
+
+/*
+ * Pages of the caches
+ * -------------------
+ * A pool is an array of pages: page p's page_bytes bytes start at base + p *
+ * page_stride (all multiples of 16). The caches of one block table (index
+ * cache, keys, values, of every layer) are pools with the same page numbers.
+ * Row r of the block table holds the first ceil(seq_lens[r] / 64) pages of its
+ * row; ref_counts[p] (int32 [num_pages]) is how many rows hold page p, 0 = free.
+ * Free pages are handed out lowest first.
+ */
+typedef struct idx_page_pool {
+  void* base;
+  int64_t page_stride; /* bytes */
+  int64_t page_bytes;
+} idx_page_pool;
+
+/* Copies page src[i] to page dst[i] in every pool, i < n (device arrays). A
+ * negative entry on either side is skipped, one >= num_pages sets
+ * IDX_DEV_BAD_BLOCK. No page may be a destination twice, or both a source and
+ * a destination of different copies. */
+idx_status indexer_copy_pages(const idx_page_pool* pools, int32_t num_pools, int64_t num_pages,
+                              const int32_t* src, const int32_t* dst, int32_t n,
+                              uint32_t* dev_error, void* stream);
+
+/*
+ * Forks n requests: row children[i] (empty before the call) becomes a copy of
+ * row parents[i]. Full pages are shared (their counts go up), a last page that
+ * is not full is copied in every pool to the lowest free page; seq_lens and the
+ * table follow. A parent may have several children; no row is parent and child.
+ * copy_src, copy_dst (int32 [n]) get the copies made, in the order of i, then
+ * -1. When free pages run out, IDX_DEV_NO_PAGE is set and the children left
+ * over hold the full pages only (their lengths cut to them). num_pools may be 0
+ * (then the caller makes the copies).
+ */
+idx_status indexer_fork_pages(const idx_page_pool* pools, int32_t num_pools, int64_t num_pages,
+                              int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+                              int32_t num_rows, int32_t* seq_lens, int32_t* ref_counts,
+                              const int32_t* parents, const int32_t* children, int32_t n,
+                              int32_t* copy_src, int32_t* copy_dst, uint32_t* dev_error,
+                              void* stream);
+
+/* Frees n distinct rows: their pages lose a reference (one without sets
+ * IDX_DEV_BAD_REF and stays at 0), their lengths become 0; the table's entries
+ * stay as they are. */
+idx_status indexer_free_pages(const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+                              int32_t num_rows, int32_t* seq_lens, int32_t* ref_counts,
+                              int64_t num_pages, const int32_t* rows, int32_t n,
+                              uint32_t* dev_error, void* stream);
+
+/* Bytes of workspace indexer_compact_pages needs. */
+idx_status indexer_compact_workspace_bytes(int64_t num_pages, size_t* bytes);
+
+/*
+ * Moves the pages in use to the front of the pools: with n of them, the i-th
+ * used page >= n goes to the i-th free page < n (pages below n stay). Data,
+ * ref_counts and the rows' table entries follow; remap[p] (int32 [num_pages])
+ * gets page p's new number, -1 if it was free; *num_live (device) gets n.
+ */
+idx_status indexer_compact_pages(const idx_page_pool* pools, int32_t num_pools, int64_t num_pages,
+                                 int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+                                 int32_t num_rows, const int32_t* seq_lens, int32_t* ref_counts,
+                                 int32_t* remap, int32_t* num_live, void* workspace,
+                                 size_t workspace_bytes, uint32_t* dev_error, void* stream);
 
 #ifdef __cplusplus
 }

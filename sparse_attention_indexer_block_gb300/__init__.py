@@ -7,9 +7,16 @@ first call does, and raises if it has not been built.
 """
 from .binding import (  # noqa: F401
     IndexerError,
+    attend_workspace,
     decode_workspace,
+    indexer_attend_paged,
+    indexer_attend_selected,
     indexer_block_topk,
+    indexer_compact_pages,
+    indexer_copy_pages,
     indexer_dcp_merge,
+    indexer_fork_pages,
+    indexer_free_pages,
     indexer_index_key_counts,
     indexer_decode_logits,
     indexer_decode_logits_mxfp4,

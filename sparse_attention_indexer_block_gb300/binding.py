@@ -21,8 +21,31 @@ IDX_OK = 0
 STATUS_NAMES = {0: "IDX_OK", 1: "IDX_ERR_INVALID_ARG", 2: "IDX_ERR_UNSUPPORTED",
                 3: "IDX_ERR_WORKSPACE", 4: "IDX_ERR_CUDA", 5: "IDX_ERR_CAPACITY"}
 DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_TIMEOUT, DEV_OVERFLOW = 1, 2, 4, 8
+DEV_BAD_ROW, DEV_NO_PAGE, DEV_BAD_REF = 32, 64, 128
 NUM_HEADS, HEAD_DIM, PAGE_TOKENS, PAGE_BYTES, MAX_TOPK = 64, 128, 64, 8448, 2048
 DCP_MAX_CANDIDATES = 16384
+
+
+class Attend(C.Structure):
+    """idx_attend of indexer.h."""
+    _fields_ = ([(n, C.c_void_p) for n in ("q", "k", "v", "block_table", "seq_lens",
+                                           "query_start_loc", "indices", "out", "lse",
+                                           "workspace")]
+                + [("workspace_bytes", C.c_size_t), ("dev_error", C.c_void_p)]
+                + [(n, C.c_int64) for n in ("q_stride_token", "q_stride_head", "k_stride_page",
+                                            "k_stride_token", "k_stride_head", "v_stride_page",
+                                            "v_stride_token", "v_stride_head", "num_pages",
+                                            "bt_stride", "indices_stride")]
+                + [(n, C.c_int32) for n in ("bt_width", "num_reqs", "num_tokens", "num_heads",
+                                            "num_kv_heads", "head_dim", "dtype", "max_query_len",
+                                            "window", "sinks", "topk")]
+                + [("scale", C.c_float)])
+
+
+class PagePool(C.Structure):
+    """idx_page_pool of indexer.h."""
+    _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("page_bytes", C.c_int64)]
+
 
 # exported symbols and their ctypes signatures (kept in step with indexer.h)
 _P, _I32, _I64, _SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
@@ -70,6 +93,19 @@ SIGNATURES = {
     "indexer_decode_logits_mxfp4": (C.c_int, [_P, _P, _P, _I64, _P, _I64, _I32, _P, _I32, _I32,
                                               _I32, _I32, _I32, _P, _I64, _P, _SZ, _P, _P]),
 }
+
+SIGNATURES.update({
+    "indexer_attend_workspace_bytes": (C.c_int, [_I32, _I32, _I32, _I32, _I32, C.POINTER(_SZ)]),
+    "indexer_attend_paged": (C.c_int, [C.POINTER(Attend), _P]),
+    "indexer_attend_selected": (C.c_int, [C.POINTER(Attend), _P]),
+    "indexer_copy_pages": (C.c_int, [C.POINTER(PagePool), _I32, _I64, _P, _P, _I32, _P, _P]),
+    "indexer_fork_pages": (C.c_int, [C.POINTER(PagePool), _I32, _I64, _P, _I64, _I32, _I32, _P, _P,
+                                     _P, _P, _I32, _P, _P, _P, _P]),
+    "indexer_free_pages": (C.c_int, [_P, _I64, _I32, _I32, _P, _P, _I64, _P, _I32, _P, _P]),
+    "indexer_compact_workspace_bytes": (C.c_int, [_I64, C.POINTER(_SZ)]),
+    "indexer_compact_pages": (C.c_int, [C.POINTER(PagePool), _I32, _I64, _P, _I64, _I32, _I32, _P,
+                                        _P, _P, _P, _P, _SZ, _P, _P]),
+})
 
 _lock = threading.Lock()
 _lib = None
@@ -513,3 +549,281 @@ def indexer_decode_topk_noalloc(q, weights, index_cache, block_table, row_seq_le
         int(q.shape[1]), int(q.shape[2]), topk, _ptr(out_idx), _ptr(dev_error), _stream(stream))
     _check("indexer_decode_topk_noalloc", st)
     return out_idx
+
+
+# ---------------------------------------------------------------------------
+# attention over a paged key/value cache, and the pages of the caches
+#
+# These calls look at their tensors' device, type, shape and strides and raise
+# IndexerError (invalid argument or unsupported) before anything is enqueued.
+# What they allocate (outputs, workspaces) belongs to the stream they run on.
+# ---------------------------------------------------------------------------
+
+_INVALID, _UNSUPPORTED = 1, 2
+
+
+def _need(ok, name, what, status=_INVALID):
+    if not ok:
+        raise IndexerError(name, status, what)
+
+
+def _need_i32(name, what, t, *shape):
+    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32, name, f"{what} must be an int32 tensor")
+    _need(t.dim() == len(shape) and all(n is None or int(a) == n for a, n in zip(t.shape, shape)),
+          name, f"{what} has shape {tuple(t.shape)}")
+    _need(t.dim() == 0 or t.stride(-1) == 1 or t.shape[-1] <= 1, name,
+          f"{what} must be contiguous in its last dimension")
+
+
+def _need_table(name, block_table, rows=None):
+    _need_i32(name, "block_table", block_table, rows, None)
+    _need(block_table.shape[1] >= 1, name, "block_table has no columns")
+    _need(block_table.shape[0] <= 1 or block_table.stride(0) >= block_table.shape[1], name,
+          "block_table's rows overlap")
+    return max(int(block_table.stride(0)), int(block_table.shape[1]))
+
+
+def _need_error(name, dev_error):
+    if dev_error is not None:
+        _need(isinstance(dev_error, torch.Tensor) and dev_error.element_size() == 4
+              and dev_error.numel() >= 1, name, "dev_error must be a tensor of a 32-bit word")
+
+
+def _need_device(name, first, *others):
+    _need(first.is_cuda, name, "tensors must be on a CUDA device")
+    for t in others:
+        _need(t is None or t.device == first.device, name, "tensors are on different devices")
+
+
+class _On:
+    """Allocates on, and hands out, the stream a call runs on (the current one
+    of the tensors' device, or the caller's)."""
+
+    def __init__(self, device, stream):
+        self.guard = None
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream is not None or torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.stream(stream if stream is not None
+                                           else torch.cuda.current_stream(device))
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+_ATTEND_TYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def attend_workspace(num_tokens: int, num_reqs: int, num_heads: int, num_kv_heads: int,
+                     head_dim: int, device="cuda"):
+    """Workspace for indexer_attend_paged / indexer_attend_selected calls of at most these sizes."""
+    n = C.c_size_t(0)
+    _check("indexer_attend_workspace_bytes",
+           load().indexer_attend_workspace_bytes(num_tokens, num_reqs, num_heads, num_kv_heads,
+                                                 head_dim, C.byref(n)))
+    return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+
+def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices, scale, out,
+            lse, workspace, dev_error, stream, max_query_len=0, window=0, sinks=0):
+    for what, t, dims in (("q", q, 3), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4)):
+        _need(isinstance(t, torch.Tensor) and t.dim() == dims, name, f"{what} must have {dims} dimensions")
+    tokens, heads, dim = q.shape
+    pages, page, kv_heads, _ = k_cache.shape
+    _need(q.dtype in _ATTEND_TYPES, name, f"q is {q.dtype}, not bfloat16 or float16", _UNSUPPORTED)
+    _need(k_cache.dtype == q.dtype and v_cache.dtype == q.dtype, name, "q, k_cache and v_cache differ in type")
+    _need(v_cache.shape == k_cache.shape and k_cache.shape[3] == dim, name,
+          "k_cache and v_cache must be [pages, 64, kv heads, head_dim of q]")
+    _need(page == PAGE_TOKENS, name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
+    _need(dim in (64, 128), name, f"head_dim {dim}, not 64 or 128", _UNSUPPORTED)
+    _need(kv_heads >= 1 and heads >= 1 and heads % kv_heads == 0, name,
+          f"{heads} heads over {kv_heads} kv heads")
+    for what, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(t.stride(-1) == 1, name, f"{what} must be contiguous in its last dimension")
+    _need_i32(name, "query_start_loc", query_start_loc, None)
+    reqs = int(query_start_loc.shape[0]) - 1
+    _need(reqs >= 0, name, "query_start_loc is empty")
+    bt_stride = _need_table(name, block_table, reqs)
+    if seq_lens is not None:
+        _need_i32(name, "seq_lens", seq_lens, reqs)
+    if indices is not None:
+        _need_i32(name, "indices", indices, tokens, None)
+        _need(indices.shape[1] >= 1, name, "indices has no columns")
+    for what, t, shape, dtype in (("out", out, (tokens, heads, dim), q.dtype),
+                                  ("lse", lse, (tokens, heads), torch.float32)):
+        if t is not None:
+            _need(isinstance(t, torch.Tensor) and tuple(t.shape) == shape and t.dtype == dtype
+                  and t.is_contiguous(), name, f"{what} must be contiguous {dtype} {shape}")
+    _need_error(name, dev_error)
+    _need_device(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices, out, lse,
+                 workspace, dev_error)
+    lib = load()
+    with _On(q.device, stream) as s:
+        if out is None:
+            out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = attend_workspace(tokens, reqs, heads, kv_heads, dim, q.device)
+        qs, ks, vs = q.stride(), k_cache.stride(), v_cache.stride()
+        a = Attend(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                   None if seq_lens is None else seq_lens.data_ptr(), query_start_loc.data_ptr(),
+                   None if indices is None else indices.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                   None if dev_error is None else dev_error.data_ptr(),
+                   qs[0], qs[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], pages, bt_stride,
+                   0 if indices is None else max(indices.stride(0), indices.shape[1]),
+                   block_table.shape[1], reqs, tokens, heads, kv_heads, dim, _ATTEND_TYPES[q.dtype],
+                   max_query_len, window, sinks, 0 if indices is None else indices.shape[1],
+                   dim ** -0.5 if scale is None else scale)
+        _check(name, getattr(lib, name)(C.byref(a), s))
+    return out, lse
+
+
+def indexer_attend_paged(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                         max_query_len: int = 0, scale=None, window: int = 0, sinks: int = 0,
+                         out=None, lse=None, workspace=None, dev_error=None, stream=None):
+    """Causal attention of every request's new tokens over its paged cache:
+    q [tokens, heads, dim] (bf16 or fp16, dim 64 or 128), k_cache and v_cache
+    [pages, 64, kv heads, dim] of the same type (any strides that keep dim
+    contiguous), block_table int32 [requests, width], seq_lens int32 [requests]
+    (keys, the new ones among them), query_start_loc int32 [requests + 1].
+    window > 0: a token sees the last `window` keys up to its own, and the
+    first `sinks` keys. max_query_len is a hint (0: unknown); scale defaults to
+    dim ** -0.5. Returns (out like q, lse float32 [tokens, heads])."""
+    return _attend("indexer_attend_paged", q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
+                   None, scale, out, lse, workspace, dev_error, stream, max_query_len, window, sinks)
+
+
+def indexer_attend_selected(q, k_cache, v_cache, block_table, indices, query_start_loc, scale=None,
+                            out=None, lse=None, workspace=None, dev_error=None, stream=None):
+    """Attention of every token to the keys listed for it: indices int32
+    [tokens, topk], positions of the token's request, entries < 0 empty (the
+    output of indexer_decode_topk / indexer_prefill_topk). Other arguments and
+    the result as indexer_attend_paged."""
+    _need(indices is not None, "indexer_attend_selected", "indices is missing")
+    return _attend("indexer_attend_selected", q, k_cache, v_cache, block_table, query_start_loc, None,
+                   indices, scale, out, lse, workspace, dev_error, stream)
+
+
+def _pools(name, pools, num_pages):
+    """The pools as idx_page_pool entries: tensors of [pages, ...] whose pages are contiguous."""
+    out = (PagePool * max(1, len(pools)))()
+    for i, t in enumerate(pools):
+        _need(isinstance(t, torch.Tensor) and t.dim() >= 2, name, "a pool must be a tensor [pages, ...]")
+        _need(num_pages is None or t.shape[0] == num_pages, name, "the pools differ in pages")
+        _need(t.shape[0] >= 1 and t[0].is_contiguous(), name, "a pool's pages must be contiguous")
+        size = t.element_size()
+        n = t[0].numel() * size
+        _need(n % 16 == 0 and t.data_ptr() % 16 == 0, name, "a pool's pages must be multiples of 16 bytes")
+        stride = t.stride(0) * size if t.shape[0] > 1 else n
+        out[i] = PagePool(t.data_ptr(), stride, n)
+        num_pages = t.shape[0]
+    return out, num_pages
+
+
+def _need_rows(name, block_table, seq_lens, ref_counts):
+    stride = _need_table(name, block_table)
+    _need_i32(name, "seq_lens", seq_lens, int(block_table.shape[0]))
+    _need_i32(name, "ref_counts", ref_counts, None)
+    return stride
+
+
+def indexer_copy_pages(pools, src, dst, dev_error=None, stream=None):
+    """Page src[i] to page dst[i] (int32 [n]) in every pool (tensors [pages, ...]); negative
+    entries are skipped."""
+    name = "indexer_copy_pages"
+    _need(len(pools) > 0, name, "no pools")
+    _need_i32(name, "src", src, None)
+    _need_i32(name, "dst", dst, int(src.shape[0]))
+    _need_error(name, dev_error)
+    arr, pages = _pools(name, pools, None)
+    _need_device(name, src, dst, dev_error, *pools)
+    with _On(src.device, stream) as s:
+        _check(name, load().indexer_copy_pages(arr, len(pools), pages, _ptr(src), _ptr(dst),
+                                               int(src.shape[0]), _ptr(dev_error), s))
+
+
+def indexer_fork_pages(pools, block_table, seq_lens, ref_counts, parents, children, copy_src=None,
+                       copy_dst=None, dev_error=None, stream=None):
+    """Makes block-table row children[i] (empty before) a copy of row parents[i]: full pages
+    shared, a partial last page copied to the lowest free page in every pool. block_table,
+    seq_lens, ref_counts (int32) and the pools change in place. Returns (copy_src, copy_dst)
+    int32 [n]: the page copies made, then -1."""
+    name = "indexer_fork_pages"
+    bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
+    _need_i32(name, "parents", parents, None)
+    n = int(parents.shape[0])
+    _need_i32(name, "children", children, n)
+    for what, t in (("copy_src", copy_src), ("copy_dst", copy_dst)):
+        if t is not None:
+            _need_i32(name, what, t, n)
+    _need_error(name, dev_error)
+    arr, pages = _pools(name, pools, int(ref_counts.shape[0]))
+    _need_device(name, block_table, seq_lens, ref_counts, parents, children, copy_src, copy_dst,
+                 dev_error, *pools)
+    with _On(block_table.device, stream) as s:
+        if copy_src is None:
+            copy_src = torch.empty_like(parents)
+        if copy_dst is None:
+            copy_dst = torch.empty_like(parents)
+        _check(name, load().indexer_fork_pages(
+            arr, len(pools), pages, _ptr(block_table), bt_stride, int(block_table.shape[1]),
+            int(block_table.shape[0]), _ptr(seq_lens), _ptr(ref_counts), _ptr(parents),
+            _ptr(children), n, _ptr(copy_src), _ptr(copy_dst), _ptr(dev_error), s))
+    return copy_src, copy_dst
+
+
+def indexer_free_pages(block_table, seq_lens, ref_counts, rows, dev_error=None, stream=None):
+    """Frees the block-table rows listed in rows (int32, distinct): their pages lose a reference
+    in ref_counts, their seq_lens become 0, in place."""
+    name = "indexer_free_pages"
+    bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
+    _need_i32(name, "rows", rows, None)
+    _need_error(name, dev_error)
+    _need_device(name, block_table, seq_lens, ref_counts, rows, dev_error)
+    with _On(block_table.device, stream) as s:
+        _check(name, load().indexer_free_pages(
+            _ptr(block_table), bt_stride, int(block_table.shape[1]), int(block_table.shape[0]),
+            _ptr(seq_lens), _ptr(ref_counts), int(ref_counts.shape[0]), _ptr(rows),
+            int(rows.shape[0]), _ptr(dev_error), s))
+
+
+def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, num_live=None,
+                          workspace=None, dev_error=None, stream=None):
+    """Moves the pages in use to the front of the pools (data, ref_counts and block_table in
+    place). Returns (remap int32 [pages]: a page's new number, -1 if it was free; num_live int32
+    [1] on the device: pages in use)."""
+    name = "indexer_compact_pages"
+    bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
+    pages = int(ref_counts.shape[0])
+    if remap is not None:
+        _need_i32(name, "remap", remap, pages)
+    if num_live is not None:
+        _need_i32(name, "num_live", num_live, 1)
+    _need_error(name, dev_error)
+    arr, pages = _pools(name, pools, pages)
+    _need_device(name, block_table, seq_lens, ref_counts, remap, num_live, workspace, dev_error, *pools)
+    lib = load()
+    with _On(block_table.device, stream) as s:
+        if remap is None:
+            remap = torch.empty(pages, dtype=torch.int32, device=ref_counts.device)
+        if num_live is None:
+            num_live = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
+        if workspace is None:
+            size = C.c_size_t(0)
+            _check("indexer_compact_workspace_bytes",
+                   lib.indexer_compact_workspace_bytes(pages, C.byref(size)))
+            workspace = torch.empty(int(size.value), dtype=torch.uint8, device=ref_counts.device)
+        _check(name, lib.indexer_compact_pages(
+            arr, len(pools), pages, _ptr(block_table), bt_stride, int(block_table.shape[1]),
+            int(block_table.shape[0]), _ptr(seq_lens), _ptr(ref_counts), _ptr(remap),
+            _ptr(num_live), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+            _ptr(dev_error), s))
+    return remap, num_live

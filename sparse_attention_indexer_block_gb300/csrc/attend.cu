@@ -1,0 +1,841 @@
+// Attention over a paged key/value cache: the split of the work over the CTAs,
+// the row-block kernel (mma.sync, one query block of 16 or 32 rows per unit)
+// and the join of units that several CTAs share. The same row-block kernel
+// attends to a list of selected tokens.
+#include <cuda_bf16.h>
+
+#include "attend.cuh"
+
+namespace saib {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kWarps = 4;        // of a row-block CTA
+constexpr int kSubKeys = 16;     // keys of a tile that one warp scores
+constexpr int kTile = kWarps * kSubKeys;
+constexpr int kStages = 3;       // sub-tiles in flight per warp
+static_assert(kTile == kPageTokens, "a tile is one page");
+
+// ---------------------------------------------------------------------------
+// small helpers
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: the 16 bytes are zero-filled and src is not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two fp32 values as a pair of T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  } else {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A pair of T values with its infinities and NaNs replaced by 0.
+template <typename T>
+__device__ __forceinline__ uint32_t clear_nonfinite(uint32_t v) {
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  if ((v & kExp) == kExp) v &= 0xffff0000u;
+  if ((v & (kExp << 16)) == kExp << 16) v &= 0xffffu;
+  return v;
+}
+
+constexpr float kLn2 = 0.693147180559945309f;
+
+// Inclusive sum of v over the block's threads; *total gets the sum of all.
+__device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += o;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  *total = warp_sums[kPlanThreads / 32 - 1];
+  return v + (warp ? warp_sums[warp - 1] : 0);
+}
+
+// Request of an entry: the last one whose first entry is not past it.
+__device__ __forceinline__ int entry_request(const int32_t* req_entry, int n, int32_t e) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (req_entry[mid] <= e) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Where CTA c of `grid` begins. A unit costs its tiles and kUnitOverhead; the
+// units, in the order request, kv head, entry, are cut into `grid` ranges of
+// equal cost. A cut inside a unit's overhead leaves the unit whole to the CTA
+// that begins there.
+__device__ int4 cut_at(const AttendParams& p, int c) {
+  const int64_t all = p.entry_cost[p.req_entry[p.num_reqs]] * p.num_kv_heads;
+  const int64_t pos = all / p.grid * c + all % p.grid * c / p.grid;
+  if (c >= p.grid || pos >= all) return make_int4(0, 0, 0, p.num_reqs);
+  int lo = 0, hi = p.num_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.entry_cost[p.req_entry[mid]] * p.num_kv_heads <= pos) lo = mid; else hi = mid - 1;
+  }
+  const int32_t e0 = p.req_entry[lo], e1 = p.req_entry[lo + 1];
+  const int64_t base = p.entry_cost[e0], cost = p.entry_cost[e1] - base;
+  const int64_t rest = pos - base * p.num_kv_heads;
+  const int32_t head = static_cast<int32_t>(rest / cost);
+  const int64_t at = base + rest % cost;
+  int32_t a = e0, b = e1 - 1;
+  while (a < b) {
+    const int32_t mid = (a + b + 1) >> 1;
+    if (p.entry_cost[mid] <= at) a = mid; else b = mid - 1;
+  }
+  const int32_t off = static_cast<int32_t>(at - p.entry_cost[a]) - kUnitOverhead;
+  return make_int4(a - e0, head, off > 0 ? off : 0, lo);
+}
+
+// One CTA: entries of the requests, their costs and the CTAs' cuts. Bound by
+// the latency of a few dependent loads and scans.
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendParams p) {
+  __shared__ int64_t sums[32];
+  pdl_wait();
+  pdl_trigger();
+  int64_t carry = 0, total;
+  for (int b0 = 0; b0 < p.num_reqs; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    const int64_t n = b < p.num_reqs ? request_entries(p, request_shape(p, b, true)) : 0;
+    const int64_t incl = carry + block_scan(n, sums, &total);
+    // offsets that are not ascending could ask for more entries than there is room for
+    if (b < p.num_reqs) {
+      if (incl > p.max_entries) set_error(p.dev_error, IDX_DEV_BAD_LEN);
+      p.req_entry[b] = static_cast<int32_t>(min(incl - n, static_cast<int64_t>(p.max_entries)));
+    }
+    carry += total;
+  }
+  const int32_t entries = static_cast<int32_t>(min(carry, static_cast<int64_t>(p.max_entries)));
+  if (threadIdx.x == 0) {
+    p.req_entry[p.num_reqs] = entries;
+    p.entry_cost[0] = 0;
+  }
+  __syncthreads();
+  carry = 0;
+  for (int e0 = 0; e0 < entries; e0 += kPlanThreads) {
+    const int e = e0 + threadIdx.x;
+    int64_t cost = 0;
+    if (e < entries) {
+      const int b = entry_request(p.req_entry, p.num_reqs, e);
+      cost = unit_tiles(p, request_shape(p, b, false), e - p.req_entry[b]).count + kUnitOverhead;
+    }
+    const int64_t incl = carry + block_scan(cost, sums, &total);
+    if (e < entries) p.entry_cost[e + 1] = incl;
+    carry += total;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c <= p.grid; c += kPlanThreads) p.bound[c] = cut_at(p, c);
+}
+
+// ---------------------------------------------------------------------------
+// row-block kernel
+// ---------------------------------------------------------------------------
+
+// Cuts of the selected form, where every unit has the same tiles: unit =
+// (token * head blocks + block) * kv heads + kv head.
+__device__ __forceinline__ int32_t selected_tiles(const AttendParams& p) {
+  return (p.topk + kTile - 1) / kTile;
+}
+__device__ __forceinline__ int2 selected_cut(const AttendParams& p, int64_t units, int c) {
+  const int64_t cost = selected_tiles(p) + kUnitOverhead, all = units * cost;
+  const int64_t pos = all / p.grid * c + all % p.grid * c / p.grid;
+  const int32_t off = static_cast<int32_t>(pos % cost) - kUnitOverhead;
+  return make_int2(static_cast<int32_t>(pos / cost), off > 0 ? off : 0);
+}
+__device__ __forceinline__ int64_t selected_units(const AttendParams& p) {
+  return static_cast<int64_t>(p.num_tokens) * ((p.group + p.rows - 1) / p.rows) * p.num_kv_heads;
+}
+
+// Request of a token row, or -1 when it lies in none.
+__device__ __forceinline__ int token_request(const AttendParams& p, int32_t t) {
+  int lo = 0, hi = p.num_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.query_start_loc[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return t >= p.query_start_loc[lo] && t < p.query_start_loc[lo + 1] ? lo : -1;
+}
+
+// A piece: tiles [t0, t1) of a unit.
+struct Piece {
+  int32_t req, head;   // request, kv head
+  int32_t row0;        // first row of the unit: (token - q0) * group + head of the group
+  int32_t rows;        // rows that exist
+  int32_t q0;          // token of row 0's request
+  int32_t ahead;       // position of the request's first new token
+  UnitTiles tiles;
+  int32_t t0, t1;
+};
+
+// Token and head of a unit's row.
+__device__ __forceinline__ void row_place(const AttendParams& p, const Piece& u, int r,
+                                          int64_t* token, int* head, int32_t* pos) {
+  const int32_t row = u.row0 + r;
+  const int32_t i = row / p.group;
+  *token = static_cast<int64_t>(u.q0) + i;
+  *head = u.head * p.group + (row - i * p.group);
+  *pos = u.ahead + i;
+}
+
+template <int D, int MT>
+struct RowsCfg {
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kStageBytes = 2 * kSubKeys * D * 2;  // K and V
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kQ = kRows * D * 2;
+  static constexpr int kPad = 4;  // floats between the joined rows, against bank conflicts
+  static constexpr int kJoin = kWarps * kRows * (D + kPad) * 4;
+  static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQ;
+};
+
+// Byte offset of 16-byte chunk c of row r in a tile of rows of D 16-bit values:
+// chunks are XORed with the row, so that eight rows' equal chunks lie in
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return r * (D * 2) + ((c ^ (r & 7)) << 4);
+}
+
+// Per unit of 16 * MT query rows of one kv head: the four warps take 16 keys
+// of every 64-key tile each, with a ring of kStages sub-tiles of K and V per
+// warp that its own lanes fill with 16-byte asynchronous copies (so no warp
+// waits for another inside a piece), products by mma.sync m16n8k16, running
+// maximum and sum per row; the warps' results are joined through shared memory
+// at the end of the piece. Bound by HBM (or L2) bytes of K and V when few rows
+// share a key: 4 * D bytes of a key feed 4 * D * 16 * MT multiply-adds.
+template <typename T, int D, int MT, bool kSel>
+__global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const AttendParams p) {
+  using C = RowsCfg<D, MT>;
+  constexpr int kChunks = D / 8;         // 16-byte chunks of a row
+  constexpr int kSteps = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
+  __shared__ uint32_t s_valid[kWarps][kStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cta = blockIdx.x;
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * C::kStageBytes);
+  uint8_t* q_smem = smem + (C::kSmem - C::kQ);
+  const uint32_t q_addr = smem_u32(q_smem);
+  const T* const kbase = static_cast<const T*>(p.k);
+  const T* const vbase = static_cast<const T*>(p.v);
+
+  pdl_wait();
+  pdl_trigger();
+
+  // this CTA's range of the units
+  int4 cur, end;
+  int64_t unit = 0, unit_end = 0;
+  if constexpr (kSel) {
+    const int64_t units = selected_units(p);
+    const int2 a = selected_cut(p, units, cta), b = selected_cut(p, units, cta + 1);
+    unit = a.x;
+    unit_end = b.x;
+    cur = make_int4(0, 0, a.y, 0);
+    end = make_int4(0, 0, b.y, 0);
+  } else {
+    cur = p.bound[cta];
+    end = p.bound[cta + 1];
+  }
+
+  for (;;) {
+    Piece u;
+    bool last;  // the range ends in (or before) this unit
+    if constexpr (kSel) {
+      last = unit >= unit_end;
+      if (last && end.z <= cur.z) break;
+      const int blocks = (p.group + p.rows - 1) / p.rows;
+      const int64_t tb = unit / p.num_kv_heads;
+      const int32_t token = static_cast<int32_t>(tb / blocks);
+      u.head = static_cast<int32_t>(unit % p.num_kv_heads);
+      u.row0 = static_cast<int32_t>(tb % blocks) * p.rows;
+      u.rows = min(p.rows, p.group - u.row0);
+      u.q0 = token;
+      u.ahead = 0;
+      u.req = token_request(p, token);
+      u.tiles = UnitTiles{0, 0, selected_tiles(p), 0, 0};
+      u.t0 = cur.z;
+      u.t1 = last ? end.z : u.tiles.count;
+    } else {
+      if (cur.w >= p.num_reqs) break;
+      last = cur.w == end.w && cur.y == end.y && cur.x == end.x;
+      if (last && end.z <= cur.z) break;
+      const ReqShape r = request_shape(p, cur.w, false);
+      const int64_t total = static_cast<int64_t>(r.nq) * p.group;
+      u.req = cur.w;
+      u.head = cur.y;
+      u.row0 = cur.x * p.rows;
+      u.rows = static_cast<int32_t>(min(static_cast<int64_t>(p.rows), total - u.row0));
+      u.q0 = r.q0;
+      u.ahead = r.keys - r.nq;
+      u.tiles = unit_tiles(p, r, cur.x);
+      u.t0 = cur.z;
+      u.t1 = last ? end.z : u.tiles.count;
+    }
+    const bool whole = u.t0 == 0 && u.t1 == u.tiles.count;
+
+    if (!kSel || u.req >= 0) {
+      const int32_t p_lo = u.tiles.p_lo, p_hi = u.tiles.p_hi;
+      // ---- queries: shared memory, then fragments
+      for (int i = threadIdx.x; i < C::kRows * kChunks; i += kWarps * 32) {
+        const int r = i / kChunks, c = i % kChunks;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < u.rows) {
+          int64_t token;
+          int head, pos;
+          row_place(p, u, r, &token, &head, &pos);
+          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                              token * p.q_stride_token + head * p.q_stride_head +
+                                              c * 8);
+        }
+        *reinterpret_cast<uint4*>(q_smem + chunk_at<D>(r, c)) = v;
+      }
+      __syncthreads();
+      uint32_t qf[MT == 1 ? kSteps : 1][4];
+      const auto q_frag = [&](uint32_t(&f)[4], int mt, int kk) {
+        const int m = lane >> 3, r = mt * 16 + (m & 1) * 8 + (lane & 7);
+        ldsm4(f, q_addr + chunk_at<D>(r, 2 * kk + (m >> 1)));
+      };
+      if constexpr (MT == 1) {
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) q_frag(qf[kk], 0, kk);
+      }
+      int32_t rpos[MT][2];  // positions of this thread's rows
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = mt * 16 + h * 8 + (lane >> 2);
+          int64_t token;
+          int head;
+          row_place(p, u, r, &token, &head, &rpos[mt][h]);
+          if (r >= u.rows) rpos[mt][h] = INT32_MIN;
+        }
+
+      float o[MT][D / 8][4];
+      float m[MT][2], l[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+        m[mt][0] = m[mt][1] = -INFINITY;
+        l[mt][0] = l[mt][1] = 0.f;
+      }
+
+      // ---- copies: where sub-tile j's keys lie is read one (list entries: two)
+      // sub-tiles before its copies are issued
+      const int32_t* const bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
+      const int32_t* const list =
+          kSel ? p.indices + static_cast<int64_t>(u.q0) * p.indices_stride : nullptr;
+      const auto load_index = [&](int j) -> int32_t {
+        const int at = j * kTile + warp * kSubKeys + (lane & 15);
+        return j < u.t1 && at < p.topk ? list[at] : -1;
+      };
+      const auto load_page = [&](int j, int32_t idx) -> int32_t {
+        if constexpr (kSel) {
+          if (idx < 0) return -1;
+          return idx < p.bt_width * kPageTokens ? bt[idx / kPageTokens] : -1;
+        } else {
+          return j < u.t1 ? bt[u.tiles.tile(j)] : 0;
+        }
+      };
+      const auto issue = [&](int j, int stage, int32_t idx, int32_t page) {
+        if (j < u.t1) {
+          const uint32_t dst = ring + stage * C::kStageBytes;
+          const int32_t s0 = kSel ? 0 : u.tiles.tile(j) * kTile + warp * kSubKeys;
+          bool ok;
+          if constexpr (kSel) {
+            ok = idx >= 0 && page >= 0 && page < p.num_pages;
+            if (idx >= 0 && !ok) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+            const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+            if (lane == 0) s_valid[warp][stage] = valid;
+          } else {
+            ok = page >= 0 && page < p.num_pages;
+            if (!ok && s0 <= p_hi) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+          }
+          constexpr int kKeysPerPass = 32 / kChunks;
+          const int c = lane % kChunks;
+#pragma unroll
+          for (int i = 0; i < kSubKeys / kKeysPerPass; ++i) {
+            const int key = i * kKeysPerPass + lane / kChunks;
+            int64_t pg = page;
+            int tok = 0;
+            bool v = ok;
+            if constexpr (kSel) {
+              pg = __shfl_sync(0xffffffffu, page, key);
+              tok = __shfl_sync(0xffffffffu, idx, key) & (kPageTokens - 1);
+              v = __shfl_sync(0xffffffffu, ok, key);
+            } else {
+              const int32_t s = s0 + key;
+              tok = warp * kSubKeys + key;
+              v = ok && s <= p_hi &&
+                  (static_cast<int64_t>(s) > static_cast<int64_t>(p_lo) - p.window || s < p.sinks);
+            }
+            if (!v) pg = 0, tok = 0;
+            const T* kp = kbase + pg * p.k_stride_page + tok * p.k_stride_token +
+                          u.head * p.k_stride_head + c * 8;
+            const T* vp = vbase + pg * p.v_stride_page + tok * p.v_stride_token +
+                          u.head * p.v_stride_head + c * 8;
+            cp_async16(dst + chunk_at<D>(key, c), kp, v);
+            cp_async16(dst + kSubKeys * D * 2 + chunk_at<D>(key, c), vp, v);
+          }
+        }
+        cp_commit();
+      };
+      int32_t idx1 = 0, idx2 = 0, page1;  // of the next sub-tile to issue (and the list entry after)
+      if constexpr (kSel) {
+        idx1 = load_index(u.t0);
+        idx2 = load_index(u.t0 + 1);
+      }
+      page1 = load_page(u.t0, idx1);
+      int next = u.t0, stage_in = 0;
+      const auto issue_next = [&] {
+        const int32_t idx = idx1, page = page1;
+        if constexpr (kSel) {
+          idx1 = idx2;
+          idx2 = load_index(next + 2);
+        }
+        page1 = load_page(next + 1, idx1);
+        issue(next, stage_in, idx, page);
+        ++next;
+        stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+      };
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue_next();
+
+      int stage = 0;
+      for (int j = u.t0; j < u.t1; ++j) {
+        cp_wait<kStages - 2>();
+        __syncwarp();
+        issue_next();  // into the sub-tile that the last round read
+        const int32_t s0 = kSel ? 0 : u.tiles.tile(j) * kTile + warp * kSubKeys;
+        uint32_t valid = 0xffffu;
+        bool any, all;
+        if constexpr (kSel) {
+          valid = s_valid[warp][stage];
+          any = valid != 0;
+          all = valid == 0xffffu;
+        } else {
+          const int64_t w_lo = static_cast<int64_t>(p_lo) - p.window;
+          const int64_t w_hi = static_cast<int64_t>(p_hi) - p.window;
+          any = s0 <= p_hi && (s0 + kSubKeys - 1 > w_lo || s0 < p.sinks);
+          all = s0 + kSubKeys - 1 <= p_lo && (s0 > w_hi || s0 + kSubKeys <= p.sinks);
+        }
+        if (any) {
+          const uint32_t kt = ring + stage * C::kStageBytes, vt = kt + kSubKeys * D * 2;
+          float s[MT][2][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < kSteps; ++kk) {
+            uint32_t b[4];
+            const int g = lane >> 3;
+            ldsm4(b, kt + chunk_at<D>((g >> 1) * 8 + (lane & 7), 2 * kk + (g & 1)));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t f[4];
+              if constexpr (MT == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = qf[kk][e];
+              } else {
+                q_frag(f, mt, kk);
+              }
+              mma16816<T>(s[mt][0], f, b[0], b[1]);
+              mma16816<T>(s[mt][1], f, b[2], b[3]);
+            }
+          }
+          const auto sees = [&](int32_t pos, int32_t k) {
+            return k <= pos && (k < p.sinks || pos - k < p.window);
+          };
+          uint32_t pa[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float alpha[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float x[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the sub-tile, c = lane % 4
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = s[mt][e >> 1][h * 2 + (e & 1)] * p.scale_log2;
+              if (!all) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int key = (e >> 1) * 8 + 2 * (lane & 3) + (e & 1);
+                  if (!(kSel ? (valid >> key) & 1 : sees(rpos[mt][h], s0 + key)))
+                    x[e] = -INFINITY;
+                }
+              }
+              float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+              mx = fmaxf(mx, m[mt][h]);
+              const float base = mx == -INFINITY ? 0.f : mx;
+              alpha[h] = exp2_approx(m[mt][h] - base);
+              m[mt][h] = mx;
+              float sum = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                x[e] = exp2_approx(x[e] - base);
+                sum += x[e];
+              }
+              l[mt][h] = l[mt][h] * alpha[h] + sum;
+              // the weights are rounded to T for the second product (half a step of T each);
+              // their sum is of the unrounded ones
+              pa[mt][h] = pack2<T>(x[0], x[1]);
+              pa[mt][2 + h] = pack2<T>(x[2], x[3]);
+            }
+            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                o[mt][n][0] *= alpha[0];
+                o[mt][n][1] *= alpha[0];
+                o[mt][n][2] *= alpha[1];
+                o[mt][n][3] *= alpha[1];
+              }
+            }
+          }
+          const auto v_frag = [&](uint32_t(&b)[4], int cc) {
+            const int g = lane >> 3;
+            ldsm4_t(b, vt + chunk_at<D>((g & 1) * 8 + (lane & 7), 2 * cc + (g >> 1)));
+          };
+          // A key that some rows see and others do not: a weight of 0 times an infinity or NaN
+          // would reach the rows that do not, so such values are left out of the product and
+          // added to the rows that see them.
+          bool odd = false;
+          if (!kSel && !all) {
+#pragma unroll
+            for (int cc = 0; cc < kSteps; ++cc) {
+              uint32_t b[4];
+              v_frag(b, cc);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) odd |= clear_nonfinite<T>(b[e]) != b[e];
+            }
+            odd = __any_sync(0xffffffffu, odd);
+          }
+#pragma unroll
+          for (int cc = 0; cc < kSteps; ++cc) {
+            uint32_t b[4];
+            v_frag(b, cc);
+            if (odd) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = clear_nonfinite<T>(b[e]);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816<T>(o[mt][2 * cc], pa[mt], b[0], b[1]);
+              mma16816<T>(o[mt][2 * cc + 1], pa[mt], b[2], b[3]);
+            }
+          }
+          if (odd) {
+            const T* v = reinterpret_cast<const T*>(smem + (vt - smem_u32(smem)));
+#pragma unroll 1
+            for (int key = 0; key < kSubKeys; ++key)
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float x =
+                      static_cast<float>(v[chunk_at<D>(key, n) / 2 + 2 * (lane & 3) + e]);
+                  if (!isfinite(x)) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                      for (int h = 0; h < 2; ++h)
+                        if (sees(rpos[mt][h], s0 + key)) o[mt][n][2 * h + e] += x;
+                  }
+                }
+          }
+        }
+        __syncwarp();
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+      }
+      cp_wait<0>();
+      __syncthreads();  // the rings are free: the warps' results go there
+
+      // ---- join of the four warps
+      float* const join = reinterpret_cast<float*>(smem);
+      constexpr int kPitch = D + C::kPad;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = mt * 16 + h * 8 + (lane >> 2);
+          float sum = l[mt][h];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if ((lane & 3) == 0) {
+            s_m[warp][r] = m[mt][h];
+            s_l[warp][r] = sum;
+          }
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(join + (warp * C::kRows + r) * kPitch + n * 8 +
+                                       2 * (lane & 3)) =
+                make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < u.rows * (D / 4); i += kWarps * 32) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = exp2_approx(s_m[w][r] - base);
+          const float4 a =
+              *reinterpret_cast<const float4*>(join + (w * C::kRows + r) * kPitch + d);
+          sum += f * s_l[w][r];
+          v.x += f * a.x;
+          v.y += f * a.y;
+          v.z += f * a.z;
+          v.w += f * a.w;
+        }
+        if (whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          int64_t token;
+          int head, pos;
+          row_place(p, u, r, &token, &head, &pos);
+          const int64_t at = token * p.num_heads + head;
+          const uint2 b = make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * D + d) = b;
+          if (d == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
+        } else {
+          const int64_t slot = 2 * static_cast<int64_t>(cta) + (u.t0 == 0 ? 1 : 0);
+          *reinterpret_cast<float4*>(p.part_o + (slot * p.rows + r) * D + d) = v;
+          if (d == 0) p.part_ml[slot * p.rows + r] = make_float2(mx, sum);
+        }
+      }
+      __syncthreads();
+    }
+
+    if (last) break;
+    // ---- next unit
+    cur.z = 0;
+    if constexpr (kSel) {
+      ++unit;
+    } else {
+      const int32_t n = p.req_entry[cur.w + 1] - p.req_entry[cur.w];
+      if (++cur.x == n) {
+        cur.x = 0;
+        if (++cur.y == p.num_kv_heads) {
+          cur.y = 0;
+          do ++cur.w;
+          while (cur.w < p.num_reqs && p.req_entry[cur.w + 1] == p.req_entry[cur.w]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// join of the pieces of units that several CTAs share
+// ---------------------------------------------------------------------------
+
+constexpr int kCombineWarps = 4;
+
+// Block (c, y): the unit whose first piece ends CTA c's range, rows 4y .. 4y +
+// 3, a warp each. Only cuts inside a unit leave work; the pieces are joined in
+// the order of the CTAs, so the result does not depend on their timing.
+template <typename T, int D, bool kSel>
+__global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(const AttendParams p) {
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+  constexpr int kV = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  Piece u;
+  // a cut as (unit, tile) with the unit as three numbers
+  const auto cut = [&](int at) -> int4 {
+    if constexpr (kSel) {
+      const int2 x = selected_cut(p, selected_units(p), at);
+      return make_int4(x.x, 0, x.y, 0);
+    } else {
+      return p.bound[at];
+    }
+  };
+  const auto same = [](const int4& a, const int4& b) {
+    return a.x == b.x && a.y == b.y && a.w == b.w;
+  };
+  const int4 here = cut(c), next = cut(c + 1);
+  if (next.z == 0 || (same(here, next) && here.z > 0)) return;
+  if constexpr (kSel) {
+    const int blocks = (p.group + p.rows - 1) / p.rows;
+    const int64_t tb = next.x / p.num_kv_heads;
+    u.q0 = static_cast<int32_t>(tb / blocks);
+    u.head = next.x % p.num_kv_heads;
+    u.row0 = static_cast<int32_t>(tb % blocks) * p.rows;
+    u.rows = min(p.rows, p.group - u.row0);
+    u.ahead = 0;
+    if (token_request(p, u.q0) < 0) return;
+  } else {
+    if (next.w >= p.num_reqs) return;
+    const ReqShape q = request_shape(p, next.w, false);
+    u.q0 = q.q0;
+    u.head = next.y;
+    u.row0 = next.x * p.rows;
+    u.rows = static_cast<int32_t>(
+        min(static_cast<int64_t>(p.rows), static_cast<int64_t>(q.nq) * p.group - u.row0));
+    u.ahead = 0;
+  }
+  if (r >= u.rows) return;
+  float mx = -INFINITY, sum = 0.f, v[kV];
+#pragma unroll
+  for (int e = 0; e < kV; ++e) v[e] = 0.f;
+  int4 at = next;
+  for (int cc = c; cc < p.grid; ++cc) {
+    // the piece of CTA cc: up to `stop` when that lies in the unit, else to its end
+    const int4 stop = cc == c ? next : cut(cc + 1);
+    const bool in = same(stop, next) && stop.z > 0;
+    if (cc == c || !in || stop.z > at.z) {
+      const int64_t slot = 2 * static_cast<int64_t>(cc) + (cc == c ? 1 : 0);
+      const float2 ml = p.part_ml[slot * p.rows + r];
+      const float* src = p.part_o + (slot * p.rows + r) * D + lane * kV;
+      const float top = fmaxf(mx, ml.x), base = top == -INFINITY ? 0.f : top;
+      const float fa = exp2_approx(mx - base), fb = exp2_approx(ml.x - base);
+      sum = sum * fa + ml.y * fb;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) v[e] = v[e] * fa + src[e] * fb;
+      mx = top;
+    }
+    if (!in) break;
+    at = stop;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  int64_t token;
+  int head, pos;
+  row_place(p, u, r, &token, &head, &pos);
+  const int64_t out = token * p.num_heads + head;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + out * D + lane * kV);
+#pragma unroll
+  for (int e = 0; e < kV; e += 2) dst[e / 2] = pack2<T>(v[e] * inv, v[e + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[out] = (mx + log2f(sum)) * kLn2;
+}
+
+template <typename T, int D, int MT, bool kSel>
+idx_status launch_rows_as(const AttendParams& p, cudaStream_t s) {
+  using C = RowsCfg<D, MT>;
+  const auto kernel = attend_rows_kernel<T, D, MT, kSel>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(launch_pdl(kernel, p.grid, kWarps * 32, C::kSmem, s, p));
+}
+
+template <typename T, int D>
+idx_status launch_rows_d(const AttendParams& p, int mt, cudaStream_t s) {
+  if (p.indices)
+    return mt == 1 ? launch_rows_as<T, D, 1, true>(p, s) : launch_rows_as<T, D, 2, true>(p, s);
+  return mt == 1 ? launch_rows_as<T, D, 1, false>(p, s) : launch_rows_as<T, D, 2, false>(p, s);
+}
+
+template <typename T, int D>
+idx_status launch_combine_as(const AttendParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid, (p.rows + kCombineWarps - 1) / kCombineWarps);
+  cfg.blockDim = dim3(kCombineWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(p.indices
+                         ? cudaLaunchKernelEx(&cfg, attend_combine_kernel<T, D, true>, p)
+                         : cudaLaunchKernelEx(&cfg, attend_combine_kernel<T, D, false>, p));
+}
+
+}  // namespace
+
+idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s) {
+  return cuda_status(launch_pdl(attend_plan_kernel, 1, kPlanThreads, 0, s, p));
+}
+
+idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, int mt,
+                              cudaStream_t s) {
+  if (half)
+    return head_dim == 64 ? launch_rows_d<__half, 64>(p, mt, s)
+                          : launch_rows_d<__half, 128>(p, mt, s);
+  return head_dim == 64 ? launch_rows_d<__nv_bfloat16, 64>(p, mt, s)
+                        : launch_rows_d<__nv_bfloat16, 128>(p, mt, s);
+}
+
+idx_status launch_attend_combine(const AttendParams& p, int head_dim, bool half, cudaStream_t s) {
+  if (half)
+    return head_dim == 64 ? launch_combine_as<__half, 64>(p, s)
+                          : launch_combine_as<__half, 128>(p, s);
+  return head_dim == 64 ? launch_combine_as<__nv_bfloat16, 64>(p, s)
+                        : launch_combine_as<__nv_bfloat16, 128>(p, s);
+}
+
+}  // namespace saib

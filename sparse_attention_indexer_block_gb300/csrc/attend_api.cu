@@ -1,0 +1,202 @@
+// C entry points of the attention calls: argument checks, the choice of a
+// kernel, the workspace and the launches.
+#include <math.h>
+
+#include "attend.cuh"
+
+namespace saib {
+
+namespace {
+
+constexpr int kRowsCtasPerSm = 2;
+
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+struct AttendWs {
+  size_t req_entry, entry_cost, bound, part_o, part_ml, total;
+};
+
+int64_t entry_bound(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t rows) {
+  return (num_tokens * group + rows - 1) / rows + num_reqs;
+}
+
+AttendWs attend_ws(int64_t num_reqs, int64_t max_entries, int64_t grid, int64_t rows,
+                   int64_t head_dim) {
+  AttendWs w{};
+  size_t off = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = round_up(off + bytes, 256);
+    return o;
+  };
+  w.req_entry = take(4 * static_cast<size_t>(num_reqs + 1));
+  w.entry_cost = take(8 * static_cast<size_t>(max_entries + 1));
+  w.bound = take(16 * static_cast<size_t>(grid + 1));
+  w.part_o = take(4 * static_cast<size_t>(2 * grid * rows * head_dim));
+  w.part_ml = take(8 * static_cast<size_t>(2 * grid * rows));
+  w.total = off;
+  return w;
+}
+
+// How a call is run: query rows per unit, keys per tile, CTAs.
+struct Variant {
+  int mt;  // row-block kernel: 16-row blocks per unit
+  int32_t rows, tile, grid;
+};
+
+Variant rows_variant(int64_t rows_per_head) {
+  const int mt = rows_per_head <= 16 ? 1 : 2;
+  return Variant{mt, 16 * mt, kPageTokens, kRowsCtasPerSm * device_sm_count()};
+}
+
+size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
+  size_t most = 0;
+  for (const int64_t rows : {int64_t{1}, int64_t{17}}) {
+    const Variant v = rows_variant(rows);
+    const size_t n = attend_ws(num_reqs, entry_bound(num_tokens, num_reqs, group, v.rows), v.grid,
+                               v.rows, head_dim)
+                         .total;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
+
+// The checks that both forms share.
+idx_status check_attend(const idx_attend* a) {
+  if (!a) return IDX_ERR_INVALID_ARG;
+  if (a->dtype != IDX_BF16 && a->dtype != IDX_FP16) return IDX_ERR_UNSUPPORTED;
+  if (a->head_dim != 64 && a->head_dim != 128) return IDX_ERR_UNSUPPORTED;
+  if (a->num_tokens < 0 || a->num_reqs < 0 || a->num_heads < 1 || a->num_kv_heads < 1)
+    return IDX_ERR_INVALID_ARG;
+  if (a->num_heads % a->num_kv_heads != 0) return IDX_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->num_tokens) * a->num_heads > INT32_MAX) return IDX_ERR_UNSUPPORTED;
+  if (!(a->scale > 0.f) || !isfinite(a->scale)) return IDX_ERR_INVALID_ARG;
+  if (a->num_pages < 1 || a->num_pages > INT32_MAX || a->bt_width < 1 ||
+      a->bt_width > INT32_MAX / kPageTokens || a->bt_stride < a->bt_width)
+    return IDX_ERR_INVALID_ARG;
+  if (a->num_tokens == 0 || a->num_reqs == 0) return IDX_OK;
+  if (!a->q || !a->k || !a->v || !a->out || !a->block_table || !a->query_start_loc)
+    return IDX_ERR_INVALID_ARG;
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16) ||
+      !aligned(a->block_table, 4) || !aligned(a->query_start_loc, 4) || !aligned(a->lse, 4))
+    return IDX_ERR_INVALID_ARG;
+  if (!stride_ok(a->q_stride_token) || !stride_ok(a->q_stride_head) ||
+      !stride_ok(a->k_stride_page) || !stride_ok(a->k_stride_token) ||
+      !stride_ok(a->k_stride_head) || !stride_ok(a->v_stride_page) ||
+      !stride_ok(a->v_stride_token) || !stride_ok(a->v_stride_head))
+    return IDX_ERR_INVALID_ARG;
+  if (!a->workspace || !aligned(a->workspace, 256)) return IDX_ERR_INVALID_ARG;
+  return IDX_OK;
+}
+
+AttendParams attend_params(const idx_attend* a) {
+  AttendParams p{};
+  p.q = a->q;
+  p.q_stride_token = a->q_stride_token;
+  p.q_stride_head = a->q_stride_head;
+  p.k = a->k;
+  p.v = a->v;
+  p.k_stride_page = a->k_stride_page;
+  p.k_stride_token = a->k_stride_token;
+  p.k_stride_head = a->k_stride_head;
+  p.v_stride_page = a->v_stride_page;
+  p.v_stride_token = a->v_stride_token;
+  p.v_stride_head = a->v_stride_head;
+  p.num_pages = a->num_pages;
+  p.block_table = a->block_table;
+  p.bt_stride = a->bt_stride;
+  p.bt_width = a->bt_width;
+  p.query_start_loc = a->query_start_loc;
+  p.num_reqs = a->num_reqs;
+  p.num_tokens = a->num_tokens;
+  p.num_heads = a->num_heads;
+  p.num_kv_heads = a->num_kv_heads;
+  p.group = a->num_heads / a->num_kv_heads;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.window = INT32_MAX;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.dev_error = a->dev_error;
+  return p;
+}
+
+idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& v) {
+  p->rows = v.rows;
+  p->tile = v.tile;
+  p->grid = v.grid;
+  p->max_entries =
+      static_cast<int32_t>(entry_bound(a->num_tokens, a->num_reqs, p->group, v.rows));
+  const AttendWs w = attend_ws(a->num_reqs, p->max_entries, v.grid, v.rows, a->head_dim);
+  if (a->workspace_bytes < w.total) return IDX_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  p->req_entry = reinterpret_cast<int32_t*>(ws + w.req_entry);
+  p->entry_cost = reinterpret_cast<int64_t*>(ws + w.entry_cost);
+  p->bound = reinterpret_cast<int4*>(ws + w.bound);
+  p->part_o = reinterpret_cast<float*>(ws + w.part_o);
+  p->part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  return IDX_OK;
+}
+
+}  // namespace
+}  // namespace saib
+
+using namespace saib;
+
+extern "C" {
+
+idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, int32_t num_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, size_t* bytes) {
+  if (!bytes || num_tokens < 0 || num_reqs < 0 || num_heads < 1 || num_kv_heads < 1 ||
+      num_heads % num_kv_heads != 0)
+    return IDX_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) ||
+      static_cast<int64_t>(num_tokens) * num_heads > INT32_MAX)
+    return IDX_ERR_UNSUPPORTED;
+  *bytes = most_workspace(num_tokens, num_reqs, num_heads / num_kv_heads, head_dim);
+  return IDX_OK;
+}
+
+idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
+  idx_status st = check_attend(a);
+  if (st != IDX_OK) return st;
+  if (a->window < 0 || a->sinks < 0 || a->max_query_len < 0) return IDX_ERR_INVALID_ARG;
+  if (a->num_tokens == 0 || a->num_reqs == 0) return IDX_OK;
+  if (!a->seq_lens || !aligned(a->seq_lens, 4)) return IDX_ERR_INVALID_ARG;
+  AttendParams p = attend_params(a);
+  p.seq_lens = a->seq_lens;
+  if (a->window > 0) {
+    p.window = a->window;
+    p.sinks = a->sinks;
+  }
+  const int64_t longest = a->max_query_len > 0 ? a->max_query_len : a->num_tokens;
+  const Variant v = rows_variant(longest * p.group);
+  if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool half = a->dtype == IDX_FP16;
+  if ((st = launch_attend_plan(p, s)) != IDX_OK) return st;
+  if ((st = launch_attend_rows(p, a->head_dim, half, v.mt, s)) != IDX_OK) return st;
+  return launch_attend_combine(p, a->head_dim, half, s);
+}
+
+idx_status indexer_attend_selected(const idx_attend* a, void* stream) {
+  idx_status st = check_attend(a);
+  if (st != IDX_OK) return st;
+  if (a->topk < 1 || a->indices_stride < a->topk) return IDX_ERR_INVALID_ARG;
+  if (a->num_tokens == 0 || a->num_reqs == 0) return IDX_OK;
+  if (!a->indices || !aligned(a->indices, 4)) return IDX_ERR_INVALID_ARG;
+  AttendParams p = attend_params(a);
+  p.indices = a->indices;
+  p.indices_stride = a->indices_stride;
+  p.topk = a->topk;
+  const Variant v = rows_variant(p.group);
+  if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool half = a->dtype == IDX_FP16;
+  if ((st = launch_attend_rows(p, a->head_dim, half, v.mt, s)) != IDX_OK) return st;
+  return launch_attend_combine(p, a->head_dim, half, s);
+}
+
+}  // extern "C"
