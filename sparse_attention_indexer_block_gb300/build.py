@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsaib.so")
 SOURCES = ["api.cu", "prep.cu", "score_select.cu", "row_select.cu", "dcp.cu",
-           "block_select.cu", "no_alloc.cu", "attend_api.cu", "attend.cu", "pages.cu"]
+           "block_select.cu", "no_alloc.cu", "attend_api.cu", "attend.cu", "attend_tc.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

@@ -2,8 +2,6 @@
 // the row-block kernel (mma.sync, one query block of 16 or 32 rows per unit)
 // and the join of units that several CTAs share. The same row-block kernel
 // attends to a list of selected tokens.
-#include <cuda_bf16.h>
-
 #include "attend.cuh"
 
 namespace saib {
@@ -20,17 +18,6 @@ static_assert(kTile == kPageTokens, "a tile is one page");
 // ---------------------------------------------------------------------------
 // small helpers
 // ---------------------------------------------------------------------------
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // 0: the 16 bytes are zero-filled and src is not read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -61,35 +48,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// Two fp32 values as a pair of T, the first in the low half.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (std::is_same<T, __half>::value) {
-    __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&h);
-  } else {
-    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&h);
-  }
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// A pair of T values with its infinities and NaNs replaced by 0.
-template <typename T>
-__device__ __forceinline__ uint32_t clear_nonfinite(uint32_t v) {
-  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-  if ((v & kExp) == kExp) v &= 0xffff0000u;
-  if ((v & (kExp << 16)) == kExp << 16) v &= 0xffffu;
-  return v;
-}
-
-constexpr float kLn2 = 0.693147180559945309f;
 
 // Inclusive sum of v over the block's threads; *total gets the sum of all.
 __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
@@ -124,7 +82,7 @@ __device__ __forceinline__ int entry_request(const int32_t* req_entry, int n, in
   return lo;
 }
 
-// Where CTA c of `grid` begins. A unit costs its tiles and kUnitOverhead; the
+// Where CTA c of `grid` begins. A unit costs its tiles and p.unit_overhead; the
 // units, in the order request, kv head, entry, are cut into `grid` ranges of
 // equal cost. A cut inside a unit's overhead leaves the unit whole to the CTA
 // that begins there.
@@ -147,7 +105,7 @@ __device__ int4 cut_at(const AttendParams& p, int c) {
     const int32_t mid = (a + b + 1) >> 1;
     if (p.entry_cost[mid] <= at) a = mid; else b = mid - 1;
   }
-  const int32_t off = static_cast<int32_t>(at - p.entry_cost[a]) - kUnitOverhead;
+  const int32_t off = static_cast<int32_t>(at - p.entry_cost[a]) - p.unit_overhead;
   return make_int4(a - e0, head, off > 0 ? off : 0, lo);
 }
 
@@ -181,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
     int64_t cost = 0;
     if (e < entries) {
       const int b = entry_request(p.req_entry, p.num_reqs, e);
-      cost = unit_tiles(p, request_shape(p, b, false), e - p.req_entry[b]).count + kUnitOverhead;
+      cost = unit_tiles(p, request_shape(p, b, false), e - p.req_entry[b]).count + p.unit_overhead;
     }
     const int64_t incl = carry + block_scan(cost, sums, &total);
     if (e < entries) p.entry_cost[e + 1] = incl;
@@ -201,9 +159,9 @@ __device__ __forceinline__ int32_t selected_tiles(const AttendParams& p) {
   return (p.topk + kTile - 1) / kTile;
 }
 __device__ __forceinline__ int2 selected_cut(const AttendParams& p, int64_t units, int c) {
-  const int64_t cost = selected_tiles(p) + kUnitOverhead, all = units * cost;
+  const int64_t cost = selected_tiles(p) + p.unit_overhead, all = units * cost;
   const int64_t pos = all / p.grid * c + all % p.grid * c / p.grid;
-  const int32_t off = static_cast<int32_t>(pos % cost) - kUnitOverhead;
+  const int32_t off = static_cast<int32_t>(pos % cost) - p.unit_overhead;
   return make_int2(static_cast<int32_t>(pos / cost), off > 0 ? off : 0);
 }
 __device__ __forceinline__ int64_t selected_units(const AttendParams& p) {
@@ -218,27 +176,6 @@ __device__ __forceinline__ int token_request(const AttendParams& p, int32_t t) {
     if (p.query_start_loc[mid] <= t) lo = mid; else hi = mid - 1;
   }
   return t >= p.query_start_loc[lo] && t < p.query_start_loc[lo + 1] ? lo : -1;
-}
-
-// A piece: tiles [t0, t1) of a unit.
-struct Piece {
-  int32_t req, head;   // request, kv head
-  int32_t row0;        // first row of the unit: (token - q0) * group + head of the group
-  int32_t rows;        // rows that exist
-  int32_t q0;          // token of row 0's request
-  int32_t ahead;       // position of the request's first new token
-  UnitTiles tiles;
-  int32_t t0, t1;
-};
-
-// Token and head of a unit's row.
-__device__ __forceinline__ void row_place(const AttendParams& p, const Piece& u, int r,
-                                          int64_t* token, int* head, int32_t* pos) {
-  const int32_t row = u.row0 + r;
-  const int32_t i = row / p.group;
-  *token = static_cast<int64_t>(u.q0) + i;
-  *head = u.head * p.group + (row - i * p.group);
-  *pos = u.ahead + i;
 }
 
 template <int D, int MT>
@@ -287,26 +224,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   pdl_trigger();
 
   // this CTA's range of the units
-  int4 cur, end;
   int64_t unit = 0, unit_end = 0;
+  int32_t first_tile = 0, last_tile = 0;
   if constexpr (kSel) {
     const int64_t units = selected_units(p);
     const int2 a = selected_cut(p, units, cta), b = selected_cut(p, units, cta + 1);
     unit = a.x;
     unit_end = b.x;
-    cur = make_int4(0, 0, a.y, 0);
-    end = make_int4(0, 0, b.y, 0);
-  } else {
-    cur = p.bound[cta];
-    end = p.bound[cta + 1];
+    first_tile = a.y;
+    last_tile = b.y;
   }
+  PieceWalk walk(kSel ? PieceWalk() : PieceWalk(p, cta));
 
   for (;;) {
     Piece u;
-    bool last;  // the range ends in (or before) this unit
     if constexpr (kSel) {
-      last = unit >= unit_end;
-      if (last && end.z <= cur.z) break;
+      const bool last = unit >= unit_end;
+      if (unit > unit_end || (last && last_tile <= first_tile)) break;
       const int blocks = (p.group + p.rows - 1) / p.rows;
       const int64_t tb = unit / p.num_kv_heads;
       const int32_t token = static_cast<int32_t>(tb / blocks);
@@ -317,25 +251,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       u.ahead = 0;
       u.req = token_request(p, token);
       u.tiles = UnitTiles{0, 0, selected_tiles(p), 0, 0};
-      u.t0 = cur.z;
-      u.t1 = last ? end.z : u.tiles.count;
+      u.t0 = first_tile;
+      u.t1 = last ? last_tile : u.tiles.count;
+      ++unit;
+      first_tile = 0;
     } else {
-      if (cur.w >= p.num_reqs) break;
-      last = cur.w == end.w && cur.y == end.y && cur.x == end.x;
-      if (last && end.z <= cur.z) break;
-      const ReqShape r = request_shape(p, cur.w, false);
-      const int64_t total = static_cast<int64_t>(r.nq) * p.group;
-      u.req = cur.w;
-      u.head = cur.y;
-      u.row0 = cur.x * p.rows;
-      u.rows = static_cast<int32_t>(min(static_cast<int64_t>(p.rows), total - u.row0));
-      u.q0 = r.q0;
-      u.ahead = r.keys - r.nq;
-      u.tiles = unit_tiles(p, r, cur.x);
-      u.t0 = cur.z;
-      u.t1 = last ? end.z : u.tiles.count;
+      if (!walk.next(p, &u)) break;
     }
-    const bool whole = u.t0 == 0 && u.t1 == u.tiles.count;
+    const bool whole = u.whole();
 
     if (!kSel || u.req >= 0) {
       const int32_t p_lo = u.tiles.p_lo, p_hi = u.tiles.p_hi;
@@ -679,22 +602,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       __syncthreads();
     }
 
-    if (last) break;
-    // ---- next unit
-    cur.z = 0;
-    if constexpr (kSel) {
-      ++unit;
-    } else {
-      const int32_t n = p.req_entry[cur.w + 1] - p.req_entry[cur.w];
-      if (++cur.x == n) {
-        cur.x = 0;
-        if (++cur.y == p.num_kv_heads) {
-          cur.y = 0;
-          do ++cur.w;
-          while (cur.w < p.num_reqs && p.req_entry[cur.w + 1] == p.req_entry[cur.w]);
-        }
-      }
-    }
   }
 }
 

@@ -10,7 +10,10 @@
 // one pass and any cut of them into pieces can be joined afterwards.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "internal.h"
 
@@ -50,6 +53,7 @@ struct AttendParams {
   int32_t grid;                    // CTAs of the row-block launch
   int32_t rows;                    // query rows of a unit
   int32_t tile;                    // keys of a tile
+  int32_t unit_overhead;           // tiles of streaming that a unit's start and end cost
   uint32_t* dev_error;
   uint64_t wait_ns;
 };
@@ -114,12 +118,119 @@ __device__ __forceinline__ UnitTiles unit_tiles(const AttendParams& p, const Req
   return t;
 }
 
-// Tiles of streaming that starting and ending a unit cost its CTA.
-constexpr int kUnitOverhead = 1;
+// A piece: tiles [t0, t1) of a unit.
+struct Piece {
+  int32_t req, head;  // request, kv head
+  int32_t row0;       // first row of the unit: (token - q0) * group + head of the group
+  int32_t rows;       // rows that exist
+  int32_t q0;         // first token of the request (selected form: the token)
+  int32_t ahead;      // position of the request's first new token
+  UnitTiles tiles;
+  int32_t t0, t1;
+
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles.count; }
+};
+
+// Token, head and position of a unit's row.
+__device__ __forceinline__ void row_place(const AttendParams& p, const Piece& u, int r,
+                                          int64_t* token, int* head, int32_t* pos) {
+  const int32_t row = u.row0 + r;
+  const int32_t i = row / p.group;
+  *token = static_cast<int64_t>(u.q0) + i;
+  *head = u.head * p.group + (row - i * p.group);
+  *pos = u.ahead + i;
+}
+
+// The pieces of a CTA's range in the paged form, in order.
+struct PieceWalk {
+  int4 cur, end;
+  bool done;
+
+  PieceWalk() = default;
+  __device__ __forceinline__ PieceWalk(const AttendParams& p, int cta)
+      : cur(p.bound[cta]), end(p.bound[cta + 1]), done(false) {}
+
+  __device__ __forceinline__ bool next(const AttendParams& p, Piece* u) {
+    if (done || cur.w >= p.num_reqs) return false;
+    const bool last = cur.w == end.w && cur.y == end.y && cur.x == end.x;
+    if (last && end.z <= cur.z) return false;
+    const ReqShape r = request_shape(p, cur.w, false);
+    const int64_t total = static_cast<int64_t>(r.nq) * p.group;
+    u->req = cur.w;
+    u->head = cur.y;
+    u->row0 = cur.x * p.rows;
+    u->rows = static_cast<int32_t>(min(static_cast<int64_t>(p.rows), total - u->row0));
+    u->q0 = r.q0;
+    u->ahead = r.keys - r.nq;
+    u->tiles = unit_tiles(p, r, cur.x);
+    u->t0 = cur.z;
+    u->t1 = last ? end.z : u->tiles.count;
+    done = last;
+    if (!last) {
+      cur.z = 0;
+      if (++cur.x == p.req_entry[cur.w + 1] - p.req_entry[cur.w]) {
+        cur.x = 0;
+        if (++cur.y == p.num_kv_heads) {
+          cur.y = 0;
+          do ++cur.w;
+          while (cur.w < p.num_reqs && p.req_entry[cur.w + 1] == p.req_entry[cur.w]);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// A pair of T values with its infinities and NaNs replaced by 0.
+template <typename T>
+__device__ __forceinline__ uint32_t clear_nonfinite(uint32_t v) {
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  if ((v & kExp) == kExp) v &= 0xffff0000u;
+  if ((v & (kExp << 16)) == kExp << 16) v &= 0xffffu;
+  return v;
+}
+
+// Two fp32 values as a pair of T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  } else {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes, asynchronously; `valid` false: zeros, and src is not read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr float kLn2 = 0.693147180559945309f;
+
+constexpr int kTileTc = 128;   // keys of a tensor-memory kernel's tile: two pages
+constexpr int kRowsTc = 256;   // its query rows: two accumulators of 128
 
 // Launchers.
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s);
 idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, int mt, cudaStream_t s);
+// (the caches' strides have to suit a tensor map: attend_tc_takes)
+bool attend_tc_takes(const AttendParams& p, int head_dim);
+idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 idx_status launch_attend_combine(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 
 }  // namespace saib

@@ -9,6 +9,7 @@ namespace saib {
 namespace {
 
 constexpr int kRowsCtasPerSm = 2;
+constexpr uint64_t kWaitNs = 2000000000ull;  // give-up time of a pipeline wait
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -41,19 +42,20 @@ AttendWs attend_ws(int64_t num_reqs, int64_t max_entries, int64_t grid, int64_t 
 
 // How a call is run: query rows per unit, keys per tile, CTAs.
 struct Variant {
-  int mt;  // row-block kernel: 16-row blocks per unit
-  int32_t rows, tile, grid;
+  int mt;  // row-block kernel: 16-row blocks per unit; 0: tensor-memory kernel
+  int32_t rows, tile, grid, overhead;
 };
 
 Variant rows_variant(int64_t rows_per_head) {
   const int mt = rows_per_head <= 16 ? 1 : 2;
-  return Variant{mt, 16 * mt, kPageTokens, kRowsCtasPerSm * device_sm_count()};
+  return Variant{mt, 16 * mt, kPageTokens, kRowsCtasPerSm * device_sm_count(), 1};
 }
+
+Variant tc_variant() { return Variant{0, kRowsTc, kTileTc, device_sm_count(), 2}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
   size_t most = 0;
-  for (const int64_t rows : {int64_t{1}, int64_t{17}}) {
-    const Variant v = rows_variant(rows);
+  for (const Variant& v : {rows_variant(1), rows_variant(17), tc_variant()}) {
     const size_t n = attend_ws(num_reqs, entry_bound(num_tokens, num_reqs, group, v.rows), v.grid,
                                v.rows, head_dim)
                          .total;
@@ -120,6 +122,7 @@ AttendParams attend_params(const idx_attend* a) {
   p.out = a->out;
   p.lse = a->lse;
   p.dev_error = a->dev_error;
+  p.wait_ns = kWaitNs;
   return p;
 }
 
@@ -127,6 +130,7 @@ idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& 
   p->rows = v.rows;
   p->tile = v.tile;
   p->grid = v.grid;
+  p->unit_overhead = v.overhead;
   p->max_entries =
       static_cast<int32_t>(entry_bound(a->num_tokens, a->num_reqs, p->group, v.rows));
   const AttendWs w = attend_ws(a->num_reqs, p->max_entries, v.grid, v.rows, a->head_dim);
@@ -172,12 +176,15 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
     p.sinks = a->sinks;
   }
   const int64_t longest = a->max_query_len > 0 ? a->max_query_len : a->num_tokens;
-  const Variant v = rows_variant(longest * p.group);
+  const bool tc = longest * p.group > 32 && attend_tc_takes(p, a->head_dim);
+  const Variant v = tc ? tc_variant() : rows_variant(longest * p.group);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
   if ((st = launch_attend_plan(p, s)) != IDX_OK) return st;
-  if ((st = launch_attend_rows(p, a->head_dim, half, v.mt, s)) != IDX_OK) return st;
+  st = tc ? launch_attend_tc(p, a->head_dim, half, s)
+          : launch_attend_rows(p, a->head_dim, half, v.mt, s);
+  if (st != IDX_OK) return st;
   return launch_attend_combine(p, a->head_dim, half, s);
 }
 

@@ -1,0 +1,668 @@
+// Attention of chunks of new tokens over a paged cache on the tcgen05 tensor
+// cores: blocks of 256 query rows of one kv head against tiles of 128 keys.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "attend.cuh"
+
+namespace saib {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSlotRows = 128;       // rows of one accumulator (a slot)
+// Registers per thread after the split: warps 0-3 and warps 4-11. 128 * 72 +
+// 256 * 216 = 384 * 168, what the block is launched with.
+constexpr int kRegsLaunch = 168, kRegsFeed = 72, kRegsSoftmax = 216;
+static_assert(128 * kRegsFeed + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+constexpr int kTmemCols = 512;
+constexpr int kColS = 0, kColO = 256;  // scores (and weights) of slot i at kColS + 128 i
+constexpr uint32_t kOddUnits = 8;
+// A row's running maximum is raised (and its accumulator rescaled) only when a
+// score exceeds it by this many units of log 2: the weights then stay below
+// 2^8, which both 16-bit types hold with the same relative precision.
+constexpr float kLazyRaise = 8.f;
+
+template <int D>
+struct TcCfg {
+  static constexpr int kSlotBytes = kSlotRows * D * 2;
+  static constexpr int kQ = 2 * kSlotBytes;
+  static constexpr int kStage = kTileTc * D * 2;
+  // Stages of K and of V. While tile j's V is in use, K of j + 1 and j + 2 and V of j + 1 and
+  // j + 2 are in flight (K of j is done by then).
+  static constexpr int kKStages = D == 128 ? 2 : 5;
+  static constexpr int kVStages = D == 128 ? 3 : 5;
+  static constexpr int kHalf = kTileTc * 128;  // 64 of the D values of 128 rows
+  static constexpr int kSmem = 1024 + kQ + (kKStages + kVStages) * kStage;
+  static constexpr int kV0 = kQ + kKStages * kStage;  // first V stage
+};
+
+struct TcBars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[5], k_empty[5];
+  uint64_t v_full[5], v_empty[5], v_ok[5];  // v_ok: edge tiles cleared (or none)
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t odd[kOddUnits];  // 1 + the last unit whose edge tiles held infinities or NaNs
+};
+
+// Instruction descriptor of kind::f16 with fp32 D: A K-major, B K-major or (kTransB) MN-major.
+template <typename T>
+__host__ __device__ constexpr uint32_t f16_idesc(int M, int N, bool trans_b) {
+  constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
+  return (1u << 4) | (kType << 7) | (kType << 10) | ((trans_b ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of an MN-major operand stored with the 128-byte
+// swizzle: 64 values of the MN dimension per 128-byte row, eight rows (K) per
+// 1024-byte atom, atoms of the next eight rows 1024 bytes on (SBO), the next 64
+// values kHalf bytes on (LBO).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                            int32_t y, int32_t z, int32_t w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A place in the ring of stages: fills go round it in order.
+template <int kStages>
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;  // parity of the current round
+
+  __device__ __forceinline__ void step() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Whether some row of the unit does not see some key of the tile.
+__device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles& t, int32_t tile) {
+  const int64_t s0 = static_cast<int64_t>(tile) * kTileTc;
+  return !(s0 + kTileTc - 1 <= t.p_lo &&
+           (s0 > static_cast<int64_t>(t.p_hi) - p.window || s0 + kTileTc <= p.sinks));
+}
+
+// One CTA per SM walks its range of units. Per unit and tile,
+//   S = Q K^T (two slots of 128 rows), P = exp2(S * scale - m), O += P V
+// with S, O in tensor memory and P written over S as the second product's A
+// operand, so that scores and weights never leave the SM:
+//   warp 0      TMA: the tile's two K and two V pages into a ring of stages
+//   warp 1      one thread issues the products: while one slot's softmax runs,
+//               the other slot's products keep the tensor pipe busy
+//   warps 2, 3  load a unit's queries; clear infinities and NaNs in the edge
+//               tiles' V (a weight of 0 would turn them into NaNs)
+//   warps 4-7, 8-11  softmax of slot 0, 1: a thread per row, running maximum
+//               raised lazily, row sums in fp32, accumulators written out
+// Tiles of 128 keys read K and V once per 256 rows; with fewer rows than 129 in
+// a unit slot 1 idles. Bound by the tensor pipe for long chunks: 512 cycles per
+// product and slot and tile at D = 128, the exponentials another 512.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tc_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  using C = TcCfg<D>;
+  constexpr int KS = C::kKStages, VS = C::kVStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TcBars bars;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t q_addr = base, k_addr = base + C::kQ, v_addr = base + C::kV0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* const abort_flag = &bars.abort_flag;
+
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    mbar_init(&bars.q_full, 64);
+    mbar_init(&bars.q_empty, 1);
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(&bars.k_full[i], 1);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], 1);
+      mbar_init(&bars.v_empty[i], 1);
+      mbar_init(&bars.v_ok[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], kSlotRows);
+      mbar_init(&bars.o_full[i], 1);
+    }
+    mbar_init(&bars.done, 1);
+    bars.abort_flag = 0;
+    for (uint32_t i = 0; i < kOddUnits; ++i) bars.odd[i] = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
+  if (warp == 1) tmem_alloc(&bars.tmem_base, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  pdl_wait();
+  pdl_trigger();
+  PieceWalk walk(p, blockIdx.x);
+  Piece u;
+
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity, abort_flag, p.dev_error, p.wait_ns);
+  };
+  // of a whole warp, which goes on together or not at all
+  const auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFeed));
+    if (warp == 0) {
+      if (lane == 0) {
+        // ---------------------------------------------------------------- TMA
+        Ring<KS> ka;
+        Ring<VS> va;
+        int64_t tiles = 0;  // K issued
+        int64_t v_tiles = 0;
+        bool ok = true;
+        while (ok && walk.next(p, &u)) {
+          const int32_t* bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
+          const auto pages_of = [&](int j) -> int2 {
+            if (j >= u.t1) return make_int2(-1, -1);
+            const int32_t c = u.tiles.tile(j) * 2;
+            // (the second page may lie past the request's last)
+            return make_int2(bt[c], (c + 1) * kPageTokens <= u.tiles.p_hi ? bt[c + 1] : -1);
+          };
+          int2 next = pages_of(u.t0);
+          for (int j = u.t0; ok && j < u.t1; ++j) {
+            const int2 pg = next;
+            next = pages_of(j + 1);
+            const bool a = pg.x >= 0 && pg.x < p.num_pages, b = pg.y >= 0 && pg.y < p.num_pages;
+            if (!a || (!b && (u.tiles.tile(j) * 2 + 1) * kPageTokens <= u.tiles.p_hi))
+              set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+            const uint32_t bytes = (static_cast<uint32_t>(a) + b) * kPageTokens * D * 2;
+            const auto fill = [&](uint32_t dst, const CUtensorMap* map, uint64_t* bar) {
+              if (bytes) mbar_arrive_expect_tx(bar, bytes);
+              else mbar_arrive(bar);
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h) {
+                if (a) tma_load_4d(dst + h * C::kHalf, map, h * 64, 0, u.head, pg.x, bar);
+                if (b)
+                  tma_load_4d(dst + h * C::kHalf + kPageTokens * 128, map, h * 64, 0, u.head, pg.y,
+                              bar);
+              }
+            };
+            if (tiles >= KS && !(ok = wait(&bars.k_empty[ka.stage], ka.phase ^ 1))) break;
+            fill(k_addr + ka.stage * C::kStage, &kmap, &bars.k_full[ka.stage]);
+            ++tiles;
+            ka.step();
+            if (v_tiles >= VS && !(ok = wait(&bars.v_empty[va.stage], va.phase ^ 1))) break;
+            fill(v_addr + va.stage * C::kStage, &vmap, &bars.v_full[va.stage]);
+            ++v_tiles;
+            va.step();
+          }
+        }
+        if (!ok) {
+          // gave up: the copies in flight land before the block leaves
+          int dummy = 0;
+          for (int64_t f = tiles < KS ? 0 : tiles - KS; f < tiles; ++f)
+            mbar_wait(&bars.k_full[f % KS], (f / KS) & 1, &dummy, p.dev_error, p.wait_ns);
+          for (int64_t f = v_tiles < VS ? 0 : v_tiles - VS; f < v_tiles; ++f)
+            mbar_wait(&bars.v_full[f % VS], (f / VS) & 1, &dummy, p.dev_error, p.wait_ns);
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        // ----------------------------------------------------------- products
+        constexpr uint32_t kDescQK = f16_idesc<T>(128, kTileTc, false);
+        constexpr uint32_t kDescPV = f16_idesc<T>(128, D, true);
+        Ring<KS> ka;
+        Ring<VS> va;
+        uint32_t q_phase = 0, p_phase[2] = {0, 0};
+        bool ok = true, issued = false;
+        const auto qk = [&](int slot, int stage) {
+          const uint32_t d = tmem + kColS + slot * 128;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
+            const uint32_t qoff = slot * C::kSlotBytes + (kk >> 2) * (kSlotRows * 128) + (kk & 3) * 32;
+            mma_f16_ss(d, sw128_kmajor_desc(q_addr + qoff),
+                       sw128_kmajor_desc(k_addr + stage * C::kStage + off), kDescQK, kk > 0);
+          }
+          mma_commit(&bars.s_full[slot]);
+        };
+        const auto pv = [&](int slot, int stage, bool first) {
+          const uint32_t d = tmem + kColO + slot * 128, a = tmem + kColS + slot * 128;
+#pragma unroll
+          for (int kk = 0; kk < kTileTc / 16; ++kk)
+            mma_f16_ts(d, a + kk * 8,
+                       sw128_mnmajor_desc(v_addr + stage * C::kStage + kk * 2048, C::kHalf), kDescPV,
+                       !first || kk > 0);
+        };
+        while (ok && walk.next(p, &u)) {
+          const int n = u.t1 - u.t0;
+          if (n <= 0) continue;
+          const bool two = u.rows > kSlotRows;
+          issued = true;
+          if (!(ok = wait(&bars.q_full, q_phase))) break;
+          q_phase ^= 1;
+          if (!(ok = wait(&bars.k_full[ka.stage], ka.phase))) break;
+          qk(0, ka.stage);
+          if (two) qk(1, ka.stage);
+          mma_commit(&bars.k_empty[ka.stage]);
+          if (n == 1) mma_commit(&bars.q_empty);
+          ka.step();
+          for (int j = 0; j < n; ++j) {
+            const int sv = va.stage;
+            if (!(ok = wait(&bars.v_ok[sv], va.phase))) break;
+            va.step();
+            int sk = 0;
+            for (int slot = 0; slot < (two ? 2 : 1); ++slot) {
+              if (!(ok = wait(&bars.p_full[slot], p_phase[slot]))) break;
+              p_phase[slot] ^= 1;
+              tc_fence_after();
+              pv(slot, sv, j == 0);
+              if (j + 1 < n) {
+                if (slot == 0) {
+                  sk = ka.stage;
+                  if (!(ok = wait(&bars.k_full[sk], ka.phase))) break;
+                  ka.step();
+                }
+                qk(slot, sk);
+              } else {
+                mma_commit(&bars.o_full[slot]);
+              }
+            }
+            if (!ok) break;
+            mma_commit(&bars.v_empty[sv]);
+            if (j + 1 < n) {
+              mma_commit(&bars.k_empty[sk]);
+              if (j + 2 == n) mma_commit(&bars.q_empty);
+            }
+          }
+        }
+        if (issued) {
+          // every product completes before tensor memory is released
+          mma_commit(&bars.done);
+          int dummy = 0;
+          mbar_wait(&bars.done, 0, &dummy, p.dev_error, p.wait_ns);
+        }
+      }
+    } else {
+      // ------------------------------------------- queries, V of edge tiles
+      const int tid = threadIdx.x - 64;
+      Ring<VS> va;
+      uint32_t unit = 0, q_phase = 0;
+      bool ok = true;
+      while (ok && walk.next(p, &u)) {
+        const int n = u.t1 - u.t0;
+        if (n <= 0) continue;
+        if (unit > 0) {
+          if (!(ok = wait_warp(&bars.q_empty, q_phase))) break;
+          q_phase ^= 1;
+        }
+        constexpr int kChunks = D / 8;
+        const int most = u.rows > kSlotRows ? kRowsTc : kSlotRows;
+        for (int i = tid; i < most * kChunks; i += 64) {
+          const int r = i / kChunks, c = i % kChunks;
+          int64_t token = 0;
+          int head = 0, pos;
+          const bool v = r < u.rows;
+          if (v) row_place(p, u, r, &token, &head, &pos);
+          const int slot = r / kSlotRows, rr = r % kSlotRows;
+          cp_async16(q_addr + slot * C::kSlotBytes + (c >> 3) * (kSlotRows * 128) + rr * 128 +
+                         (((c & 7) ^ (rr & 7)) << 4),
+                     static_cast<const T*>(p.q) + token * p.q_stride_token +
+                         head * p.q_stride_head + c * 8,
+                     v);
+        }
+        cp_commit();
+        cp_wait<0>();
+        fence_proxy_async_shared();
+        mbar_arrive(&bars.q_full);
+        for (int j = 0; j < n; ++j) {
+          const int32_t tile = u.tiles.tile(u.t0 + j);
+          const int stage = va.stage;
+          if (!(ok = wait_warp(&bars.v_full[stage], va.phase))) break;
+          va.step();
+          if (!edge_tile(p, u.tiles, tile)) {
+            if (lane == 0) mbar_arrive(&bars.v_ok[stage]);
+            continue;
+          }
+          uint4* v = reinterpret_cast<uint4*>(smem + C::kV0 + stage * C::kStage);
+          bool seen = false;
+          for (int i = tid; i < C::kStage / 16; i += 64) {
+            uint4 x = v[i];
+            const uint4 y = make_uint4(clear_nonfinite<T>(x.x), clear_nonfinite<T>(x.y),
+                                       clear_nonfinite<T>(x.z), clear_nonfinite<T>(x.w));
+            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
+              v[i] = y;
+              const int32_t key = tile * kTileTc + (i >> 3) % kTileTc;
+              seen |= key <= u.tiles.p_hi &&
+                      (key < p.sinks || static_cast<int64_t>(u.tiles.p_lo) - key < p.window);
+            }
+          }
+          if (seen) *reinterpret_cast<volatile uint32_t*>(&bars.odd[unit % kOddUnits]) = unit + 1;
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.v_ok[stage]);
+        }
+        ++unit;
+      }
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // -------------------------------------------------------------- softmax
+    const int slot = (warp - 4) >> 2;
+    const int r = slot * kSlotRows + (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_col = lanes + kColS + slot * 128, o_col = lanes + kColO + slot * 128;
+    const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+    uint32_t s_phase = 0, o_phase = 0, unit = 0;
+    bool ok = true;
+    while (ok && walk.next(p, &u)) {
+      const int n = u.t1 - u.t0;
+      const uint32_t this_unit = unit;
+      if (n > 0) ++unit;
+      if (slot == 1 && u.rows <= kSlotRows) continue;
+      int64_t token;
+      int head, pos;
+      row_place(p, u, r, &token, &head, &pos);
+      if (r >= u.rows) pos = INT32_MIN;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        const int32_t tile = u.tiles.tile(u.t0 + j);
+        if (!(ok = wait_warp(&bars.s_full[slot], s_phase))) break;
+        s_phase ^= 1;
+        tc_fence_after();
+        float s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
+        tmem_ld_wait();
+        if (edge_tile(p, u.tiles, tile)) {
+          const int32_t s0 = tile * kTileTc;
+          // key s0 + i is seen when i <= hi and (i > lo or i < first)
+          const int64_t hi = static_cast<int64_t>(pos) - s0, lo = hi - p.window;
+          const int32_t h32 = hi < 0 ? -1 : (hi > 127 ? 127 : static_cast<int32_t>(hi));
+          const int32_t l32 = lo < -1 ? -1 : (lo > 127 ? 127 : static_cast<int32_t>(lo));
+          const int32_t first = p.sinks - s0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int k = c * 32 + i;
+              if (!(k <= h32 && (k > l32 || k < first))) s[c][i] = -INFINITY;
+            }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = fmaxf(s[c][0], s[c][1]);
+#pragma unroll
+          for (int i = 2; i < 32; i += 2) mx[c] = fmaxf(mx[c], fmaxf(s[c][i], s[c][i + 1]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        float alpha = 1.f;
+        if (top > m + kLazyRaise) {
+          alpha = exp2_approx(m - top);
+          m = top;
+          l *= alpha;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(o_col + c * 32, o);
+            tmem_ld_wait();
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * alpha);
+            tmem_st32(o_col + c * 32, w);
+          }
+        }
+        const float sub = m == -INFINITY ? 0.f : -m;
+        const uint64_t sub2 = pack_f32x2(sub, sub);
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float(&v)[32] = s[2 * c + (i >> 4)];
+            const int e = (i & 15) * 2;
+            const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(v[e], v[e + 1]), scale2, sub2));
+            const float a = exp2_approx(x.x), b = exp2_approx(x.y);
+            sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(a, b));
+            // the weights are rounded to T for the second product (half a step of T
+            // each); their sum is of the unrounded ones
+            w[i] = pack2<T>(a, b);
+          }
+          tmem_st32(s_col + c * 32, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[slot]);
+        const float2 sum = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
+        l += sum.x + sum.y;
+      }
+      if (!ok) break;
+      // ------------------------------------------------------- accumulators
+      if (n > 0) {
+        if (!(ok = wait_warp(&bars.o_full[slot], o_phase))) break;
+        o_phase ^= 1;
+        tc_fence_after();
+      }
+      const bool odd =
+          n > 0 && *reinterpret_cast<volatile uint32_t*>(&bars.odd[this_unit % kOddUnits]) ==
+                       this_unit + 1;
+      const bool whole = u.whole();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t at = token * p.num_heads + head;
+      const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (u.t0 == 0 ? 1 : 0)) * p.rows + r;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld32(o_col + c * 32, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (odd && r < u.rows) {
+          // the infinities and NaNs left out of the edge tiles' products, for the rows that see them
+          const int32_t* bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
+#pragma unroll 1
+          for (int j = u.t0; j < u.t1; ++j) {
+            const int32_t tile = u.tiles.tile(j);
+            if (!edge_tile(p, u.tiles, tile)) continue;
+#pragma unroll 1
+            for (int i = 0; i < kTileTc; ++i) {
+              const int32_t key = tile * kTileTc + i;
+              if (key > pos || (key >= p.sinks && pos - key >= p.window)) continue;
+              const int32_t page = bt[key / kPageTokens];
+              if (page < 0 || page >= p.num_pages) continue;
+              const T* v = static_cast<const T*>(p.v) + page * p.v_stride_page +
+                           (key % kPageTokens) * p.v_stride_token + u.head * p.v_stride_head +
+                           c * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = static_cast<float>(v[e]);
+                if (!isfinite(x)) o[e] += x;
+              }
+            }
+          }
+        }
+        if (r < u.rows) {
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                  pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                  pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                  pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        __syncwarp();  // the odd path's loops diverge; tensor-memory loads are warp-wide
+      }
+      if (r < u.rows) {
+        if (!whole) p.part_ml[part] = make_float2(m, l);
+        else if (p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Map of a cache: [64 tokens of a page][64 of the head_dim values] boxes of one
+// head and page.
+bool encode_map(CUtensorMap* map, const void* base, bool half, int head_dim, int64_t tok,
+                int64_t head, int64_t page, int64_t heads, int64_t pages) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!encode) return false;
+  // (the stride of a dimension of one entry is never used; it only has to be valid)
+  if (heads == 1) head = tok;
+  if (pages == 1) page = tok;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), kPageTokens,
+                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(2 * tok), static_cast<cuuint64_t>(2 * head),
+                                 static_cast<cuuint64_t>(2 * page)};
+  const cuuint32_t box[4] = {64, kPageTokens, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode(map,
+                half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+idx_status launch_tc_as(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        cudaStream_t s) {
+  using C = TcCfg<D>;
+  const auto kernel = attend_tc_kernel<T, D>;
+  static std::atomic<bool> configured[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0) return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidDevice);
+  if (dev >= kMaxDevices || !configured[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes a;
+    if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return cuda_status(e);
+    // the register split hands out what the launch holds, no more
+    if (a.numRegs != kRegsLaunch) return cuda_status(cudaErrorInvalidConfiguration);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (dev < kMaxDevices) configured[dev].store(true, std::memory_order_release);
+  }
+  return cuda_status(launch_pdl(kernel, p.grid, kThreads, C::kSmem, s, p, kmap, vmap));
+}
+
+bool map_stride_ok(int64_t stride, int64_t entries) {
+  return entries == 1 || (stride > 0 && stride < (int64_t{1} << 38));
+}
+
+}  // namespace
+
+bool attend_tc_takes(const AttendParams& p, int) {
+  return map_stride_ok(p.k_stride_token, 2) && map_stride_ok(p.v_stride_token, 2) &&
+         map_stride_ok(p.k_stride_head, p.num_kv_heads) &&
+         map_stride_ok(p.v_stride_head, p.num_kv_heads) &&
+         map_stride_ok(p.k_stride_page, p.num_pages) && map_stride_ok(p.v_stride_page, p.num_pages);
+}
+
+idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, cudaStream_t s) {
+  CUtensorMap kmap, vmap;
+  if (!encode_map(&kmap, p.k, half, head_dim, p.k_stride_token, p.k_stride_head, p.k_stride_page,
+                  p.num_kv_heads, p.num_pages) ||
+      !encode_map(&vmap, p.v, half, head_dim, p.v_stride_token, p.v_stride_head, p.v_stride_page,
+                  p.num_kv_heads, p.num_pages))
+    return IDX_ERR_CUDA;
+  if (half)
+    return head_dim == 64 ? launch_tc_as<__half, 64>(p, kmap, vmap, s)
+                          : launch_tc_as<__half, 128>(p, kmap, vmap, s);
+  return head_dim == 64 ? launch_tc_as<__nv_bfloat16, 64>(p, kmap, vmap, s)
+                        : launch_tc_as<__nv_bfloat16, 128>(p, kmap, vmap, s);
+}
+
+}  // namespace saib
