@@ -144,36 +144,43 @@ __device__ __forceinline__ void row_place(const AttendParams& p, const Piece& u,
 // The pieces of a CTA's range in the paged form, in order.
 struct PieceWalk {
   int4 cur, end;
-  bool done;
+  ReqShape shape;   // of request cur.w
+  int32_t entries;  // its entries
+  bool done, stale;
 
   PieceWalk() = default;
   __device__ __forceinline__ PieceWalk(const AttendParams& p, int cta)
-      : cur(p.bound[cta]), end(p.bound[cta + 1]), done(false) {}
+      : cur(p.bound[cta]), end(p.bound[cta + 1]), done(false), stale(true) {}
 
   __device__ __forceinline__ bool next(const AttendParams& p, Piece* u) {
     if (done || cur.w >= p.num_reqs) return false;
     const bool last = cur.w == end.w && cur.y == end.y && cur.x == end.x;
     if (last && end.z <= cur.z) return false;
-    const ReqShape r = request_shape(p, cur.w, false);
-    const int64_t total = static_cast<int64_t>(r.nq) * p.group;
+    if (stale) {
+      shape = request_shape(p, cur.w, false);
+      entries = p.req_entry[cur.w + 1] - p.req_entry[cur.w];
+      stale = false;
+    }
+    const int64_t total = static_cast<int64_t>(shape.nq) * p.group;
     u->req = cur.w;
     u->head = cur.y;
     u->row0 = cur.x * p.rows;
     u->rows = static_cast<int32_t>(min(static_cast<int64_t>(p.rows), total - u->row0));
-    u->q0 = r.q0;
-    u->ahead = r.keys - r.nq;
-    u->tiles = unit_tiles(p, r, cur.x);
+    u->q0 = shape.q0;
+    u->ahead = shape.keys - shape.nq;
+    u->tiles = unit_tiles(p, shape, cur.x);
     u->t0 = cur.z;
     u->t1 = last ? end.z : u->tiles.count;
     done = last;
     if (!last) {
       cur.z = 0;
-      if (++cur.x == p.req_entry[cur.w + 1] - p.req_entry[cur.w]) {
+      if (++cur.x == entries) {
         cur.x = 0;
         if (++cur.y == p.num_kv_heads) {
           cur.y = 0;
           do ++cur.w;
           while (cur.w < p.num_reqs && p.req_entry[cur.w + 1] == p.req_entry[cur.w]);
+          stale = true;
         }
       }
     }

@@ -123,6 +123,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t v;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(v));
+  return v != 0;
+}
+
 // A place in the ring of stages: fills go round it in order.
 template <int kStages>
 struct Ring {
@@ -136,6 +145,24 @@ struct Ring {
     }
   }
 };
+
+// Lane 4a + i's chunk j goes to lane 4a + j's chunk i.
+__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
+  const auto swap = [&](uint4& a, uint4& b, int mask) {
+    // the lower lane of a pair keeps a and gets the other's a as b, the upper the reverse
+    const bool up = lane & mask;
+    const uint4 give = up ? a : b;
+    const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, mask),
+                                 __shfl_xor_sync(0xffffffffu, give.y, mask),
+                                 __shfl_xor_sync(0xffffffffu, give.z, mask),
+                                 __shfl_xor_sync(0xffffffffu, give.w, mask));
+    if (up) a = got; else b = got;
+  };
+  swap(w[0], w[1], 1);
+  swap(w[2], w[3], 1);
+  swap(w[0], w[2], 2);
+  swap(w[1], w[3], 2);
+}
 
 // Whether some row of the unit does not see some key of the tile.
 __device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles& t, int32_t tile) {
@@ -169,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t q_addr = base, k_addr = base + C::kQ, v_addr = base + C::kV0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* const abort_flag = &bars.abort_flag;
 
   if (threadIdx.x == 0) {
@@ -199,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
   pdl_wait();
   pdl_trigger();
   PieceWalk walk(p, blockIdx.x);
@@ -270,81 +297,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 1) {
-      if (lane == 0) {
-        // ----------------------------------------------------------- products
-        constexpr uint32_t kDescQK = f16_idesc<T>(128, kTileTc, false);
-        constexpr uint32_t kDescPV = f16_idesc<T>(128, D, true);
-        Ring<KS> ka;
-        Ring<VS> va;
-        uint32_t q_phase = 0, p_phase[2] = {0, 0};
-        bool ok = true, issued = false;
-        const auto qk = [&](int slot, int stage) {
-          const uint32_t d = tmem + kColS + slot * 128;
+      // ------------------------------------------------------------- products
+      // The whole warp walks; one elected lane issues. (Descriptors from warp-uniform values
+      // with constant steps: computed by a single diverged thread, they cost 140 cycles a
+      // product to issue, against 64 to execute.)
+      constexpr uint32_t kDescQK = f16_idesc<T>(128, kTileTc, false);
+      constexpr uint32_t kDescPV = f16_idesc<T>(128, D, true);
+      const uint64_t q_desc = sw128_kmajor_desc(q_addr), k_desc = sw128_kmajor_desc(k_addr);
+      const uint64_t v_desc = sw128_mnmajor_desc(v_addr, C::kHalf);
+      Ring<KS> ka;
+      Ring<VS> va;
+      uint32_t q_phase = 0, p_phase = 0;  // (bit i: slot i)
+      bool ok = true, issued = false;
+      const auto qk = [&](int slot, int stage) {
+        const uint32_t d = tmem + kColS + slot * 128;
+        const uint64_t a = q_desc + slot * (C::kSlotBytes >> 4);
+        const uint64_t b = k_desc + stage * (C::kStage >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-            const uint32_t qoff = slot * C::kSlotBytes + (kk >> 2) * (kSlotRows * 128) + (kk & 3) * 32;
-            mma_f16_ss(d, sw128_kmajor_desc(q_addr + qoff),
-                       sw128_kmajor_desc(k_addr + stage * C::kStage + off), kDescQK, kk > 0);
-          }
-          mma_commit(&bars.s_full[slot]);
-        };
-        const auto pv = [&](int slot, int stage, bool first) {
-          const uint32_t d = tmem + kColO + slot * 128, a = tmem + kColS + slot * 128;
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(d, a + (((kk >> 2) * (kSlotRows * 128) + (kk & 3) * 32) >> 4),
+                     b + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), kDescQK, kk > 0);
+        mma_commit(&bars.s_full[slot]);
+      };
+      const auto pv = [&](int slot, int stage, bool first) {
+        const uint32_t d = tmem + kColO + slot * 128, a = tmem + kColS + slot * 128;
+        const uint64_t b = v_desc + stage * (C::kStage >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kTileTc / 16; ++kk)
-            mma_f16_ts(d, a + kk * 8,
-                       sw128_mnmajor_desc(v_addr + stage * C::kStage + kk * 2048, C::kHalf), kDescPV,
-                       !first || kk > 0);
-        };
-        while (ok && walk.next(p, &u)) {
-          const int n = u.t1 - u.t0;
-          if (n <= 0) continue;
-          const bool two = u.rows > kSlotRows;
-          issued = true;
-          if (!(ok = wait(&bars.q_full, q_phase))) break;
-          q_phase ^= 1;
-          if (!(ok = wait(&bars.k_full[ka.stage], ka.phase))) break;
+        for (int kk = 0; kk < kTileTc / 16; ++kk)
+          mma_f16_ts(d, a + kk * 8, b + (kk * 2048 >> 4), kDescPV, !first || kk > 0);
+      };
+      while (ok && walk.next(p, &u)) {
+        const int n = u.t1 - u.t0;
+        if (n <= 0) continue;
+        const bool two = u.rows > kSlotRows;
+        issued = true;
+        if (!(ok = wait_warp(&bars.q_full, q_phase))) break;
+        q_phase ^= 1;
+        if (!(ok = wait_warp(&bars.k_full[ka.stage], ka.phase))) break;
+        if (elect_one()) {
           qk(0, ka.stage);
           if (two) qk(1, ka.stage);
           mma_commit(&bars.k_empty[ka.stage]);
           if (n == 1) mma_commit(&bars.q_empty);
-          ka.step();
-          for (int j = 0; j < n; ++j) {
-            const int sv = va.stage;
-            if (!(ok = wait(&bars.v_ok[sv], va.phase))) break;
-            va.step();
-            int sk = 0;
-            for (int slot = 0; slot < (two ? 2 : 1); ++slot) {
-              if (!(ok = wait(&bars.p_full[slot], p_phase[slot]))) break;
-              p_phase[slot] ^= 1;
-              tc_fence_after();
-              pv(slot, sv, j == 0);
-              if (j + 1 < n) {
-                if (slot == 0) {
-                  sk = ka.stage;
-                  if (!(ok = wait(&bars.k_full[sk], ka.phase))) break;
-                  ka.step();
-                }
-                qk(slot, sk);
-              } else {
-                mma_commit(&bars.o_full[slot]);
+        }
+        __syncwarp();
+        ka.step();
+        for (int j = 0; j < n; ++j) {
+          const int sv = va.stage, sk = ka.stage;
+          const bool more = j + 1 < n;
+          if (!(ok = wait_warp(&bars.v_ok[sv], va.phase))) break;
+          va.step();
+          if (!(ok = wait_warp(&bars.p_full[0], p_phase & 1))) break;
+          p_phase ^= 1;
+          tc_fence_after();
+          if (elect_one()) {
+            pv(0, sv, j == 0);
+            if (!more) {
+              mma_commit(&bars.o_full[0]);
+              if (!two) mma_commit(&bars.v_empty[sv]);
+            }
+          }
+          __syncwarp();
+          if (more) {
+            if (!(ok = wait_warp(&bars.k_full[sk], ka.phase))) break;
+            ka.step();
+            if (elect_one()) {
+              qk(0, sk);
+              if (!two) {
+                mma_commit(&bars.v_empty[sv]);
+                mma_commit(&bars.k_empty[sk]);
+                if (j + 2 == n) mma_commit(&bars.q_empty);
               }
             }
-            if (!ok) break;
+            __syncwarp();
+          }
+          if (!two) continue;
+          if (!(ok = wait_warp(&bars.p_full[1], p_phase >> 1))) break;
+          p_phase ^= 2;
+          tc_fence_after();
+          if (elect_one()) {
+            pv(1, sv, j == 0);
+            if (!more) mma_commit(&bars.o_full[1]);
             mma_commit(&bars.v_empty[sv]);
-            if (j + 1 < n) {
+            if (more) {
+              qk(1, sk);
               mma_commit(&bars.k_empty[sk]);
               if (j + 2 == n) mma_commit(&bars.q_empty);
             }
           }
+          __syncwarp();
         }
-        if (issued) {
-          // every product completes before tensor memory is released
+      }
+      if (issued) {
+        // every product completes before tensor memory is released
+        if (elect_one()) {
           mma_commit(&bars.done);
           int dummy = 0;
           mbar_wait(&bars.done, 0, &dummy, p.dev_error, p.wait_ns);
         }
+        __syncwarp();
       }
     } else {
       // ------------------------------------------- queries, V of edge tiles
@@ -359,20 +410,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_warp(&bars.q_empty, q_phase))) break;
           q_phase ^= 1;
         }
-        constexpr int kChunks = D / 8;
+        // a lane places a row; D / 8 lanes copy it
+        constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
         const int most = u.rows > kSlotRows ? kRowsTc : kSlotRows;
-        for (int i = tid; i < most * kChunks; i += 64) {
-          const int r = i / kChunks, c = i % kChunks;
+        const int c = lane % kChunks;
+        for (int r0 = (warp - 2) * 32; r0 < most; r0 += 64) {
           int64_t token = 0;
           int head = 0, pos;
-          const bool v = r < u.rows;
-          if (v) row_place(p, u, r, &token, &head, &pos);
-          const int slot = r / kSlotRows, rr = r % kSlotRows;
-          cp_async16(q_addr + slot * C::kSlotBytes + (c >> 3) * (kSlotRows * 128) + rr * 128 +
-                         (((c & 7) ^ (rr & 7)) << 4),
-                     static_cast<const T*>(p.q) + token * p.q_stride_token +
-                         head * p.q_stride_head + c * 8,
-                     v);
+          const int row = r0 + lane;
+          if (row < u.rows) row_place(p, u, row, &token, &head, &pos);
+          const int64_t from = token * p.q_stride_token + head * p.q_stride_head;
+          const uint32_t to = q_addr + (r0 / kSlotRows) * C::kSlotBytes;
+#pragma unroll 8
+          for (int i = 0; i < 32; i += kRowsAtOnce) {
+            const int k = i + lane / kChunks, rr = r0 % kSlotRows + k;
+            const int64_t at = __shfl_sync(0xffffffffu, from, k);
+            cp_async16(to + (c >> 3) * (kSlotRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
+                       static_cast<const T*>(p.q) + at + c * 8, r0 + k < u.rows);
+          }
         }
         cp_commit();
         cp_wait<0>();
@@ -552,21 +607,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (r < u.rows) {
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * D + c * 32);
+        if (whole) {
+          // four lanes exchange 16-byte chunks, so that together they write 64 bytes of one row
+          uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                  pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                  pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+          for (int i = 0; i < 4; ++i)
+            w[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                              pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                              pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                              pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          __syncwarp();
+          transpose4(w, lane);
+          uint4* const out = reinterpret_cast<uint4*>(p.out);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 4; ++i) {
+            const int from = (lane & ~3) + i;
+            const int64_t row = __shfl_sync(0xffffffffu, at, from);
+            if (r - lane + from < u.rows) out[row * (D / 8) + c * 4 + (lane & 3)] = w[i];
           }
+        } else if (r < u.rows) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
         __syncwarp();  // the odd path's loops diverge; tensor-memory loads are warp-wide
       }
