@@ -651,8 +651,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(cons
     u.q0 = q.q0;
     u.head = next.y;
     u.row0 = next.x * p.rows;
-    u.rows = static_cast<int32_t>(
-        min(static_cast<int64_t>(p.rows), static_cast<int64_t>(q.nq) * p.group - u.row0));
+    u.rows = min(p.rows, q.nq * p.group - u.row0);
     u.ahead = 0;
   }
   if (r >= u.rows) return;

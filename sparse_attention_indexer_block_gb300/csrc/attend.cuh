@@ -39,8 +39,9 @@ struct AttendParams {
   int32_t num_reqs, num_tokens;
   int32_t num_heads, num_kv_heads, group;
   float scale_log2;                // scale * log2(e)
-  int32_t window;                  // INT32_MAX: no window
+  int32_t window;                  // (2^30: none)
   int32_t sinks;
+  int32_t sinks_tiles;             // tiles that hold them
   void* out;                       // [num_tokens, num_heads, head_dim]
   float* lse;                      // nullable [num_tokens, num_heads]
   // workspace
@@ -52,7 +53,7 @@ struct AttendParams {
   int32_t max_entries;
   int32_t grid;                    // CTAs of the row-block launch
   int32_t rows;                    // query rows of a unit
-  int32_t tile;                    // keys of a tile
+  int32_t tile_log2;               // keys of a tile
   int32_t unit_overhead;           // tiles of streaming that a unit's start and end cost
   uint32_t* dev_error;
   uint64_t wait_ns;
@@ -92,28 +93,26 @@ __device__ __forceinline__ ReqShape request_shape(const AttendParams& p, int32_t
 }
 
 __device__ __forceinline__ int32_t request_entries(const AttendParams& p, const ReqShape& r) {
-  return static_cast<int32_t>((static_cast<int64_t>(r.nq) * p.group + p.rows - 1) / p.rows);
+  return (r.nq * p.group + p.rows - 1) / p.rows;
 }
 
+// (All in 32 bits: num_tokens * num_heads and the table's tokens fit with room for a tile.)
 __device__ __forceinline__ UnitTiles unit_tiles(const AttendParams& p, const ReqShape& r, int32_t u) {
   UnitTiles t;
-  const int64_t row0 = static_cast<int64_t>(u) * p.rows;
-  const int64_t total = static_cast<int64_t>(r.nq) * p.group;
-  const int64_t row1 = row0 + p.rows < total ? row0 + p.rows : total;
+  const int32_t row0 = u * p.rows;
+  const int32_t row1 = min(row0 + p.rows, r.nq * p.group);
   const int32_t ahead = r.keys - r.nq;
-  t.p_lo = ahead + static_cast<int32_t>(row0 / p.group);
-  t.p_hi = ahead + static_cast<int32_t>((row1 - 1) / p.group);
+  t.p_lo = ahead + row0 / p.group;
+  t.p_hi = ahead + (row1 - 1) / p.group;
   if (t.p_hi < 0) {
     t.first = t.skip = t.count = 0;
     return t;
   }
-  const int32_t end = t.p_hi / p.tile + 1;
-  const int64_t lo = static_cast<int64_t>(t.p_lo) - p.window + 1;
-  const int32_t start = lo > 0 ? static_cast<int32_t>(lo) / p.tile : 0;
-  int32_t first = (p.sinks + p.tile - 1) / p.tile;
-  first = first < start ? first : start;
-  t.first = first;
-  t.skip = start - first;
+  const int32_t end = (t.p_hi >> p.tile_log2) + 1;
+  const int32_t lo = max(t.p_lo, 0) - p.window + 1;
+  const int32_t start = max(lo, 0) >> p.tile_log2;
+  t.first = min(p.sinks_tiles, start);
+  t.skip = start - t.first;
   t.count = end - t.skip;
   return t;
 }
@@ -161,11 +160,10 @@ struct PieceWalk {
       entries = p.req_entry[cur.w + 1] - p.req_entry[cur.w];
       stale = false;
     }
-    const int64_t total = static_cast<int64_t>(shape.nq) * p.group;
     u->req = cur.w;
     u->head = cur.y;
     u->row0 = cur.x * p.rows;
-    u->rows = static_cast<int32_t>(min(static_cast<int64_t>(p.rows), total - u->row0));
+    u->rows = min(p.rows, shape.nq * p.group - u->row0);
     u->q0 = shape.q0;
     u->ahead = shape.keys - shape.nq;
     u->tiles = unit_tiles(p, shape, cur.x);

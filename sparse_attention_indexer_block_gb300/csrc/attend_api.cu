@@ -2,6 +2,8 @@
 // kernel, the workspace and the launches.
 #include <math.h>
 
+#include <algorithm>
+
 #include "attend.cuh"
 
 namespace saib {
@@ -9,6 +11,10 @@ namespace saib {
 namespace {
 
 constexpr int kRowsCtasPerSm = 2;
+// Keys of a request; a window that wide hides nothing. Positions less windows less keys fit in
+// 32 bits.
+constexpr int32_t kMostKeys = 1 << 30;
+constexpr int64_t kMostRows = INT32_MAX - 1024;  // num_tokens * num_heads
 constexpr uint64_t kWaitNs = 2000000000ull;  // give-up time of a pipeline wait
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -43,15 +49,15 @@ AttendWs attend_ws(int64_t num_reqs, int64_t max_entries, int64_t grid, int64_t 
 // How a call is run: query rows per unit, keys per tile, CTAs.
 struct Variant {
   int mt;  // row-block kernel: 16-row blocks per unit; 0: tensor-memory kernel
-  int32_t rows, tile, grid, overhead;
+  int32_t rows, tile_log2, grid, overhead;
 };
 
 Variant rows_variant(int64_t rows_per_head) {
   const int mt = rows_per_head <= 16 ? 1 : 2;
-  return Variant{mt, 16 * mt, kPageTokens, kRowsCtasPerSm * device_sm_count(), 1};
+  return Variant{mt, 16 * mt, 6, kRowsCtasPerSm * device_sm_count(), 1};
 }
 
-Variant tc_variant() { return Variant{0, kRowsTc, kTileTc, device_sm_count(), 2}; }
+Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 2}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
   size_t most = 0;
@@ -74,10 +80,10 @@ idx_status check_attend(const idx_attend* a) {
   if (a->num_tokens < 0 || a->num_reqs < 0 || a->num_heads < 1 || a->num_kv_heads < 1)
     return IDX_ERR_INVALID_ARG;
   if (a->num_heads % a->num_kv_heads != 0) return IDX_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(a->num_tokens) * a->num_heads > INT32_MAX) return IDX_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(a->num_tokens) * a->num_heads > kMostRows) return IDX_ERR_UNSUPPORTED;
   if (!(a->scale > 0.f) || !isfinite(a->scale)) return IDX_ERR_INVALID_ARG;
   if (a->num_pages < 1 || a->num_pages > INT32_MAX || a->bt_width < 1 ||
-      a->bt_width > INT32_MAX / kPageTokens || a->bt_stride < a->bt_width)
+      a->bt_width > kMostKeys / kPageTokens || a->bt_stride < a->bt_width)
     return IDX_ERR_INVALID_ARG;
   if (a->num_tokens == 0 || a->num_reqs == 0) return IDX_OK;
   if (!a->q || !a->k || !a->v || !a->out || !a->block_table || !a->query_start_loc)
@@ -118,7 +124,7 @@ AttendParams attend_params(const idx_attend* a) {
   p.num_kv_heads = a->num_kv_heads;
   p.group = a->num_heads / a->num_kv_heads;
   p.scale_log2 = a->scale * 1.4426950408889634f;
-  p.window = INT32_MAX;
+  p.window = kMostKeys;
   p.out = a->out;
   p.lse = a->lse;
   p.dev_error = a->dev_error;
@@ -128,7 +134,9 @@ AttendParams attend_params(const idx_attend* a) {
 
 idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& v) {
   p->rows = v.rows;
-  p->tile = v.tile;
+  p->tile_log2 = v.tile_log2;
+  p->sinks_tiles = static_cast<int32_t>((static_cast<int64_t>(p->sinks) + (1 << v.tile_log2) - 1) >>
+                                        v.tile_log2);
   p->grid = v.grid;
   p->unit_overhead = v.overhead;
   p->max_entries =
@@ -157,7 +165,7 @@ idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, 
       num_heads % num_kv_heads != 0)
     return IDX_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) ||
-      static_cast<int64_t>(num_tokens) * num_heads > INT32_MAX)
+      static_cast<int64_t>(num_tokens) * num_heads > kMostRows)
     return IDX_ERR_UNSUPPORTED;
   *bytes = most_workspace(num_tokens, num_reqs, num_heads / num_kv_heads, head_dim);
   return IDX_OK;
@@ -172,7 +180,7 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
   AttendParams p = attend_params(a);
   p.seq_lens = a->seq_lens;
   if (a->window > 0) {
-    p.window = a->window;
+    p.window = std::min(a->window, kMostKeys);
     p.sinks = a->sinks;
   }
   const int64_t longest = a->max_query_len > 0 ? a->max_query_len : a->num_tokens;

@@ -166,9 +166,47 @@ __device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
 
 // Whether some row of the unit does not see some key of the tile.
 __device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles& t, int32_t tile) {
-  const int64_t s0 = static_cast<int64_t>(tile) * kTileTc;
-  return !(s0 + kTileTc - 1 <= t.p_lo &&
-           (s0 > static_cast<int64_t>(t.p_hi) - p.window || s0 + kTileTc <= p.sinks));
+  const int32_t s0 = tile * kTileTc;
+  return !(s0 + kTileTc - 1 <= t.p_lo && (s0 > t.p_hi - p.window || s0 + kTileTc <= p.sinks));
+}
+
+// The n lowest bits of a word, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t low_bits(int32_t n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// Bits of v whose 16-bit halves are infinities or NaNs (their top bits, else 0).
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t v) {
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr uint32_t kExp = kHalf ? 0x7c007c00u : 0x7f807f80u;
+  return ((v & kExp) + (kHalf ? 0x04000400u : 0x00800080u)) & 0x80008000u;
+}
+
+// The infinities and NaNs that were left out of the edge tiles' products, for
+// a row that sees them: added to the row where it was written.
+template <typename T, int D>
+__device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u, int32_t pos,
+                                           T* out, float* part) {
+  const int32_t* bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
+  for (int j = u.t0; j < u.t1; ++j) {
+    const int32_t tile = u.tiles.tile(j);
+    if (!edge_tile(p, u.tiles, tile)) continue;
+    for (int i = 0; i < kTileTc; ++i) {
+      const int32_t key = tile * kTileTc + i;
+      if (key > pos || (key >= p.sinks && pos - key >= p.window)) continue;
+      const int32_t page = bt[key / kPageTokens];
+      if (page < 0 || page >= p.num_pages) continue;
+      const T* v = static_cast<const T*>(p.v) + page * p.v_stride_page +
+                   (key % kPageTokens) * p.v_stride_token + u.head * p.v_stride_head;
+      for (int e = 0; e < D; ++e) {
+        const float x = static_cast<float>(v[e]);
+        if (isfinite(x)) continue;
+        if (out) out[e] = static_cast<T>(static_cast<float>(out[e]) + x);
+        else part[e] += x;
+      }
+    }
+  }
 }
 
 // One CTA per SM walks its range of units. Per unit and tile,
@@ -187,7 +225,7 @@ __device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles
 // product and slot and tile at D = 128, the exponentials another 512.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_tc_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
+    attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   using C = TcCfg<D>;
   constexpr int KS = C::kKStages, VS = C::kVStages;
@@ -444,15 +482,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint4* v = reinterpret_cast<uint4*>(smem + C::kV0 + stage * C::kStage);
           bool seen = false;
-          for (int i = tid; i < C::kStage / 16; i += 64) {
-            uint4 x = v[i];
-            const uint4 y = make_uint4(clear_nonfinite<T>(x.x), clear_nonfinite<T>(x.y),
-                                       clear_nonfinite<T>(x.z), clear_nonfinite<T>(x.w));
-            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
-              v[i] = y;
-              const int32_t key = tile * kTileTc + (i >> 3) % kTileTc;
-              seen |= key <= u.tiles.p_hi &&
-                      (key < p.sinks || static_cast<int64_t>(u.tiles.p_lo) - key < p.window);
+          constexpr int kAtOnce = 8;
+          static_assert(C::kStage / 16 % (64 * kAtOnce) == 0, "whole rounds");
+#pragma unroll 1
+          for (int i0 = tid; i0 < C::kStage / 16; i0 += 64 * kAtOnce) {
+            uint32_t hit = 0;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+              const uint4 x = v[i0 + e * 64];
+              hit |= nonfinite_bits<T>(x.x) | nonfinite_bits<T>(x.y) | nonfinite_bits<T>(x.z) |
+                     nonfinite_bits<T>(x.w);
+            }
+            if (!hit) continue;
+#pragma unroll 1
+            for (int i = i0; i < i0 + 64 * kAtOnce; i += 64) {
+              const uint4 x = v[i];
+              const uint4 y = make_uint4(clear_nonfinite<T>(x.x), clear_nonfinite<T>(x.y),
+                                         clear_nonfinite<T>(x.z), clear_nonfinite<T>(x.w));
+              if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
+                v[i] = y;
+                const int32_t key = tile * kTileTc + (i >> 3) % kTileTc;
+                seen |= key <= u.tiles.p_hi && (key < p.sinks || max(u.tiles.p_lo, 0) - key < p.window);
+              }
             }
           }
           if (seen) *reinterpret_cast<volatile uint32_t*>(&bars.odd[unit % kOddUnits]) = unit + 1;
@@ -494,19 +545,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
         tmem_ld_wait();
         if (edge_tile(p, u.tiles, tile)) {
+          // bit i of a word: key s0 + i is seen (i <= hi and (i > lo or i < first))
           const int32_t s0 = tile * kTileTc;
-          // key s0 + i is seen when i <= hi and (i > lo or i < first)
-          const int64_t hi = static_cast<int64_t>(pos) - s0, lo = hi - p.window;
-          const int32_t h32 = hi < 0 ? -1 : (hi > 127 ? 127 : static_cast<int32_t>(hi));
-          const int32_t l32 = lo < -1 ? -1 : (lo > 127 ? 127 : static_cast<int32_t>(lo));
+          const int32_t hi = max(pos, -1) - s0, lo = max(pos, -1) - p.window - s0;
           const int32_t first = p.sinks - s0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = low_bits(hi + 1 - 32 * c) &
+                                 (~low_bits(lo + 1 - 32 * c) | low_bits(first - 32 * c));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int k = c * 32 + i;
-              if (!(k <= h32 && (k > l32 || k < first))) s[c][i] = -INFINITY;
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!(see >> i & 1)) s[c][i] = -INFINITY;
+          }
         }
         float mx[4];
 #pragma unroll
@@ -583,30 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        if (odd && r < u.rows) {
-          // the infinities and NaNs left out of the edge tiles' products, for the rows that see them
-          const int32_t* bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
-#pragma unroll 1
-          for (int j = u.t0; j < u.t1; ++j) {
-            const int32_t tile = u.tiles.tile(j);
-            if (!edge_tile(p, u.tiles, tile)) continue;
-#pragma unroll 1
-            for (int i = 0; i < kTileTc; ++i) {
-              const int32_t key = tile * kTileTc + i;
-              if (key > pos || (key >= p.sinks && pos - key >= p.window)) continue;
-              const int32_t page = bt[key / kPageTokens];
-              if (page < 0 || page >= p.num_pages) continue;
-              const T* v = static_cast<const T*>(p.v) + page * p.v_stride_page +
-                           (key % kPageTokens) * p.v_stride_token + u.head * p.v_stride_head +
-                           c * 32;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = static_cast<float>(v[e]);
-                if (!isfinite(x)) o[e] += x;
-              }
-            }
-          }
-        }
         if (whole) {
           // four lanes exchange 16-byte chunks, so that together they write 64 bytes of one row
           uint4 w[4];
@@ -631,11 +657,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 8; ++i)
             dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
-        __syncwarp();  // the odd path's loops diverge; tensor-memory loads are warp-wide
+        __syncwarp();
       }
       if (r < u.rows) {
         if (!whole) p.part_ml[part] = make_float2(m, l);
         else if (p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
+      }
+      if (odd) {
+        __threadfence_block();  // (the row was written by four lanes)
+        __syncwarp();
+        if (r < u.rows)
+          add_nonfinite<T, D>(p, u, pos, whole ? static_cast<T*>(p.out) + at * D : nullptr,
+                              p.part_o + part * D);
+        __syncwarp();
       }
       tc_fence_before();
     }
