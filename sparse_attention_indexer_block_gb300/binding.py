@@ -9,6 +9,7 @@ streams. There is no fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import threading
 
@@ -560,57 +561,78 @@ def indexer_decode_topk_noalloc(q, weights, index_cache, block_table, row_seq_le
 # ---------------------------------------------------------------------------
 
 _INVALID, _UNSUPPORTED = 1, 2
+_I32T, _F32T = torch.int32, torch.float32
 
 
-def _need(ok, name, what, status=_INVALID):
-    if not ok:
-        raise IndexerError(name, status, what)
+def _refuse(name, what, status=_INVALID):
+    raise IndexerError(name, status, what)
 
 
 def _need_i32(name, what, t, *shape):
-    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32, name, f"{what} must be an int32 tensor")
-    _need(t.dim() == len(shape) and all(n is None or int(a) == n for a, n in zip(t.shape, shape)),
-          name, f"{what} has shape {tuple(t.shape)}")
-    _need(t.dim() == 0 or t.stride(-1) == 1 or t.shape[-1] <= 1, name,
-          f"{what} must be contiguous in its last dimension")
+    """An int32 tensor of that shape (None: any size), contiguous in its last dimension."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32T:
+        _refuse(name, f"{what} must be an int32 tensor")
+    if t.dim() != len(shape):
+        _refuse(name, f"{what} has shape {tuple(t.shape)}")
+    for a, n in zip(t.shape, shape):
+        if n is not None and a != n:
+            _refuse(name, f"{what} has shape {tuple(t.shape)}")
+    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        _refuse(name, f"{what} must be contiguous in its last dimension")
 
 
 def _need_table(name, block_table, rows=None):
+    """(width, row stride) of a block table."""
     _need_i32(name, "block_table", block_table, rows, None)
-    _need(block_table.shape[1] >= 1, name, "block_table has no columns")
-    _need(block_table.shape[0] <= 1 or block_table.stride(0) >= block_table.shape[1], name,
-          "block_table's rows overlap")
-    return max(int(block_table.stride(0)), int(block_table.shape[1]))
+    n, width = block_table.shape
+    if width < 1:
+        _refuse(name, "block_table has no columns")
+    stride = block_table.stride(0)
+    if stride < width:
+        if n > 1:
+            _refuse(name, "block_table's rows overlap")
+        stride = width
+    return width, stride
 
 
 def _need_error(name, dev_error):
-    if dev_error is not None:
-        _need(isinstance(dev_error, torch.Tensor) and dev_error.element_size() == 4
-              and dev_error.numel() >= 1, name, "dev_error must be a tensor of a 32-bit word")
+    if dev_error is not None and not (isinstance(dev_error, torch.Tensor)
+                                      and dev_error.element_size() == 4 and dev_error.numel() >= 1):
+        _refuse(name, "dev_error must be a tensor of a 32-bit word")
 
 
 def _need_device(name, first, *others):
-    _need(first.is_cuda, name, "tensors must be on a CUDA device")
+    """The index of the CUDA device that all the tensors are on."""
+    if not first.is_cuda:
+        _refuse(name, "tensors must be on a CUDA device")
+    index = first.get_device()
     for t in others:
-        _need(t is None or t.device == first.device, name, "tensors are on different devices")
+        if t is not None and t.get_device() != index:
+            _refuse(name, "tensors are on different devices")
+    return index
 
 
 class _On:
-    """Allocates on, and hands out, the stream a call runs on (the current one
-    of the tensors' device, or the caller's)."""
+    """Allocates on, and hands out, the stream a call runs on: the current one
+    of the tensors' device, or the caller's."""
 
-    def __init__(self, device, stream):
+    __slots__ = ("guard",)
+
+    def __init__(self, index, stream):
         self.guard = None
-        if isinstance(stream, int):
+        if stream is None and torch.cuda.current_device() == index:
+            return
+        device = torch.device("cuda", index)
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
-        if stream is not None or torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.stream(stream if stream is not None
-                                           else torch.cuda.current_stream(device))
+        self.guard = torch.cuda.stream(stream)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -620,69 +642,88 @@ class _On:
 _ATTEND_TYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
+@functools.lru_cache(maxsize=256)
+def _attend_workspace_bytes(device, *sizes):
+    n = C.c_size_t(0)
+    _check("indexer_attend_workspace_bytes", load().indexer_attend_workspace_bytes(*sizes, C.byref(n)))
+    return n.value
+
+
 def attend_workspace(num_tokens: int, num_reqs: int, num_heads: int, num_kv_heads: int,
                      head_dim: int, device="cuda"):
     """Workspace for indexer_attend_paged / indexer_attend_selected calls of at most these sizes."""
-    n = C.c_size_t(0)
-    _check("indexer_attend_workspace_bytes",
-           load().indexer_attend_workspace_bytes(num_tokens, num_reqs, num_heads, num_kv_heads,
-                                                 head_dim, C.byref(n)))
-    return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+    n = _attend_workspace_bytes(torch.cuda.current_device(), num_tokens, num_reqs, num_heads,
+                                num_kv_heads, head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices, scale, out,
             lse, workspace, dev_error, stream, max_query_len=0, window=0, sinks=0):
     for what, t, dims in (("q", q, 3), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4)):
-        _need(isinstance(t, torch.Tensor) and t.dim() == dims, name, f"{what} must have {dims} dimensions")
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            _refuse(name, f"{what} must have {dims} dimensions")
     tokens, heads, dim = q.shape
-    pages, page, kv_heads, _ = k_cache.shape
-    _need(q.dtype in _ATTEND_TYPES, name, f"q is {q.dtype}, not bfloat16 or float16", _UNSUPPORTED)
-    _need(k_cache.dtype == q.dtype and v_cache.dtype == q.dtype, name, "q, k_cache and v_cache differ in type")
-    _need(v_cache.shape == k_cache.shape and k_cache.shape[3] == dim, name,
-          "k_cache and v_cache must be [pages, 64, kv heads, head_dim of q]")
-    _need(page == PAGE_TOKENS, name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
-    _need(dim in (64, 128), name, f"head_dim {dim}, not 64 or 128", _UNSUPPORTED)
-    _need(kv_heads >= 1 and heads >= 1 and heads % kv_heads == 0, name,
-          f"{heads} heads over {kv_heads} kv heads")
-    for what, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(t.stride(-1) == 1, name, f"{what} must be contiguous in its last dimension")
+    pages, page, kv_heads, kv_dim = k_cache.shape
+    dtype = q.dtype
+    if dtype not in _ATTEND_TYPES:
+        _refuse(name, f"q is {dtype}, not bfloat16 or float16", _UNSUPPORTED)
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        _refuse(name, "q, k_cache and v_cache differ in type")
+    if v_cache.shape != k_cache.shape or kv_dim != dim:
+        _refuse(name, "k_cache and v_cache must be [pages, 64, kv heads, head_dim of q]")
+    if page != PAGE_TOKENS:
+        _refuse(name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
+    if dim != 64 and dim != 128:
+        _refuse(name, f"head_dim {dim}, not 64 or 128", _UNSUPPORTED)
+    if kv_heads < 1 or heads < 1 or heads % kv_heads:
+        _refuse(name, f"{heads} heads over {kv_heads} kv heads")
+    qt, qh, qd = q.stride()
+    kp, kt, kh, kd = k_cache.stride()
+    vp, vt, vh, vd = v_cache.stride()
+    if qd != 1 or kd != 1 or vd != 1:
+        _refuse(name, "q, k_cache and v_cache must be contiguous in their last dimension")
     _need_i32(name, "query_start_loc", query_start_loc, None)
-    reqs = int(query_start_loc.shape[0]) - 1
-    _need(reqs >= 0, name, "query_start_loc is empty")
-    bt_stride = _need_table(name, block_table, reqs)
+    reqs = query_start_loc.shape[0] - 1
+    if reqs < 0:
+        _refuse(name, "query_start_loc is empty")
+    bt_width, bt_stride = _need_table(name, block_table, reqs)
+    topk = idx_stride = 0
     if seq_lens is not None:
         _need_i32(name, "seq_lens", seq_lens, reqs)
     if indices is not None:
         _need_i32(name, "indices", indices, tokens, None)
-        _need(indices.shape[1] >= 1, name, "indices has no columns")
-    for what, t, shape, dtype in (("out", out, (tokens, heads, dim), q.dtype),
-                                  ("lse", lse, (tokens, heads), torch.float32)):
-        if t is not None:
-            _need(isinstance(t, torch.Tensor) and tuple(t.shape) == shape and t.dtype == dtype
-                  and t.is_contiguous(), name, f"{what} must be contiguous {dtype} {shape}")
+        topk = indices.shape[1]
+        if topk < 1:
+            _refuse(name, "indices has no columns")
+        idx_stride = indices.stride(0) if tokens > 1 else topk
+    if out is not None and not (isinstance(out, torch.Tensor) and out.shape == q.shape
+                                and out.dtype is dtype and out.is_contiguous()):
+        _refuse(name, f"out must be a contiguous {dtype} tensor of q's shape")
+    if lse is not None and not (isinstance(lse, torch.Tensor) and tuple(lse.shape) == (tokens, heads)
+                                and lse.dtype is _F32T and lse.is_contiguous()):
+        _refuse(name, "lse must be a contiguous float32 tensor [tokens, heads]")
     _need_error(name, dev_error)
-    _need_device(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices, out, lse,
-                 workspace, dev_error)
-    lib = load()
-    with _On(q.device, stream) as s:
+    index = _need_device(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices,
+                         out, lse, workspace, dev_error)
+    with _On(index, stream) as s:
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+            out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
         if lse is None:
-            lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+            lse = torch.empty((tokens, heads), dtype=_F32T, device=q.device)
         if workspace is None:
-            workspace = attend_workspace(tokens, reqs, heads, kv_heads, dim, q.device)
-        qs, ks, vs = q.stride(), k_cache.stride(), v_cache.stride()
+            workspace = torch.empty(_attend_workspace_bytes(index, tokens, reqs, heads, kv_heads, dim),
+                                    dtype=torch.uint8, device=q.device)
         a = Attend(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                    None if seq_lens is None else seq_lens.data_ptr(), query_start_loc.data_ptr(),
                    None if indices is None else indices.data_ptr(), out.data_ptr(), lse.data_ptr(),
                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                    None if dev_error is None else dev_error.data_ptr(),
-                   qs[0], qs[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], pages, bt_stride,
-                   0 if indices is None else max(indices.stride(0), indices.shape[1]),
-                   block_table.shape[1], reqs, tokens, heads, kv_heads, dim, _ATTEND_TYPES[q.dtype],
-                   max_query_len, window, sinks, 0 if indices is None else indices.shape[1],
-                   dim ** -0.5 if scale is None else scale)
-        _check(name, getattr(lib, name)(C.byref(a), s))
+                   qt, qh, kp, kt, kh, vp, vt, vh, pages, bt_stride, idx_stride, bt_width, reqs,
+                   tokens, heads, kv_heads, dim, _ATTEND_TYPES[dtype], max_query_len, window, sinks,
+                   topk, dim ** -0.5 if scale is None else scale)
+        st = getattr(load(), name)(C.byref(a), s)
+        if st:
+            _check(name, st)
     return out, lse
 
 
@@ -707,7 +748,8 @@ def indexer_attend_selected(q, k_cache, v_cache, block_table, indices, query_sta
     [tokens, topk], positions of the token's request, entries < 0 empty (the
     output of indexer_decode_topk / indexer_prefill_topk). Other arguments and
     the result as indexer_attend_paged."""
-    _need(indices is not None, "indexer_attend_selected", "indices is missing")
+    if indices is None:
+        _refuse("indexer_attend_selected", "indices is missing")
     return _attend("indexer_attend_selected", q, k_cache, v_cache, block_table, query_start_loc, None,
                    indices, scale, out, lse, workspace, dev_error, stream)
 
@@ -716,36 +758,48 @@ def _pools(name, pools, num_pages):
     """The pools as idx_page_pool entries: tensors of [pages, ...] whose pages are contiguous."""
     out = (PagePool * max(1, len(pools)))()
     for i, t in enumerate(pools):
-        _need(isinstance(t, torch.Tensor) and t.dim() >= 2, name, "a pool must be a tensor [pages, ...]")
-        _need(num_pages is None or t.shape[0] == num_pages, name, "the pools differ in pages")
-        _need(t.shape[0] >= 1 and t[0].is_contiguous(), name, "a pool's pages must be contiguous")
+        if not isinstance(t, torch.Tensor) or t.dim() < 2:
+            _refuse(name, "a pool must be a tensor [pages, ...]")
+        pages = t.shape[0]
+        if pages < 1 or (num_pages is not None and pages != num_pages):
+            _refuse(name, "the pools differ in pages")
+        num_pages = pages
         size = t.element_size()
-        n = t[0].numel() * size
-        _need(n % 16 == 0 and t.data_ptr() % 16 == 0, name, "a pool's pages must be multiples of 16 bytes")
-        stride = t.stride(0) * size if t.shape[0] > 1 else n
-        out[i] = PagePool(t.data_ptr(), stride, n)
-        num_pages = t.shape[0]
+        if t.is_contiguous():
+            n = stride = t.numel() // pages * size
+        else:
+            one = t[0]
+            n = one.numel() * size
+            stride = t.stride(0) * size if pages > 1 else n
+            if not one.is_contiguous():
+                _refuse(name, "a pool's pages must be contiguous")
+        at = t.data_ptr()
+        if n % 16 or at % 16:
+            _refuse(name, "a pool's pages must be multiples of 16 bytes")
+        p = out[i]
+        p.base, p.page_stride, p.page_bytes = at, stride, n
     return out, num_pages
 
 
 def _need_rows(name, block_table, seq_lens, ref_counts):
-    stride = _need_table(name, block_table)
-    _need_i32(name, "seq_lens", seq_lens, int(block_table.shape[0]))
+    width, stride = _need_table(name, block_table)
+    _need_i32(name, "seq_lens", seq_lens, block_table.shape[0])
     _need_i32(name, "ref_counts", ref_counts, None)
-    return stride
+    return block_table.shape[0], width, stride
 
 
 def indexer_copy_pages(pools, src, dst, dev_error=None, stream=None):
     """Page src[i] to page dst[i] (int32 [n]) in every pool (tensors [pages, ...]); negative
     entries are skipped."""
     name = "indexer_copy_pages"
-    _need(len(pools) > 0, name, "no pools")
+    if not pools:
+        _refuse(name, "no pools")
     _need_i32(name, "src", src, None)
     _need_i32(name, "dst", dst, int(src.shape[0]))
     _need_error(name, dev_error)
     arr, pages = _pools(name, pools, None)
-    _need_device(name, src, dst, dev_error, *pools)
-    with _On(src.device, stream) as s:
+    index = _need_device(name, src, dst, dev_error, *pools)
+    with _On(index, stream) as s:
         _check(name, load().indexer_copy_pages(arr, len(pools), pages, _ptr(src), _ptr(dst),
                                                int(src.shape[0]), _ptr(dev_error), s))
 
@@ -757,7 +811,7 @@ def indexer_fork_pages(pools, block_table, seq_lens, ref_counts, parents, childr
     seq_lens, ref_counts (int32) and the pools change in place. Returns (copy_src, copy_dst)
     int32 [n]: the page copies made, then -1."""
     name = "indexer_fork_pages"
-    bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
+    rows_n, width, bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
     _need_i32(name, "parents", parents, None)
     n = int(parents.shape[0])
     _need_i32(name, "children", children, n)
@@ -766,17 +820,16 @@ def indexer_fork_pages(pools, block_table, seq_lens, ref_counts, parents, childr
             _need_i32(name, what, t, n)
     _need_error(name, dev_error)
     arr, pages = _pools(name, pools, int(ref_counts.shape[0]))
-    _need_device(name, block_table, seq_lens, ref_counts, parents, children, copy_src, copy_dst,
-                 dev_error, *pools)
-    with _On(block_table.device, stream) as s:
+    index = _need_device(name, block_table, seq_lens, ref_counts, parents, children, copy_src, copy_dst,
+                         dev_error, *pools)
+    with _On(index, stream) as s:
         if copy_src is None:
             copy_src = torch.empty_like(parents)
         if copy_dst is None:
             copy_dst = torch.empty_like(parents)
         _check(name, load().indexer_fork_pages(
-            arr, len(pools), pages, _ptr(block_table), bt_stride, int(block_table.shape[1]),
-            int(block_table.shape[0]), _ptr(seq_lens), _ptr(ref_counts), _ptr(parents),
-            _ptr(children), n, _ptr(copy_src), _ptr(copy_dst), _ptr(dev_error), s))
+            arr, len(pools), pages, _ptr(block_table), bt_stride, width, rows_n,
+            _ptr(seq_lens), _ptr(ref_counts), _ptr(parents), _ptr(children), n, _ptr(copy_src), _ptr(copy_dst), _ptr(dev_error), s))
     return copy_src, copy_dst
 
 
@@ -784,15 +837,23 @@ def indexer_free_pages(block_table, seq_lens, ref_counts, rows, dev_error=None, 
     """Frees the block-table rows listed in rows (int32, distinct): their pages lose a reference
     in ref_counts, their seq_lens become 0, in place."""
     name = "indexer_free_pages"
-    bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
+    rows_n, width, bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
     _need_i32(name, "rows", rows, None)
     _need_error(name, dev_error)
-    _need_device(name, block_table, seq_lens, ref_counts, rows, dev_error)
-    with _On(block_table.device, stream) as s:
+    index = _need_device(name, block_table, seq_lens, ref_counts, rows, dev_error)
+    with _On(index, stream) as s:
         _check(name, load().indexer_free_pages(
-            _ptr(block_table), bt_stride, int(block_table.shape[1]), int(block_table.shape[0]),
+            _ptr(block_table), bt_stride, width, rows_n,
             _ptr(seq_lens), _ptr(ref_counts), int(ref_counts.shape[0]), _ptr(rows),
             int(rows.shape[0]), _ptr(dev_error), s))
+
+
+@functools.lru_cache(maxsize=256)
+def _compact_workspace_bytes(pages):
+    n = C.c_size_t(0)
+    _check("indexer_compact_workspace_bytes",
+           load().indexer_compact_workspace_bytes(pages, C.byref(n)))
+    return n.value
 
 
 def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, num_live=None,
@@ -801,7 +862,7 @@ def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, 
     place). Returns (remap int32 [pages]: a page's new number, -1 if it was free; num_live int32
     [1] on the device: pages in use)."""
     name = "indexer_compact_pages"
-    bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
+    rows_n, width, bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
     pages = int(ref_counts.shape[0])
     if remap is not None:
         _need_i32(name, "remap", remap, pages)
@@ -809,21 +870,18 @@ def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, 
         _need_i32(name, "num_live", num_live, 1)
     _need_error(name, dev_error)
     arr, pages = _pools(name, pools, pages)
-    _need_device(name, block_table, seq_lens, ref_counts, remap, num_live, workspace, dev_error, *pools)
+    index = _need_device(name, block_table, seq_lens, ref_counts, remap, num_live, workspace, dev_error, *pools)
     lib = load()
-    with _On(block_table.device, stream) as s:
+    with _On(index, stream) as s:
         if remap is None:
             remap = torch.empty(pages, dtype=torch.int32, device=ref_counts.device)
         if num_live is None:
             num_live = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
         if workspace is None:
-            size = C.c_size_t(0)
-            _check("indexer_compact_workspace_bytes",
-                   lib.indexer_compact_workspace_bytes(pages, C.byref(size)))
-            workspace = torch.empty(int(size.value), dtype=torch.uint8, device=ref_counts.device)
+            workspace = torch.empty(_compact_workspace_bytes(pages), dtype=torch.uint8,
+                                    device=ref_counts.device)
         _check(name, lib.indexer_compact_pages(
-            arr, len(pools), pages, _ptr(block_table), bt_stride, int(block_table.shape[1]),
-            int(block_table.shape[0]), _ptr(seq_lens), _ptr(ref_counts), _ptr(remap),
-            _ptr(num_live), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+            arr, len(pools), pages, _ptr(block_table), bt_stride, width, rows_n,
+            _ptr(seq_lens), _ptr(ref_counts), _ptr(remap), _ptr(num_live), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
             _ptr(dev_error), s))
     return remap, num_live

@@ -692,8 +692,8 @@ template <typename T, int D, int MT, bool kSel>
 idx_status launch_rows_as(const AttendParams& p, cudaStream_t s) {
   using C = RowsCfg<D, MT>;
   const auto kernel = attend_rows_kernel<T, D, MT, kSel>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_pdl(kernel, p.grid, kWarps * 32, C::kSmem, s, p));
 }

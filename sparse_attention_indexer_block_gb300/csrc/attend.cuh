@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -229,6 +230,26 @@ constexpr float kLn2 = 0.693147180559945309f;
 
 constexpr int kTileTc = 128;   // keys of a tensor-memory kernel's tile: two pages
 constexpr int kRowsTc = 256;   // its query rows: two accumulators of 128
+
+// Raises the kernel's limit of dynamic shared memory, once per device (any host
+// thread; doing it twice is harmless). kRegs: registers a thread that the kernel
+// must have been built with (0: any).
+template <int kBytes, int kRegs, typename Kernel>
+inline cudaError_t allow_smem(Kernel* kernel, std::atomic<bool>* configured) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  if (cached && configured[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  if (kRegs) {
+    cudaFuncAttributes a;
+    if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return e;
+    if (a.numRegs != kRegs) return cudaErrorInvalidConfiguration;
+  }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e == cudaSuccess && cached) configured[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 // Launchers.
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s);

@@ -2,7 +2,6 @@
 // cores: blocks of 256 query rows of one kv head against tiles of 128 keys.
 #include <cudaTypedefs.h>
 
-#include <atomic>
 #include <mutex>
 
 #include "attend.cuh"
@@ -719,19 +718,10 @@ idx_status launch_tc_as(const AttendParams& p, const CUtensorMap& kmap, const CU
                         cudaStream_t s) {
   using C = TcCfg<D>;
   const auto kernel = attend_tc_kernel<T, D>;
+  // (the register split hands out what the launch holds, no more)
   static std::atomic<bool> configured[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || dev < 0) return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidDevice);
-  if (dev >= kMaxDevices || !configured[dev].load(std::memory_order_acquire)) {
-    cudaFuncAttributes a;
-    if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return cuda_status(e);
-    // the register split hands out what the launch holds, no more
-    if (a.numRegs != kRegsLaunch) return cuda_status(cudaErrorInvalidConfiguration);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return cuda_status(e);
-    if (dev < kMaxDevices) configured[dev].store(true, std::memory_order_release);
-  }
+  const cudaError_t e = allow_smem<C::kSmem, kRegsLaunch>(kernel, configured);
+  if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_pdl(kernel, p.grid, kThreads, C::kSmem, s, p, kmap, vmap));
 }
 
