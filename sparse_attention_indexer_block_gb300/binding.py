@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -41,6 +42,11 @@ class Attend(C.Structure):
                                             "num_kv_heads", "head_dim", "dtype", "max_query_len",
                                             "window", "sinks", "topk")]
                 + [("scale", C.c_float)])
+
+
+# the same as packed bytes (building the structure costs three times as much)
+_ATTEND_BYTES = struct.Struct("=12Q11q11if")
+assert _ATTEND_BYTES.size == C.sizeof(Attend)
 
 
 class PagePool(C.Structure):
@@ -97,8 +103,8 @@ SIGNATURES = {
 
 SIGNATURES.update({
     "indexer_attend_workspace_bytes": (C.c_int, [_I32, _I32, _I32, _I32, _I32, C.POINTER(_SZ)]),
-    "indexer_attend_paged": (C.c_int, [C.POINTER(Attend), _P]),
-    "indexer_attend_selected": (C.c_int, [C.POINTER(Attend), _P]),
+    "indexer_attend_paged": (C.c_int, [_P, _P]),
+    "indexer_attend_selected": (C.c_int, [_P, _P]),
     "indexer_copy_pages": (C.c_int, [C.POINTER(PagePool), _I32, _I64, _P, _P, _I32, _P, _P]),
     "indexer_fork_pages": (C.c_int, [C.POINTER(PagePool), _I32, _I64, _P, _I64, _I32, _I32, _P, _P,
                                      _P, _P, _I32, _P, _P, _P, _P]),
@@ -616,10 +622,11 @@ class _On:
     """Allocates on, and hands out, the stream a call runs on: the current one
     of the tensors' device, or the caller's."""
 
-    __slots__ = ("guard",)
+    __slots__ = ("guard", "index")
 
     def __init__(self, index, stream):
         self.guard = None
+        self.index = index
         if stream is None and torch.cuda.current_device() == index:
             return
         device = torch.device("cuda", index)
@@ -632,7 +639,8 @@ class _On:
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        # (the handle that current_stream().cuda_stream gives, without the stream object)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -702,6 +710,9 @@ def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, i
     if lse is not None and not (isinstance(lse, torch.Tensor) and tuple(lse.shape) == (tokens, heads)
                                 and lse.dtype is _F32T and lse.is_contiguous()):
         _refuse(name, "lse must be a contiguous float32 tensor [tokens, heads]")
+    for what, n in (("max_query_len", max_query_len), ("window", window), ("sinks", sinks)):
+        if not 0 <= n <= 0x7fffffff:
+            _refuse(name, f"{what} {n}")
     _need_error(name, dev_error)
     index = _need_device(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices,
                          out, lse, workspace, dev_error)
@@ -713,15 +724,16 @@ def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, i
         if workspace is None:
             workspace = torch.empty(_attend_workspace_bytes(index, tokens, reqs, heads, kv_heads, dim),
                                     dtype=torch.uint8, device=q.device)
-        a = Attend(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                   None if seq_lens is None else seq_lens.data_ptr(), query_start_loc.data_ptr(),
-                   None if indices is None else indices.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                   None if dev_error is None else dev_error.data_ptr(),
-                   qt, qh, kp, kt, kh, vp, vt, vh, pages, bt_stride, idx_stride, bt_width, reqs,
-                   tokens, heads, kv_heads, dim, _ATTEND_TYPES[dtype], max_query_len, window, sinks,
-                   topk, dim ** -0.5 if scale is None else scale)
-        st = getattr(load(), name)(C.byref(a), s)
+        a = _ATTEND_BYTES.pack(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+            0 if seq_lens is None else seq_lens.data_ptr(), query_start_loc.data_ptr(),
+            0 if indices is None else indices.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            0 if dev_error is None else dev_error.data_ptr(),
+            qt, qh, kp, kt, kh, vp, vt, vh, pages, bt_stride, idx_stride, bt_width, reqs, tokens,
+            heads, kv_heads, dim, _ATTEND_TYPES[dtype], max_query_len, window, sinks, topk,
+            dim ** -0.5 if scale is None else scale)
+        st = getattr(load(), name)(a, s)
         if st:
             _check(name, st)
     return out, lse

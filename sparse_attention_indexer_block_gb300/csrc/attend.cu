@@ -50,6 +50,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // Inclusive sum of v over the block's threads; *total gets the sum of all.
+template <int kThreads>
 __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int d = 1; d < 32; d <<= 1) {
@@ -60,7 +61,7 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    int64_t w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+    int64_t w = lane < kThreads / 32 ? warp_sums[lane] : 0;
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, w, d);
       if (lane >= d) w += o;
@@ -68,7 +69,7 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
     warp_sums[lane] = w;
   }
   __syncthreads();
-  *total = warp_sums[kPlanThreads / 32 - 1];
+  *total = warp_sums[kThreads / 32 - 1];
   return v + (warp ? warp_sums[warp - 1] : 0);
 }
 
@@ -109,6 +110,35 @@ __device__ int4 cut_at(const AttendParams& p, int c) {
   return make_int4(a - e0, head, off > 0 ? off : 0, lo);
 }
 
+// The same from the costs of whole requests (cost[b]: exclusive prefix of
+// their units' costs for one kv head), which a CTA of the row-block kernel works
+// out for itself when there are few requests.
+__device__ int4 cut_at_request(const AttendParams& p, const int64_t* cost, int c) {
+  const int64_t all = cost[p.num_reqs] * p.num_kv_heads;
+  const int64_t pos = all / p.grid * c + all % p.grid * c / p.grid;
+  if (c >= p.grid || pos >= all) return make_int4(0, 0, 0, p.num_reqs);
+  int lo = 0, hi = p.num_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cost[mid] * p.num_kv_heads <= pos) lo = mid; else hi = mid - 1;
+  }
+  const int64_t one = cost[lo + 1] - cost[lo], rest = pos - cost[lo] * p.num_kv_heads;
+  const int32_t head = static_cast<int32_t>(rest / one);
+  int64_t off = rest % one;
+  const ReqShape r = request_shape(p, lo, false);
+  int32_t u = 0;
+  for (;; ++u) {
+    const int32_t n = unit_tiles(p, r, u).count + p.unit_overhead;
+    if (off < n) break;
+    off -= n;
+  }
+  return make_int4(u, head, static_cast<int32_t>(max(off - p.unit_overhead, int64_t{0})), lo);
+}
+
+// Requests up to which a CTA of the row-block kernel plans for itself: one
+// scan of their lengths, against a launch of the planning kernel (4 us).
+constexpr int kSelfPlanReqs = 512;
+
 // One CTA: entries of the requests, their costs and the CTAs' cuts. Bound by
 // the latency of a few dependent loads and scans.
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendParams p) {
@@ -119,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
   for (int b0 = 0; b0 < p.num_reqs; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
     const int64_t n = b < p.num_reqs ? request_entries(p, request_shape(p, b, true)) : 0;
-    const int64_t incl = carry + block_scan(n, sums, &total);
+    const int64_t incl = carry + block_scan<kPlanThreads>(n, sums, &total);
     // offsets that are not ascending could ask for more entries than there is room for
     if (b < p.num_reqs) {
       if (incl > p.max_entries) set_error(p.dev_error, IDX_DEV_BAD_LEN);
@@ -141,7 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
       const int b = entry_request(p.req_entry, p.num_reqs, e);
       cost = unit_tiles(p, request_shape(p, b, false), e - p.req_entry[b]).count + p.unit_overhead;
     }
-    const int64_t incl = carry + block_scan(cost, sums, &total);
+    const int64_t incl = carry + block_scan<kPlanThreads>(cost, sums, &total);
     if (e < entries) p.entry_cost[e + 1] = incl;
     carry += total;
   }
@@ -234,7 +264,40 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
     first_tile = a.y;
     last_tile = b.y;
   }
-  PieceWalk walk(kSel ? PieceWalk() : PieceWalk(p, cta));
+  PieceWalk walk;
+  if constexpr (!kSel) {
+    if (p.self_plan) {
+      int64_t* const cost = reinterpret_cast<int64_t*>(smem);  // [num_reqs + 1]
+      __shared__ int64_t sums[32];
+      __shared__ int4 cuts[2];
+      constexpr int kThreads = kWarps * 32;
+      int64_t carry = 0, total;
+      for (int b0 = 0; b0 < p.num_reqs; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int64_t n = 0;
+        if (b < p.num_reqs) {
+          const ReqShape r = request_shape(p, b, cta == 0);
+          const int32_t e = request_entries(p, r);
+          for (int32_t i = 0; i < e; ++i) n += unit_tiles(p, r, i).count + p.unit_overhead;
+        }
+        const int64_t incl = carry + block_scan<kThreads>(n, sums, &total);
+        if (b < p.num_reqs) cost[b + 1] = incl;
+        carry += total;
+      }
+      if (threadIdx.x == 0) cost[0] = 0;
+      __syncthreads();
+      if (threadIdx.x < 2) {
+        const int4 at = cut_at_request(p, cost, cta + threadIdx.x);
+        cuts[threadIdx.x] = at;
+        // (for the join; the last CTA's end too)
+        if (threadIdx.x == 0 || cta == p.grid - 1) p.bound[cta + threadIdx.x] = at;
+      }
+      __syncthreads();
+      walk = PieceWalk(cuts[0], cuts[1]);
+    } else {
+      walk = PieceWalk(p.bound[cta], p.bound[cta + 1]);
+    }
+  }
 
   for (;;) {
     Piece u;
@@ -722,6 +785,8 @@ idx_status launch_combine_as(const AttendParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+int attend_self_plan_reqs() { return kSelfPlanReqs; }
 
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s) {
   return cuda_status(launch_pdl(attend_plan_kernel, 1, kPlanThreads, 0, s, p));

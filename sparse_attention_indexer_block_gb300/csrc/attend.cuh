@@ -52,6 +52,7 @@ struct AttendParams {
   float* part_o;                   // [2 * grid, rows, head_dim] unnormalised pieces
   float2* part_ml;                 // [2 * grid, rows] their maximum and sum
   int32_t max_entries;
+  int32_t self_plan;               // the row-block kernel works `bound` out for itself
   int32_t grid;                    // CTAs of the row-block launch
   int32_t rows;                    // query rows of a unit
   int32_t tile_log2;               // keys of a tile
@@ -149,8 +150,8 @@ struct PieceWalk {
   bool done, stale;
 
   PieceWalk() = default;
-  __device__ __forceinline__ PieceWalk(const AttendParams& p, int cta)
-      : cur(p.bound[cta]), end(p.bound[cta + 1]), done(false), stale(true) {}
+  __device__ __forceinline__ PieceWalk(const int4& from, const int4& to)
+      : cur(from), end(to), done(false), stale(true) {}
 
   __device__ __forceinline__ bool next(const AttendParams& p, Piece* u) {
     if (done || cur.w >= p.num_reqs) return false;
@@ -158,7 +159,7 @@ struct PieceWalk {
     if (last && end.z <= cur.z) return false;
     if (stale) {
       shape = request_shape(p, cur.w, false);
-      entries = p.req_entry[cur.w + 1] - p.req_entry[cur.w];
+      entries = request_entries(p, shape);
       stale = false;
     }
     u->req = cur.w;
@@ -177,9 +178,11 @@ struct PieceWalk {
         cur.x = 0;
         if (++cur.y == p.num_kv_heads) {
           cur.y = 0;
-          do ++cur.w;
-          while (cur.w < p.num_reqs && p.req_entry[cur.w + 1] == p.req_entry[cur.w]);
-          stale = true;
+          do {
+            if (++cur.w == p.num_reqs) break;
+            shape = request_shape(p, cur.w, false);
+            entries = request_entries(p, shape);
+          } while (entries == 0);
         }
       }
     }
@@ -252,6 +255,7 @@ inline cudaError_t allow_smem(Kernel* kernel, std::atomic<bool>* configured) {
 }
 
 // Launchers.
+int attend_self_plan_reqs();
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s);
 idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, int mt, cudaStream_t s);
 // (the caches' strides have to suit a tensor map: attend_tc_takes)

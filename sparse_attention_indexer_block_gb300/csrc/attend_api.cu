@@ -189,7 +189,8 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
-  if ((st = launch_attend_plan(p, s)) != IDX_OK) return st;
+  p.self_plan = !tc && a->num_reqs <= attend_self_plan_reqs() && longest * p.group <= 4 * v.rows;
+  if (!p.self_plan && (st = launch_attend_plan(p, s)) != IDX_OK) return st;
   st = tc ? launch_attend_tc(p, a->head_dim, half, s)
           : launch_attend_rows(p, a->head_dim, half, v.mt, s);
   if (st != IDX_OK) return st;

@@ -17,7 +17,6 @@ constexpr int kSlotRows = 128;       // rows of one accumulator (a slot)
 constexpr int kRegsLaunch = 168, kRegsFeed = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsFeed + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr int kTmemCols = 512;
-constexpr int kColS = 0, kColO = 256;  // scores (and weights) of slot i at kColS + 128 i
 constexpr uint32_t kOddUnits = 8;
 // A row's running maximum is raised (and its accumulator rescaled) only when a
 // score exceeds it by this many units of log 2: the weights then stay below
@@ -26,6 +25,13 @@ constexpr float kLazyRaise = 8.f;
 
 template <int D>
 struct TcCfg {
+  // Tensor memory: scores of slot i at 128 i, its accumulator at kColO + D i. At D = 64 the
+  // weights have columns of their own, so that the next tile's scores are on their way while
+  // this one's weights are worked out; at D = 128 they take the first half of the scores'.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr int kColO = 256;
+  static constexpr int kColP = kOwnP ? kColO + 2 * D : 0;
+  static constexpr int kStepP = kOwnP ? 64 : 128;  // from slot 0's weights to slot 1's
   static constexpr int kSlotBytes = kSlotRows * D * 2;
   static constexpr int kQ = 2 * kSlotBytes;
   static constexpr int kStage = kTileTc * D * 2;
@@ -42,7 +48,9 @@ struct TcBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[5], k_empty[5];
   uint64_t v_full[5], v_empty[5], v_ok[5];  // v_ok: edge tiles cleared (or none)
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], o_full[2];
+  uint64_t p_full[2][2];           // halves of the weights: keys 0-63 and 64-127 of the tile
+  uint64_t s_free[2], p_free[2];   // kOwnP: scores read, weights used
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag;
@@ -250,7 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], kSlotRows);
+      mbar_init(&bars.p_full[i][0], 4);
+      mbar_init(&bars.p_full[i][1], 4);
+      mbar_init(&bars.s_free[i], 4);
+      mbar_init(&bars.p_free[i], 1);
       mbar_init(&bars.o_full[i], 1);
     }
     mbar_init(&bars.done, 1);
@@ -266,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
   pdl_wait();
   pdl_trigger();
-  PieceWalk walk(p, blockIdx.x);
+  PieceWalk walk(p.bound[blockIdx.x], p.bound[blockIdx.x + 1]);
   Piece u;
 
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -344,10 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = sw128_mnmajor_desc(v_addr, C::kHalf);
       Ring<KS> ka;
       Ring<VS> va;
-      uint32_t q_phase = 0, p_phase = 0;  // (bit i: slot i)
+      uint32_t q_phase = 0, p_phase = 0, s_phase = 0, s_used = 0;  // (bit i: slot i)
       bool ok = true, issued = false;
       const auto qk = [&](int slot, int stage) {
-        const uint32_t d = tmem + kColS + slot * 128;
+        const uint32_t d = tmem + slot * 128;
         const uint64_t a = q_desc + slot * (C::kSlotBytes >> 4);
         const uint64_t b = k_desc + stage * (C::kStage >> 4);
 #pragma unroll
@@ -356,73 +367,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                      b + (((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4), kDescQK, kk > 0);
         mma_commit(&bars.s_full[slot]);
       };
-      const auto pv = [&](int slot, int stage, bool first) {
-        const uint32_t d = tmem + kColO + slot * 128, a = tmem + kColS + slot * 128;
+      const auto pv = [&](int slot, int stage, int half, bool first) {
+        const uint32_t d = tmem + C::kColO + slot * D, a = tmem + C::kColP + slot * C::kStepP;
         const uint64_t b = v_desc + stage * (C::kStage >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kTileTc / 16; ++kk)
-          mma_f16_ts(d, a + kk * 8, b + (kk * 2048 >> 4), kDescPV, !first || kk > 0);
+        for (int i = 0; i < kTileTc / 32; ++i) {
+          const int kk = half * (kTileTc / 32) + i;
+          mma_f16_ts(d, a + kk * 8, b + kk * (2048 >> 4), kDescPV, !first || kk > 0);
+        }
+      };
+      // with weights of their own, a slot's scores may be overwritten once they have been read
+      const auto scores_free = [&](int slot) -> bool {
+        if (!C::kOwnP) return true;
+        const uint32_t bit = 1u << slot;
+        if (s_used & bit) {
+          if (!wait_warp(&bars.s_free[slot], (s_phase >> slot) & 1)) return false;
+          s_phase ^= bit;
+        }
+        s_used |= bit;
+        return true;
       };
       while (ok && walk.next(p, &u)) {
         const int n = u.t1 - u.t0;
         if (n <= 0) continue;
-        const bool two = u.rows > kSlotRows;
+        const int slots = u.rows > kSlotRows ? 2 : 1;
         issued = true;
         if (!(ok = wait_warp(&bars.q_full, q_phase))) break;
         q_phase ^= 1;
-        if (!(ok = wait_warp(&bars.k_full[ka.stage], ka.phase))) break;
-        if (elect_one()) {
-          qk(0, ka.stage);
-          if (two) qk(1, ka.stage);
-          mma_commit(&bars.k_empty[ka.stage]);
-          if (n == 1) mma_commit(&bars.q_empty);
-        }
-        __syncwarp();
-        ka.step();
-        for (int j = 0; j < n; ++j) {
-          const int sv = va.stage, sk = ka.stage;
-          const bool more = j + 1 < n;
-          if (!(ok = wait_warp(&bars.v_ok[sv], va.phase))) break;
-          va.step();
-          if (!(ok = wait_warp(&bars.p_full[0], p_phase & 1))) break;
-          p_phase ^= 1;
-          tc_fence_after();
+        // the scores of tile j for one slot; the last slot frees K (and the queries)
+        const auto scores = [&](int j, int slot) -> bool {
+          if (slot == 0 && !wait_warp(&bars.k_full[ka.stage], ka.phase)) return false;
+          if (!scores_free(slot)) return false;
           if (elect_one()) {
-            pv(0, sv, j == 0);
-            if (!more) {
-              mma_commit(&bars.o_full[0]);
-              if (!two) mma_commit(&bars.v_empty[sv]);
+            qk(slot, ka.stage);
+            if (slot == slots - 1) {
+              mma_commit(&bars.k_empty[ka.stage]);
+              if (j == n - 1) mma_commit(&bars.q_empty);
             }
           }
           __syncwarp();
-          if (more) {
-            if (!(ok = wait_warp(&bars.k_full[sk], ka.phase))) break;
-            ka.step();
+          if (slot == slots - 1) ka.step();
+          return true;
+        };
+        for (int slot = 0; ok && slot < slots; ++slot) ok = scores(0, slot);
+        for (int j = 0; ok && j < n; ++j) {
+          const int sv = va.stage;
+          const bool more = j + 1 < n;
+          if (C::kOwnP && more)
+            for (int slot = 0; ok && slot < slots; ++slot) ok = scores(j + 1, slot);
+          if (!ok || !(ok = wait_warp(&bars.v_ok[sv], va.phase))) break;
+          va.step();
+          for (int slot = 0; slot < slots; ++slot) {
+            const uint32_t parity = (p_phase >> slot) & 1;
+            p_phase ^= 1u << slot;
+            if (!(ok = wait_warp(&bars.p_full[slot][0], parity))) break;
+            tc_fence_after();
+            if (elect_one()) pv(slot, sv, 0, j == 0);
+            __syncwarp();
+            if (!(ok = wait_warp(&bars.p_full[slot][1], parity))) break;
+            tc_fence_after();
             if (elect_one()) {
-              qk(0, sk);
-              if (!two) {
-                mma_commit(&bars.v_empty[sv]);
-                mma_commit(&bars.k_empty[sk]);
-                if (j + 2 == n) mma_commit(&bars.q_empty);
-              }
+              pv(slot, sv, 1, j == 0);
+              if (!more) mma_commit(&bars.o_full[slot]);
+              else if (C::kOwnP) mma_commit(&bars.p_free[slot]);
+              if (slot == slots - 1) mma_commit(&bars.v_empty[sv]);
             }
             __syncwarp();
+            if (!C::kOwnP && more && !(ok = scores(j + 1, slot))) break;
           }
-          if (!two) continue;
-          if (!(ok = wait_warp(&bars.p_full[1], p_phase >> 1))) break;
-          p_phase ^= 2;
-          tc_fence_after();
-          if (elect_one()) {
-            pv(1, sv, j == 0);
-            if (!more) mma_commit(&bars.o_full[1]);
-            mma_commit(&bars.v_empty[sv]);
-            if (more) {
-              qk(1, sk);
-              mma_commit(&bars.k_empty[sk]);
-              if (j + 2 == n) mma_commit(&bars.q_empty);
-            }
-          }
-          __syncwarp();
         }
       }
       if (issued) {
@@ -520,9 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slot = (warp - 4) >> 2;
     const int r = slot * kSlotRows + (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_col = lanes + kColS + slot * 128, o_col = lanes + kColO + slot * 128;
+    const uint32_t s_col = lanes + slot * 128, o_col = lanes + C::kColO + slot * D;
+    const uint32_t p_col = lanes + C::kColP + slot * C::kStepP;
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    uint32_t s_phase = 0, o_phase = 0, unit = 0;
+    uint32_t s_phase = 0, o_phase = 0, f_phase = 0, unit = 0;
     bool ok = true;
     while (ok && walk.next(p, &u)) {
       const int n = u.t1 - u.t0;
@@ -543,6 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
         tmem_ld_wait();
+        if (C::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.s_free[slot]);
+        }
         if (edge_tile(p, u.tiles, tile)) {
           // bit i of a word: key s0 + i is seen (i <= hi and (i > lo or i < first))
           const int32_t s0 = tile * kTileTc;
@@ -570,6 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = exp2_approx(m - top);
           m = top;
           l *= alpha;
+        }
+        if (C::kOwnP && j > 0) {
+          // (else the scores' arrival says that the last tile's products are done)
+          if (!(ok = wait_warp(&bars.p_free[slot], f_phase))) break;
+          f_phase ^= 1;
+          tc_fence_after();
         }
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
@@ -600,11 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // each); their sum is of the unrounded ones
             w[i] = pack2<T>(a, b);
           }
-          tmem_st32(s_col + c * 32, w);
+          tmem_st32(p_col + c * 32, w);
+          // (the second product begins with the first half of the keys)
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.p_full[slot][c]);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bars.p_full[slot]);
         const float2 sum = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
         l += sum.x + sum.y;
       }

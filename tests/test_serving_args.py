@@ -175,6 +175,7 @@ BAD_TENSORS = [
     dict(out=torch.zeros(6, 8, 128)), dict(lse=torch.zeros(6, 4)),
     dict(dev_error=torch.zeros(1, dtype=torch.int64)),
     dict(),  # all well but on the CPU
+    dict(window=-1), dict(window=1 << 31), dict(sinks=-5), dict(max_query_len=1 << 40),
 ]
 
 
@@ -182,7 +183,7 @@ BAD_TENSORS = [
 def test_binding_refuses_tensors(over):
     with pytest.raises(saib.IndexerError):
         saib.indexer_attend_paged(**_tensors(**over))
-    if "seq_lens" not in over:
+    if not {"seq_lens", "window", "sinks", "max_query_len"} & set(over):
         t = _tensors(**over)
         t.pop("seq_lens")
         with pytest.raises(saib.IndexerError):
