@@ -25,13 +25,8 @@ constexpr float kLazyRaise = 8.f;
 
 template <int D>
 struct TcCfg {
-  // Tensor memory: scores of slot i at 128 i, its accumulator at kColO + D i. At D = 64 the
-  // weights have columns of their own, so that the next tile's scores are on their way while
-  // this one's weights are worked out; at D = 128 they take the first half of the scores'.
-  static constexpr bool kOwnP = D == 64;
+  // Tensor memory: scores of slot i at 128 i, its weights over them, its accumulator at kColO + D i
   static constexpr int kColO = 256;
-  static constexpr int kColP = kOwnP ? kColO + 2 * D : 0;
-  static constexpr int kStepP = kOwnP ? 64 : 128;  // from slot 0's weights to slot 1's
   static constexpr int kSlotBytes = kSlotRows * D * 2;
   static constexpr int kQ = 2 * kSlotBytes;
   static constexpr int kStage = kTileTc * D * 2;
@@ -50,7 +45,6 @@ struct TcBars {
   uint64_t v_full[5], v_empty[5], v_ok[5];  // v_ok: edge tiles cleared (or none)
   uint64_t s_full[2], o_full[2];
   uint64_t p_full[2][2];           // halves of the weights: keys 0-63 and 64-127 of the tile
-  uint64_t s_free[2], p_free[2];   // kOwnP: scores read, weights used
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag;
@@ -128,6 +122,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // True in one lane of a converged warp.
@@ -260,8 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.p_full[i][0], 4);
       mbar_init(&bars.p_full[i][1], 4);
-      mbar_init(&bars.s_free[i], 4);
-      mbar_init(&bars.p_free[i], 1);
       mbar_init(&bars.o_full[i], 1);
     }
     mbar_init(&bars.done, 1);
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = sw128_mnmajor_desc(v_addr, C::kHalf);
       Ring<KS> ka;
       Ring<VS> va;
-      uint32_t q_phase = 0, p_phase = 0, s_phase = 0, s_used = 0;  // (bit i: slot i)
+      uint32_t q_phase = 0, p_phase = 0;  // (bit i: slot i)
       bool ok = true, issued = false;
       const auto qk = [&](int slot, int stage) {
         const uint32_t d = tmem + slot * 128;
@@ -368,24 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&bars.s_full[slot]);
       };
       const auto pv = [&](int slot, int stage, int half, bool first) {
-        const uint32_t d = tmem + C::kColO + slot * D, a = tmem + C::kColP + slot * C::kStepP;
+        const uint32_t d = tmem + C::kColO + slot * D, a = tmem + slot * 128;
         const uint64_t b = v_desc + stage * (C::kStage >> 4);
 #pragma unroll
         for (int i = 0; i < kTileTc / 32; ++i) {
           const int kk = half * (kTileTc / 32) + i;
           mma_f16_ts(d, a + kk * 8, b + kk * (2048 >> 4), kDescPV, !first || kk > 0);
         }
-      };
-      // with weights of their own, a slot's scores may be overwritten once they have been read
-      const auto scores_free = [&](int slot) -> bool {
-        if (!C::kOwnP) return true;
-        const uint32_t bit = 1u << slot;
-        if (s_used & bit) {
-          if (!wait_warp(&bars.s_free[slot], (s_phase >> slot) & 1)) return false;
-          s_phase ^= bit;
-        }
-        s_used |= bit;
-        return true;
       };
       while (ok && walk.next(p, &u)) {
         const int n = u.t1 - u.t0;
@@ -397,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the scores of tile j for one slot; the last slot frees K (and the queries)
         const auto scores = [&](int j, int slot) -> bool {
           if (slot == 0 && !wait_warp(&bars.k_full[ka.stage], ka.phase)) return false;
-          if (!scores_free(slot)) return false;
           if (elect_one()) {
             qk(slot, ka.stage);
             if (slot == slots - 1) {
@@ -413,9 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; ok && j < n; ++j) {
           const int sv = va.stage;
           const bool more = j + 1 < n;
-          if (C::kOwnP && more)
-            for (int slot = 0; ok && slot < slots; ++slot) ok = scores(j + 1, slot);
-          if (!ok || !(ok = wait_warp(&bars.v_ok[sv], va.phase))) break;
+          if (!(ok = wait_warp(&bars.v_ok[sv], va.phase))) break;
           va.step();
           for (int slot = 0; slot < slots; ++slot) {
             const uint32_t parity = (p_phase >> slot) & 1;
@@ -429,11 +413,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
               pv(slot, sv, 1, j == 0);
               if (!more) mma_commit(&bars.o_full[slot]);
-              else if (C::kOwnP) mma_commit(&bars.p_free[slot]);
               if (slot == slots - 1) mma_commit(&bars.v_empty[sv]);
             }
             __syncwarp();
-            if (!C::kOwnP && more && !(ok = scores(j + 1, slot))) break;
+            if (more && !(ok = scores(j + 1, slot))) break;
           }
         }
       }
@@ -533,9 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = slot * kSlotRows + (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = lanes + slot * 128, o_col = lanes + C::kColO + slot * D;
-    const uint32_t p_col = lanes + C::kColP + slot * C::kStepP;
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    uint32_t s_phase = 0, o_phase = 0, f_phase = 0, unit = 0;
+    uint32_t s_phase = 0, o_phase = 0, unit = 0;
     bool ok = true;
     while (ok && walk.next(p, &u)) {
       const int n = u.t1 - u.t0;
@@ -556,11 +538,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
         tmem_ld_wait();
-        if (C::kOwnP) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.s_free[slot]);
-        }
         if (edge_tile(p, u.tiles, tile)) {
           // bit i of a word: key s0 + i is seen (i <= hi and (i > lo or i < first))
           const int32_t s0 = tile * kTileTc;
@@ -580,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) {
           mx[c] = fmaxf(s[c][0], s[c][1]);
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) mx[c] = fmaxf(mx[c], fmaxf(s[c][i], s[c][i + 1]));
+          for (int i = 2; i < 32; i += 2) mx[c] = max3(mx[c], s[c][i], s[c][i + 1]);
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         float alpha = 1.f;
@@ -588,12 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = exp2_approx(m - top);
           m = top;
           l *= alpha;
-        }
-        if (C::kOwnP && j > 0) {
-          // (else the scores' arrival says that the last tile's products are done)
-          if (!(ok = wait_warp(&bars.p_free[slot], f_phase))) break;
-          f_phase ^= 1;
-          tc_fence_after();
         }
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
@@ -624,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // each); their sum is of the unrounded ones
             w[i] = pack2<T>(a, b);
           }
-          tmem_st32(p_col + c * 32, w);
+          tmem_st32(s_col + c * 32, w);
           // (the second product begins with the first half of the keys)
           tmem_st_wait();
           tc_fence_before();
