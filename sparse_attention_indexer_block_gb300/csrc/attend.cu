@@ -49,30 +49,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Inclusive sum of v over the block's threads; *total gets the sum of all.
-template <int kThreads>
-__device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t w = lane < kThreads / 32 ? warp_sums[lane] : 0;
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, w, d);
-      if (lane >= d) w += o;
-    }
-    warp_sums[lane] = w;
-  }
-  __syncthreads();
-  *total = warp_sums[kThreads / 32 - 1];
-  return v + (warp ? warp_sums[warp - 1] : 0);
-}
-
 // Request of an entry: the last one whose first entry is not past it.
 __device__ __forceinline__ int entry_request(const int32_t* req_entry, int n, int32_t e) {
   int lo = 0, hi = n - 1;
@@ -89,8 +65,8 @@ __device__ __forceinline__ int entry_request(const int32_t* req_entry, int n, in
 // that begins there.
 __device__ int4 cut_at(const AttendParams& p, int c) {
   const int64_t all = p.entry_cost[p.req_entry[p.num_reqs]] * p.num_kv_heads;
-  const int64_t pos = all / p.grid * c + all % p.grid * c / p.grid;
-  if (c >= p.grid || pos >= all) return make_int4(0, 0, 0, p.num_reqs);
+  const int64_t pos = cut_position(p, all, c);
+  if (pos >= all) return make_int4(0, 0, 0, p.num_reqs);
   int lo = 0, hi = p.num_reqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -109,35 +85,6 @@ __device__ int4 cut_at(const AttendParams& p, int c) {
   const int32_t off = static_cast<int32_t>(at - p.entry_cost[a]) - p.unit_overhead;
   return make_int4(a - e0, head, off > 0 ? off : 0, lo);
 }
-
-// The same from the costs of whole requests (cost[b]: exclusive prefix of
-// their units' costs for one kv head), which a CTA of the row-block kernel works
-// out for itself when there are few requests.
-__device__ int4 cut_at_request(const AttendParams& p, const int64_t* cost, int c) {
-  const int64_t all = cost[p.num_reqs] * p.num_kv_heads;
-  const int64_t pos = all / p.grid * c + all % p.grid * c / p.grid;
-  if (c >= p.grid || pos >= all) return make_int4(0, 0, 0, p.num_reqs);
-  int lo = 0, hi = p.num_reqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cost[mid] * p.num_kv_heads <= pos) lo = mid; else hi = mid - 1;
-  }
-  const int64_t one = cost[lo + 1] - cost[lo], rest = pos - cost[lo] * p.num_kv_heads;
-  const int32_t head = static_cast<int32_t>(rest / one);
-  int64_t off = rest % one;
-  const ReqShape r = request_shape(p, lo, false);
-  int32_t u = 0;
-  for (;; ++u) {
-    const int32_t n = unit_tiles(p, r, u).count + p.unit_overhead;
-    if (off < n) break;
-    off -= n;
-  }
-  return make_int4(u, head, static_cast<int32_t>(max(off - p.unit_overhead, int64_t{0})), lo);
-}
-
-// Requests up to which a CTA of the row-block kernel plans for itself: one
-// scan of their lengths, against a launch of the planning kernel (4 us).
-constexpr int kSelfPlanReqs = 512;
 
 // One CTA: entries of the requests, their costs and the CTAs' cuts. Bound by
 // the latency of a few dependent loads and scans.
@@ -189,8 +136,8 @@ __device__ __forceinline__ int32_t selected_tiles(const AttendParams& p) {
   return (p.topk + kTile - 1) / kTile;
 }
 __device__ __forceinline__ int2 selected_cut(const AttendParams& p, int64_t units, int c) {
-  const int64_t cost = selected_tiles(p) + p.unit_overhead, all = units * cost;
-  const int64_t pos = all / p.grid * c + all % p.grid * c / p.grid;
+  const int64_t cost = selected_tiles(p) + p.unit_overhead;
+  const int64_t pos = cut_position(p, units * cost, c);
   const int32_t off = static_cast<int32_t>(pos % cost) - p.unit_overhead;
   return make_int2(static_cast<int32_t>(pos / cost), off > 0 ? off : 0);
 }
@@ -267,32 +214,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   PieceWalk walk;
   if constexpr (!kSel) {
     if (p.self_plan) {
-      int64_t* const cost = reinterpret_cast<int64_t*>(smem);  // [num_reqs + 1]
       __shared__ int64_t sums[32];
       __shared__ int4 cuts[2];
-      constexpr int kThreads = kWarps * 32;
-      int64_t carry = 0, total;
-      for (int b0 = 0; b0 < p.num_reqs; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        int64_t n = 0;
-        if (b < p.num_reqs) {
-          const ReqShape r = request_shape(p, b, cta == 0);
-          const int32_t e = request_entries(p, r);
-          for (int32_t i = 0; i < e; ++i) n += unit_tiles(p, r, i).count + p.unit_overhead;
-        }
-        const int64_t incl = carry + block_scan<kThreads>(n, sums, &total);
-        if (b < p.num_reqs) cost[b + 1] = incl;
-        carry += total;
-      }
-      if (threadIdx.x == 0) cost[0] = 0;
-      __syncthreads();
-      if (threadIdx.x < 2) {
-        const int4 at = cut_at_request(p, cost, cta + threadIdx.x);
-        cuts[threadIdx.x] = at;
-        // (for the join; the last CTA's end too)
-        if (threadIdx.x == 0 || cta == p.grid - 1) p.bound[cta + threadIdx.x] = at;
-      }
-      __syncthreads();
+      self_plan<kWarps * 32>(p, cta, reinterpret_cast<int64_t*>(smem), sums, cuts);
       walk = PieceWalk(cuts[0], cuts[1]);
     } else {
       walk = PieceWalk(p.bound[cta], p.bound[cta + 1]);
@@ -674,13 +598,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
 
 constexpr int kCombineWarps = 4;
 
-// Block (c, y): the unit whose first piece ends CTA c's range, rows 4y .. 4y +
-// 3, a warp each. Only cuts inside a unit leave work; the pieces are joined in
-// the order of the CTAs, so the result does not depend on their timing.
+// Rows that one warp joins: 1 of a row-block kernel's unit, 4 of 256.
+__host__ __device__ constexpr int combine_rows(int32_t rows) { return rows > 64 ? 4 : 1; }
+
+// Block (c, y): the unit whose first piece ends CTA c's range, a warp for
+// combine_rows of its rows. Only cuts inside a unit leave work. The lanes look
+// at 32 following CTAs' cuts at once, then at their pieces' maxima and sums, so
+// that the accumulators' loads do not wait for one another; the pieces are
+// joined in the order of the CTAs, so the result does not depend on timing.
+// Bound by latency: four dependent loads (one token of 8 units over 34 CTAs:
+// TIMING).
 template <typename T, int D, bool kSel>
 __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(const AttendParams p) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+  const int rows = combine_rows(p.rows);
+  const int r0 = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * rows;
   constexpr int kV = D / 32;
   pdl_wait();
   pdl_trigger();
@@ -717,38 +649,61 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(cons
     u.rows = min(p.rows, q.nq * p.group - u.row0);
     u.ahead = 0;
   }
-  if (r >= u.rows) return;
-  float mx = -INFINITY, sum = 0.f, v[kV];
+  for (int r = r0; r < min(r0 + rows, u.rows); ++r) {
+    // the first piece is the last of CTA c, the others the first of theirs
+    const int64_t slot0 = 2 * static_cast<int64_t>(c) + 1;
+    const float2 ml0 = p.part_ml[slot0 * p.rows + r];
+    float mx = ml0.x, sum = ml0.y, v[kV];
+    const float* src0 = p.part_o + (slot0 * p.rows + r) * D + lane * kV;
 #pragma unroll
-  for (int e = 0; e < kV; ++e) v[e] = 0.f;
-  int4 at = next;
-  for (int cc = c; cc < p.grid; ++cc) {
-    // the piece of CTA cc: up to `stop` when that lies in the unit, else to its end
-    const int4 stop = cc == c ? next : cut(cc + 1);
-    const bool in = same(stop, next) && stop.z > 0;
-    if (cc == c || !in || stop.z > at.z) {
-      const int64_t slot = 2 * static_cast<int64_t>(cc) + (cc == c ? 1 : 0);
-      const float2 ml = p.part_ml[slot * p.rows + r];
-      const float* src = p.part_o + (slot * p.rows + r) * D + lane * kV;
-      const float top = fmaxf(mx, ml.x), base = top == -INFINITY ? 0.f : top;
-      const float fa = exp2_approx(mx - base), fb = exp2_approx(ml.x - base);
-      sum = sum * fa + ml.y * fb;
+    for (int e = 0; e < kV; ++e) v[e] = src0[e];
+    for (int c0 = c + 1; c0 < p.grid; c0 += 32) {
+      const int cc = c0 + lane;
+      bool in = false, empty = false;
+      if (cc < p.grid) {
+        const int4 a = cut(cc), b = cut(cc + 1);
+        in = same(a, next) && a.z > 0;
+        empty = same(b, next) && b.z == a.z;
+      }
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      uint32_t full = __ballot_sync(0xffffffffu, in && !empty);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (in && !empty) ml = p.part_ml[2 * static_cast<int64_t>(cc) * p.rows + r];
+      float top = ml.x;
 #pragma unroll
-      for (int e = 0; e < kV; ++e) v[e] = v[e] * fa + src[e] * fb;
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = fmaxf(top, mx);
+      const float base = top == -INFINITY ? 0.f : top;
+      const float keep = exp2_approx(mx - base), f = exp2_approx(ml.x - base);
+      float add = f * ml.y;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+      sum = sum * keep + add;
       mx = top;
-    }
-    if (!in) break;
-    at = stop;
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  int64_t token;
-  int head, pos;
-  row_place(p, u, r, &token, &head, &pos);
-  const int64_t out = token * p.num_heads + head;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + out * D + lane * kV);
 #pragma unroll
-  for (int e = 0; e < kV; e += 2) dst[e / 2] = pack2<T>(v[e] * inv, v[e + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[out] = (mx + log2f(sum)) * kLn2;
+      for (int e = 0; e < kV; ++e) v[e] *= keep;
+      const int n = full ? 32 - __clz(full) : 0;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        if (!(full >> i & 1)) continue;
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        const float* src =
+            p.part_o + (2 * static_cast<int64_t>(c0 + i) * p.rows + r) * D + lane * kV;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) v[e] += w * src[e];
+      }
+      if (all != 0xffffffffu) break;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    int64_t token;
+    int head, pos;
+    row_place(p, u, r, &token, &head, &pos);
+    const int64_t out = token * p.num_heads + head;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + out * D + lane * kV);
+#pragma unroll
+    for (int e = 0; e < kV; e += 2) dst[e / 2] = pack2<T>(v[e] * inv, v[e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[out] = (mx + log2f(sum)) * kLn2;
+  }
 }
 
 template <typename T, int D, int MT, bool kSel>
@@ -771,7 +726,8 @@ idx_status launch_rows_d(const AttendParams& p, int mt, cudaStream_t s) {
 template <typename T, int D>
 idx_status launch_combine_as(const AttendParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, (p.rows + kCombineWarps - 1) / kCombineWarps);
+  const int per_block = kCombineWarps * combine_rows(p.rows);
+  cfg.gridDim = dim3(p.grid, (p.rows + per_block - 1) / per_block);
   cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -785,8 +741,6 @@ idx_status launch_combine_as(const AttendParams& p, cudaStream_t s) {
 }
 
 }  // namespace
-
-int attend_self_plan_reqs() { return kSelfPlanReqs; }
 
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s) {
   return cuda_status(launch_pdl(attend_plan_kernel, 1, kPlanThreads, 0, s, p));

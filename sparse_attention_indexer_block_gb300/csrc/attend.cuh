@@ -52,7 +52,8 @@ struct AttendParams {
   float* part_o;                   // [2 * grid, rows, head_dim] unnormalised pieces
   float2* part_ml;                 // [2 * grid, rows] their maximum and sum
   int32_t max_entries;
-  int32_t self_plan;               // the row-block kernel works `bound` out for itself
+  int32_t self_plan;               // the CTAs work `bound` out for themselves
+  int32_t min_cost;                // least work of a CTA, in tiles
   int32_t grid;                    // CTAs of the row-block launch
   int32_t rows;                    // query rows of a unit
   int32_t tile_log2;               // keys of a tile
@@ -234,6 +235,94 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kTileTc = 128;   // keys of a tensor-memory kernel's tile: two pages
 constexpr int kRowsTc = 256;   // its query rows: two accumulators of 128
 
+// Position of cut c in the sequence of all the work, `all` long: equal shares of
+// at least min_cost for as many CTAs as that allows.
+__device__ __forceinline__ int64_t cut_position(const AttendParams& p, int64_t all, int c) {
+  const int64_t n = max(min(all / p.min_cost, static_cast<int64_t>(p.grid)), int64_t{1});
+  return c >= n ? all : all / n * c + all % n * c / n;
+}
+
+// Inclusive sum of v over the block's threads; *total gets the sum of all.
+template <int kThreads>
+__device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = lane < kThreads / 32 ? warp_sums[lane] : 0;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += o;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  *total = warp_sums[kThreads / 32 - 1];
+  return v + (warp ? warp_sums[warp - 1] : 0);
+}
+
+// The same from the costs of whole requests (cost[b]: exclusive prefix of
+// their units' costs for one kv head), which a CTA works out for itself
+// when there are few requests.
+__device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost, int c) {
+  const int64_t all = cost[p.num_reqs] * p.num_kv_heads;
+  const int64_t pos = cut_position(p, all, c);
+  if (pos >= all) return make_int4(0, 0, 0, p.num_reqs);
+  int lo = 0, hi = p.num_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cost[mid] * p.num_kv_heads <= pos) lo = mid; else hi = mid - 1;
+  }
+  const int64_t one = cost[lo + 1] - cost[lo], rest = pos - cost[lo] * p.num_kv_heads;
+  const int32_t head = static_cast<int32_t>(rest / one);
+  int64_t off = rest % one;
+  const ReqShape r = request_shape(p, lo, false);
+  int32_t u = 0;
+  for (;; ++u) {
+    const int32_t n = unit_tiles(p, r, u).count + p.unit_overhead;
+    if (off < n) break;
+    off -= n;
+  }
+  return make_int4(u, head, static_cast<int32_t>(max(off - p.unit_overhead, int64_t{0})), lo);
+}
+
+// Requests, and entries of each, up to which the CTAs plan for themselves: one
+// scan of the requests' costs each, against a launch of the planning kernel
+// (4 us).
+constexpr int kSelfPlanReqs = 512, kSelfPlanEntries = 8;
+
+// The cuts at both ends of a CTA's range, by its kThreads threads; `cost` has
+// room for num_reqs + 1. p.bound gets them too, for the join.
+template <int kThreads>
+__device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t* sums, int4* cuts) {
+  int64_t carry = 0, total;
+  for (int b0 = 0; b0 < p.num_reqs; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t n = 0;
+    if (b < p.num_reqs) {
+      const ReqShape r = request_shape(p, b, cta == 0);
+      const int32_t e = request_entries(p, r);
+      for (int32_t i = 0; i < e; ++i) n += unit_tiles(p, r, i).count + p.unit_overhead;
+    }
+    const int64_t incl = carry + block_scan<kThreads>(n, sums, &total);
+    if (b < p.num_reqs) cost[b + 1] = incl;
+    carry += total;
+  }
+  if (threadIdx.x == 0) cost[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    const int4 at = cut_at_request(p, cost, cta + threadIdx.x);
+    cuts[threadIdx.x] = at;
+    if (threadIdx.x == 0 || cta == p.grid - 1) p.bound[cta + threadIdx.x] = at;
+  }
+  __syncthreads();
+}
+
 // Raises the kernel's limit of dynamic shared memory, once per device (any host
 // thread; doing it twice is harmless). kRegs: registers a thread that the kernel
 // must have been built with (0: any).
@@ -255,7 +344,6 @@ inline cudaError_t allow_smem(Kernel* kernel, std::atomic<bool>* configured) {
 }
 
 // Launchers.
-int attend_self_plan_reqs();
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s);
 idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, int mt, cudaStream_t s);
 // (the caches' strides have to suit a tensor map: attend_tc_takes)

@@ -49,15 +49,15 @@ AttendWs attend_ws(int64_t num_reqs, int64_t max_entries, int64_t grid, int64_t 
 // How a call is run: query rows per unit, keys per tile, CTAs.
 struct Variant {
   int mt;  // row-block kernel: 16-row blocks per unit; 0: tensor-memory kernel
-  int32_t rows, tile_log2, grid, overhead;
+  int32_t rows, tile_log2, grid, overhead, min_cost;
 };
 
 Variant rows_variant(int64_t rows_per_head) {
   const int mt = rows_per_head <= 16 ? 1 : 2;
-  return Variant{mt, 16 * mt, 6, kRowsCtasPerSm * device_sm_count(), 1};
+  return Variant{mt, 16 * mt, 6, kRowsCtasPerSm * device_sm_count(), 1, 4};
 }
 
-Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 2}; }
+Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 2, 4}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
   size_t most = 0;
@@ -139,6 +139,7 @@ idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& 
                                         v.tile_log2);
   p->grid = v.grid;
   p->unit_overhead = v.overhead;
+  p->min_cost = v.min_cost;
   p->max_entries =
       static_cast<int32_t>(entry_bound(a->num_tokens, a->num_reqs, p->group, v.rows));
   const AttendWs w = attend_ws(a->num_reqs, p->max_entries, v.grid, v.rows, a->head_dim);
@@ -189,7 +190,8 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
-  p.self_plan = !tc && a->num_reqs <= attend_self_plan_reqs() && longest * p.group <= 4 * v.rows;
+  p.self_plan = !tc && a->num_reqs <= kSelfPlanReqs &&
+                longest * p.group <= kSelfPlanEntries * int64_t{v.rows};
   if (!p.self_plan && (st = launch_attend_plan(p, s)) != IDX_OK) return st;
   st = tc ? launch_attend_tc(p, a->head_dim, half, s)
           : launch_attend_rows(p, a->head_dim, half, v.mt, s);
