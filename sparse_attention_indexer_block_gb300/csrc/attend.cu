@@ -10,10 +10,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kWarps = 4;        // of a row-block CTA
-constexpr int kSubKeys = 16;     // keys of a tile that one warp scores
-constexpr int kTile = kWarps * kSubKeys;
 constexpr int kStages = 3;       // sub-tiles in flight per warp
-static_assert(kTile == kPageTokens, "a tile is one page");
 
 // ---------------------------------------------------------------------------
 // small helpers
@@ -133,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
 // Cuts of the selected form, where every unit has the same tiles: unit =
 // (token * head blocks + block) * kv heads + kv head.
 __device__ __forceinline__ int32_t selected_tiles(const AttendParams& p) {
-  return (p.topk + kTile - 1) / kTile;
+  return (p.topk + (1 << p.tile_log2) - 1) >> p.tile_log2;
 }
 __device__ __forceinline__ int2 selected_cut(const AttendParams& p, int64_t units, int c) {
   const int64_t cost = selected_tiles(p) + p.unit_overhead;
@@ -158,7 +155,9 @@ __device__ __forceinline__ int token_request(const AttendParams& p, int32_t t) {
 template <int D, int MT>
 struct RowsCfg {
   static constexpr int kRows = 16 * MT;
-  static constexpr int kStageBytes = 2 * kSubKeys * D * 2;  // K and V
+  static constexpr int kSub = rows_tile_keys(D) / kWarps;  // keys of a warp's sub-tile
+  static constexpr int kSubBytes = kSub * D * 2;           // of K or V: 4 KB
+  static constexpr int kStageBytes = 2 * kSubBytes;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kPad = 4;  // floats between the joined rows, against bank conflicts
@@ -174,8 +173,8 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return r * (D * 2) + ((c ^ (r & 7)) << 4);
 }
 
-// Per unit of 16 * MT query rows of one kv head: the four warps take 16 keys
-// of every 64-key tile each, with a ring of kStages sub-tiles of K and V per
+// Per unit of 16 * MT query rows of one kv head: the four warps take a quarter
+// of every tile's keys each (16 at D = 128, 32 at D = 64), with a ring of kStages sub-tiles of K and V per
 // warp that its own lanes fill with 16-byte asynchronous copies (so no warp
 // waits for another inside a piece), products by mma.sync m16n8k16, running
 // maximum and sum per row; the warps' results are joined through shared memory
@@ -186,6 +185,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   using C = RowsCfg<D, MT>;
   constexpr int kChunks = D / 8;         // 16-byte chunks of a row
   constexpr int kSteps = D / 16;
+  constexpr int kSub = C::kSub, kTiles8 = kSub / 8;  // keys of a sub-tile; 8-key column blocks
+  constexpr int kTile = kWarps * kSub;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
   __shared__ uint32_t s_valid[kWarps][kStages];
@@ -194,8 +195,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   const uint32_t ring = smem_u32(smem) + warp * (kStages * C::kStageBytes);
   uint8_t* q_smem = smem + (C::kSmem - C::kQ);
   const uint32_t q_addr = smem_u32(q_smem);
-  const T* const kbase = static_cast<const T*>(p.k);
-  const T* const vbase = static_cast<const T*>(p.v);
 
   pdl_wait();
   pdl_trigger();
@@ -297,13 +296,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
         l[mt][0] = l[mt][1] = 0.f;
       }
 
-      // ---- copies: where sub-tile j's keys lie is read one (list entries: two)
-      // sub-tiles before its copies are issued
+      // ---- copies: a pass of the warp copies 32 / kChunks rows of K and of V. Where sub-tile
+      // j's keys lie is read one (list entries: two) sub-tiles before its copies are issued.
+      constexpr int kPerPass = 32 / kChunks;
+      const int c = lane % kChunks, h0 = lane / kChunks;
+      // chunk_at of the lane's row and chunk in pass 0; pass i XORs and adds constants
+      const uint32_t lane_at = chunk_at<D>(h0, c);
+      const T* const k_lane = static_cast<const T*>(p.k) + u.head * p.k_stride_head + c * 8;
+      const T* const v_lane = static_cast<const T*>(p.v) + u.head * p.v_stride_head + c * 8;
       const int32_t* const bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
       const int32_t* const list =
           kSel ? p.indices + static_cast<int64_t>(u.q0) * p.indices_stride : nullptr;
+      const int32_t w_lo = max(p_lo, 0) - p.window, w_hi = max(p_hi, 0) - p.window;
+      const auto first_key = [&](int j) -> int32_t { return u.tiles.tile(j) * kTile + warp * kSub; };
       const auto load_index = [&](int j) -> int32_t {
-        const int at = j * kTile + warp * kSubKeys + (lane & 15);
+        const int at = j * kTile + warp * kSub + (lane & (kSub - 1));
         return j < u.t1 && at < p.topk ? list[at] : -1;
       };
       const auto load_page = [&](int j, int32_t idx) -> int32_t {
@@ -311,48 +318,64 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
           if (idx < 0) return -1;
           return idx < p.bt_width * kPageTokens ? bt[idx / kPageTokens] : -1;
         } else {
-          return j < u.t1 ? bt[u.tiles.tile(j)] : 0;
+          if (j >= u.t1) return 0;
+          const int32_t s0 = first_key(j);
+          return s0 <= p_hi ? bt[s0 / kPageTokens] : 0;
         }
       };
       const auto issue = [&](int j, int stage, int32_t idx, int32_t page) {
         if (j < u.t1) {
           const uint32_t dst = ring + stage * C::kStageBytes;
-          const int32_t s0 = kSel ? 0 : u.tiles.tile(j) * kTile + warp * kSubKeys;
-          bool ok;
+          const bool ok = (!kSel || idx >= 0) && page >= 0 && page < p.num_pages;
+          const auto at = [&](int i) -> uint32_t {
+            return dst + i * kPerPass * (D * 2) + (lane_at ^ (((i * kPerPass) & 7) << 4));
+          };
           if constexpr (kSel) {
-            ok = idx >= 0 && page >= 0 && page < p.num_pages;
             if (idx >= 0 && !ok) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
-            const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+            uint32_t valid = __ballot_sync(0xffffffffu, ok);
+            if (kSub < 32) valid &= (1u << (kSub & 31)) - 1;
             if (lane == 0) s_valid[warp][stage] = valid;
-          } else {
-            ok = page >= 0 && page < p.num_pages;
-            if (!ok && s0 <= p_hi) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
-          }
-          constexpr int kKeysPerPass = 32 / kChunks;
-          const int c = lane % kChunks;
+            const int64_t pg = ok ? page : 0;
+            const int32_t tok = ok ? idx & (kPageTokens - 1) : 0;
+            const int64_t k_at = pg * p.k_stride_page + tok * p.k_stride_token;
+            const int64_t v_at = p.same_strides ? k_at : pg * p.v_stride_page + tok * p.v_stride_token;
 #pragma unroll
-          for (int i = 0; i < kSubKeys / kKeysPerPass; ++i) {
-            const int key = i * kKeysPerPass + lane / kChunks;
-            int64_t pg = page;
-            int tok = 0;
-            bool v = ok;
-            if constexpr (kSel) {
-              pg = __shfl_sync(0xffffffffu, page, key);
-              tok = __shfl_sync(0xffffffffu, idx, key) & (kPageTokens - 1);
-              v = __shfl_sync(0xffffffffu, ok, key);
-            } else {
-              const int32_t s = s0 + key;
-              tok = warp * kSubKeys + key;
-              v = ok && s <= p_hi &&
-                  (static_cast<int64_t>(s) > static_cast<int64_t>(p_lo) - p.window || s < p.sinks);
+            for (int i = 0; i < kSub / kPerPass; ++i) {
+              const int key = i * kPerPass + h0;
+              const int64_t ka = __shfl_sync(0xffffffffu, k_at, key);
+              const int64_t va = p.same_strides ? ka : __shfl_sync(0xffffffffu, v_at, key);
+              const bool v = (valid >> key) & 1;
+              cp_async16(at(i), k_lane + ka, v);
+              cp_async16(at(i) + C::kSubBytes, v_lane + va, v);
             }
-            if (!v) pg = 0, tok = 0;
-            const T* kp = kbase + pg * p.k_stride_page + tok * p.k_stride_token +
-                          u.head * p.k_stride_head + c * 8;
-            const T* vp = vbase + pg * p.v_stride_page + tok * p.v_stride_token +
-                          u.head * p.v_stride_head + c * 8;
-            cp_async16(dst + chunk_at<D>(key, c), kp, v);
-            cp_async16(dst + kSubKeys * D * 2 + chunk_at<D>(key, c), vp, v);
+          } else {
+            const int32_t s0 = first_key(j);
+            if (!ok && s0 <= p_hi) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+            const int64_t pg = ok ? page : 0;
+            const int32_t tok = (s0 & (kPageTokens - 1)) + h0;
+            const T* kp = k_lane + (pg * p.k_stride_page + tok * p.k_stride_token);
+            const T* vp = v_lane + (pg * p.v_stride_page + tok * p.v_stride_token);
+            const int64_t k_step = kPerPass * p.k_stride_token, v_step = kPerPass * p.v_stride_token;
+            // (every key of most sub-tiles is one that some row sees)
+            if (ok && s0 + kSub - 1 <= p_hi && (s0 > w_lo || s0 + kSub <= p.sinks)) {
+#pragma unroll
+              for (int i = 0; i < kSub / kPerPass; ++i) {
+                cp_async16(at(i), kp, true);
+                cp_async16(at(i) + C::kSubBytes, vp, true);
+                kp += k_step;
+                vp += v_step;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kSub / kPerPass; ++i) {
+                const int32_t s = s0 + i * kPerPass + h0;
+                const bool v = ok && s <= p_hi && (s > w_lo || s < p.sinks);
+                cp_async16(at(i), kp, v);
+                cp_async16(at(i) + C::kSubBytes, vp, v);
+                kp += k_step;
+                vp += v_step;
+              }
+            }
           }
         }
         cp_commit();
@@ -378,89 +401,113 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) issue_next();
 
+      // ---- fragments: addresses of the 16-key blocks' chunks within a sub-tile, for step & 3
+      const int g = lane >> 3, r7 = lane & 7;
+      uint32_t k_at[4], v_at[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        k_at[q] = chunk_at<D>((g >> 1) * 8 + r7, 2 * q + (g & 1));
+        v_at[q] = C::kSubBytes + chunk_at<D>((g & 1) * 8 + r7, 2 * q + (g >> 1));
+      }
+      const auto sees = [&](int32_t pos, int32_t k) {
+        return k <= pos && (k < p.sinks || pos - k < p.window);
+      };
       int stage = 0;
       for (int j = u.t0; j < u.t1; ++j) {
         cp_wait<kStages - 2>();
         __syncwarp();
         issue_next();  // into the sub-tile that the last round read
-        const int32_t s0 = kSel ? 0 : u.tiles.tile(j) * kTile + warp * kSubKeys;
-        uint32_t valid = 0xffffu;
+        const int32_t s0 = kSel ? 0 : first_key(j);
+        uint32_t valid = 0xffffffffu;
         bool any, all;
         if constexpr (kSel) {
           valid = s_valid[warp][stage];
           any = valid != 0;
-          all = valid == 0xffffu;
+          all = valid == (0xffffffffu >> (32 - kSub));
         } else {
-          const int64_t w_lo = static_cast<int64_t>(p_lo) - p.window;
-          const int64_t w_hi = static_cast<int64_t>(p_hi) - p.window;
-          any = s0 <= p_hi && (s0 + kSubKeys - 1 > w_lo || s0 < p.sinks);
-          all = s0 + kSubKeys - 1 <= p_lo && (s0 > w_hi || s0 + kSubKeys <= p.sinks);
+          any = s0 <= p_hi && (s0 + kSub - 1 > w_lo || s0 < p.sinks);
+          all = s0 + kSub - 1 <= p_lo && (s0 > w_hi || s0 + kSub <= p.sinks);
         }
         if (any) {
-          const uint32_t kt = ring + stage * C::kStageBytes, vt = kt + kSubKeys * D * 2;
-          float s[MT][2][4];
+          const uint32_t kt = ring + stage * C::kStageBytes;
+          // (two sums per block of scores where there are few, to shorten the chain of products)
+          constexpr int kSplit = kTiles8 == 2 ? 2 : 1;
+          float s[kSplit][MT][kTiles8][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int f = 0; f < kSplit; ++f)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+              for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[f][mt][n][e] = 0.f;
 #pragma unroll
           for (int kk = 0; kk < kSteps; ++kk) {
-            uint32_t b[4];
-            const int g = lane >> 3;
-            ldsm4(b, kt + chunk_at<D>((g >> 1) * 8 + (lane & 7), 2 * kk + (g & 1)));
+            uint32_t qa[MT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              uint32_t f[4];
               if constexpr (MT == 1) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = qf[kk][e];
+                for (int e = 0; e < 4; ++e) qa[mt][e] = qf[kk][e];
               } else {
-                q_frag(f, mt, kk);
+                q_frag(qa[mt], mt, kk);
               }
-              mma16816<T>(s[mt][0], f, b[0], b[1]);
-              mma16816<T>(s[mt][1], f, b[2], b[3]);
+            }
+#pragma unroll
+            for (int b = 0; b < kSub / 16; ++b) {
+              uint32_t f[4];
+              ldsm4(f, kt + k_at[kk & 3] + (kk >> 2) * 128 + b * 16 * (D * 2));
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma16816<T>(s[kk % kSplit][mt][2 * b], qa[mt], f[0], f[1]);
+                mma16816<T>(s[kk % kSplit][mt][2 * b + 1], qa[mt], f[2], f[3]);
+              }
             }
           }
-          const auto sees = [&](int32_t pos, int32_t k) {
-            return k <= pos && (k < p.sinks || pos - k < p.window);
-          };
-          uint32_t pa[MT][4];
+          uint32_t pa[MT][kSub / 16][4];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             float alpha[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float x[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the sub-tile, c = lane % 4
+              // the row's scores of keys 8 n + 2 (lane % 4) + e
+              float x[kTiles8][2];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = s[mt][e >> 1][h * 2 + (e & 1)] * p.scale_log2;
+              for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float y = s[0][mt][n][2 * h + e];
+                  if (kSplit == 2) y += s[kSplit - 1][mt][n][2 * h + e];
+                  x[n][e] = y * p.scale_log2;
+                }
               if (!all) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int key = (e >> 1) * 8 + 2 * (lane & 3) + (e & 1);
-                  if (!(kSel ? (valid >> key) & 1 : sees(rpos[mt][h], s0 + key)))
-                    x[e] = -INFINITY;
-                }
+                for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int key = n * 8 + 2 * (lane & 3) + e;
+                    if (!(kSel ? (valid >> key) & 1 : sees(rpos[mt][h], s0 + key)))
+                      x[n][e] = -INFINITY;
+                  }
               }
-              float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+              float mx = fmaxf(x[0][0], x[0][1]);
+#pragma unroll
+              for (int n = 1; n < kTiles8; ++n) mx = max3(mx, x[n][0], x[n][1]);
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              mx = fmaxf(mx, m[mt][h]);
+              mx = max3(mx, __shfl_xor_sync(0xffffffffu, mx, 2), m[mt][h]);
               const float base = mx == -INFINITY ? 0.f : mx;
               alpha[h] = exp2_approx(m[mt][h] - base);
               m[mt][h] = mx;
               float sum = 0.f;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                x[e] = exp2_approx(x[e] - base);
-                sum += x[e];
+              for (int n = 0; n < kTiles8; ++n) {
+                const float a = exp2_approx(x[n][0] - base), b = exp2_approx(x[n][1] - base);
+                sum += a + b;
+                // the weights are rounded to T for the second product (half a step of T each);
+                // their sum is of the unrounded ones
+                pa[mt][n >> 1][2 * (n & 1) + h] = pack2<T>(a, b);
               }
               l[mt][h] = l[mt][h] * alpha[h] + sum;
-              // the weights are rounded to T for the second product (half a step of T each);
-              // their sum is of the unrounded ones
-              pa[mt][h] = pack2<T>(x[0], x[1]);
-              pa[mt][2 + h] = pack2<T>(x[2], x[3]);
             }
             if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
@@ -472,42 +519,46 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
               }
             }
           }
-          const auto v_frag = [&](uint32_t(&b)[4], int cc) {
-            const int g = lane >> 3;
-            ldsm4_t(b, vt + chunk_at<D>((g & 1) * 8 + (lane & 7), 2 * cc + (g >> 1)));
+          const auto v_frag = [&](uint32_t(&f)[4], int b, int cc) {
+            ldsm4_t(f, kt + v_at[cc & 3] + (cc >> 2) * 128 + b * 16 * (D * 2));
           };
           // A key that some rows see and others do not: a weight of 0 times an infinity or NaN
           // would reach the rows that do not, so such values are left out of the product and
-          // added to the rows that see them.
+          // added to the rows that see them. (A list's keys are seen by all rows or none, and
+          // read as zeros where they are seen by none.)
           bool odd = false;
           if (!kSel && !all) {
+#pragma unroll 1
+            for (int b = 0; b < kSub / 16; ++b)
 #pragma unroll
-            for (int cc = 0; cc < kSteps; ++cc) {
-              uint32_t b[4];
-              v_frag(b, cc);
+              for (int cc = 0; cc < kSteps; ++cc) {
+                uint32_t f[4];
+                v_frag(f, b, cc);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) odd |= clear_nonfinite<T>(b[e]) != b[e];
-            }
+                for (int e = 0; e < 4; ++e) odd |= nonfinite_bits<T>(f[e]) != 0;
+              }
             odd = __any_sync(0xffffffffu, odd);
           }
 #pragma unroll
-          for (int cc = 0; cc < kSteps; ++cc) {
-            uint32_t b[4];
-            v_frag(b, cc);
-            if (odd) {
+          for (int b = 0; b < kSub / 16; ++b)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) b[e] = clear_nonfinite<T>(b[e]);
-            }
+            for (int cc = 0; cc < kSteps; ++cc) {
+              uint32_t f[4];
+              v_frag(f, b, cc);
+              if (odd) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma16816<T>(o[mt][2 * cc], pa[mt], b[0], b[1]);
-              mma16816<T>(o[mt][2 * cc + 1], pa[mt], b[2], b[3]);
+                for (int e = 0; e < 4; ++e) f[e] = clear_nonfinite<T>(f[e]);
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma16816<T>(o[mt][2 * cc], pa[mt][b], f[0], f[1]);
+                mma16816<T>(o[mt][2 * cc + 1], pa[mt][b], f[2], f[3]);
+              }
             }
-          }
           if (odd) {
-            const T* v = reinterpret_cast<const T*>(smem + (vt - smem_u32(smem)));
+            const T* v = reinterpret_cast<const T*>(smem + (kt + C::kSubBytes - smem_u32(smem)));
 #pragma unroll 1
-            for (int key = 0; key < kSubKeys; ++key)
+            for (int key = 0; key < kSub; ++key)
 #pragma unroll
               for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -718,9 +769,8 @@ idx_status launch_rows_as(const AttendParams& p, cudaStream_t s) {
 
 template <typename T, int D>
 idx_status launch_rows_d(const AttendParams& p, int mt, cudaStream_t s) {
-  if (p.indices)
-    return mt == 1 ? launch_rows_as<T, D, 1, true>(p, s) : launch_rows_as<T, D, 2, true>(p, s);
-  return mt == 1 ? launch_rows_as<T, D, 1, false>(p, s) : launch_rows_as<T, D, 2, false>(p, s);
+  if (!p.indices) return launch_rows_as<T, D, 1, false>(p, s);
+  return mt == 1 ? launch_rows_as<T, D, 1, true>(p, s) : launch_rows_as<T, D, 2, true>(p, s);
 }
 
 template <typename T, int D>

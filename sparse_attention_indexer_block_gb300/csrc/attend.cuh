@@ -37,6 +37,7 @@ struct AttendParams {
   const int32_t* indices;          // [num_tokens, topk] (selected form), else nullptr
   int64_t indices_stride;
   int32_t topk;
+  int32_t same_strides;            // K's and V's pages and tokens lie alike (selected form)
   int32_t num_reqs, num_tokens;
   int32_t num_heads, num_kv_heads, group;
   float scale_log2;                // scale * log2(e)
@@ -200,6 +201,14 @@ __device__ __forceinline__ uint32_t clear_nonfinite(uint32_t v) {
   return v;
 }
 
+// Bits of v whose 16-bit halves are infinities or NaNs (their top bits, else 0).
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t v) {
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr uint32_t kExp = kHalf ? 0x7c007c00u : 0x7f807f80u;
+  return ((v & kExp) + (kHalf ? 0x04000400u : 0x00800080u)) & 0x80008000u;
+}
+
 // Two fp32 values as a pair of T, the first in the low half.
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -218,6 +227,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 16 bytes, asynchronously; `valid` false: zeros, and src is not read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;
@@ -231,6 +246,9 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 constexpr float kLn2 = 0.693147180559945309f;
+
+// Keys of a tile of the row-block kernel: 4 KB of K per warp either way.
+__host__ __device__ constexpr int rows_tile_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
 
 constexpr int kTileTc = 128;   // keys of a tensor-memory kernel's tile: two pages
 constexpr int kRowsTc = 256;   // its query rows: two accumulators of 128

@@ -52,16 +52,16 @@ struct Variant {
   int32_t rows, tile_log2, grid, overhead, min_cost;
 };
 
-Variant rows_variant(int64_t rows_per_head) {
-  const int mt = rows_per_head <= 16 ? 1 : 2;
-  return Variant{mt, 16 * mt, 6, kRowsCtasPerSm * device_sm_count(), 1, 4};
+Variant rows_variant(int mt, int head_dim) {
+  return Variant{mt, 16 * mt, rows_tile_keys(head_dim) == 64 ? 6 : 7,
+                 kRowsCtasPerSm * device_sm_count(), 1, 4};
 }
 
 Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 2, 4}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
   size_t most = 0;
-  for (const Variant& v : {rows_variant(1), rows_variant(17), tc_variant()}) {
+  for (const Variant& v : {rows_variant(1, head_dim), rows_variant(2, head_dim), tc_variant()}) {
     const size_t n = attend_ws(num_reqs, entry_bound(num_tokens, num_reqs, group, v.rows), v.grid,
                                v.rows, head_dim)
                          .total;
@@ -185,8 +185,11 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
     p.sinks = a->sinks;
   }
   const int64_t longest = a->max_query_len > 0 ? a->max_query_len : a->num_tokens;
-  const bool tc = longest * p.group > 32 && attend_tc_takes(p, a->head_dim);
-  const Variant v = tc ? tc_variant() : rows_variant(longest * p.group);
+  // The row-block kernel holds 16 rows at once and reads K and V again for the next 16; from
+  // 17 rows on the tensor-memory kernel is faster (24 requests of 8000 keys, 8 kv heads of 128:
+  // 15 rows 132 against 140 us, 20 rows 173 against 142).
+  const bool tc = longest * p.group > 16 && attend_tc_takes(p, a->head_dim);
+  const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
@@ -209,7 +212,8 @@ idx_status indexer_attend_selected(const idx_attend* a, void* stream) {
   p.indices = a->indices;
   p.indices_stride = a->indices_stride;
   p.topk = a->topk;
-  const Variant v = rows_variant(p.group);
+  p.same_strides = p.k_stride_page == p.v_stride_page && p.k_stride_token == p.v_stride_token;
+  const Variant v = rows_variant(p.group <= 16 ? 1 : 2, a->head_dim);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;

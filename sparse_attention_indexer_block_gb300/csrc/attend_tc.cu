@@ -124,12 +124,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t v;
@@ -180,14 +174,6 @@ __device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles
 // The n lowest bits of a word, n clamped to [0, 32].
 __device__ __forceinline__ uint32_t low_bits(int32_t n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
-}
-
-// Bits of v whose 16-bit halves are infinities or NaNs (their top bits, else 0).
-template <typename T>
-__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t v) {
-  constexpr bool kHalf = std::is_same<T, __half>::value;
-  constexpr uint32_t kExp = kHalf ? 0x7c007c00u : 0x7f807f80u;
-  return ((v & kExp) + (kHalf ? 0x04000400u : 0x00800080u)) & 0x80008000u;
 }
 
 // The infinities and NaNs that were left out of the edge tiles' products, for
