@@ -144,6 +144,9 @@ __device__ __forceinline__ int64_t selected_units(const AttendParams& p) {
 
 // Request of a token row, or -1 when it lies in none.
 __device__ __forceinline__ int token_request(const AttendParams& p, int32_t t) {
+  // (equal numbers of tokens per request: two loads side by side instead of a chain)
+  const int guess = static_cast<int>(static_cast<int64_t>(t) * p.num_reqs / p.num_tokens);
+  if (p.query_start_loc[guess] <= t && t < p.query_start_loc[guess + 1]) return guess;
   int lo = 0, hi = p.num_reqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
 
   // this CTA's range of the units
   int64_t unit = 0, unit_end = 0;
-  int32_t first_tile = 0, last_tile = 0;
+  int32_t first_tile = 0, last_tile = 0, req_token = -1, req = -1;
   if constexpr (kSel) {
     const int64_t units = selected_units(p);
     const int2 a = selected_cut(p, units, cta), b = selected_cut(p, units, cta + 1);
@@ -235,7 +238,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       u.rows = min(p.rows, p.group - u.row0);
       u.q0 = token;
       u.ahead = 0;
-      u.req = token_request(p, token);
+      if (token != req_token) {
+        req = token_request(p, token);
+        req_token = token;
+      }
+      u.req = req;
       u.tiles = UnitTiles{0, 0, selected_tiles(p), 0, 0};
       u.t0 = first_tile;
       u.t1 = last ? last_tile : u.tiles.count;
@@ -248,30 +255,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
 
     if (!kSel || u.req >= 0) {
       const int32_t p_lo = u.tiles.p_lo, p_hi = u.tiles.p_hi;
-      // ---- queries: shared memory, then fragments
-      for (int i = threadIdx.x; i < C::kRows * kChunks; i += kWarps * 32) {
-        const int r = i / kChunks, c = i % kChunks;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < u.rows) {
-          int64_t token;
-          int head, pos;
-          row_place(p, u, r, &token, &head, &pos);
-          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                              token * p.q_stride_token + head * p.q_stride_head +
-                                              c * 8);
-        }
-        *reinterpret_cast<uint4*>(q_smem + chunk_at<D>(r, c)) = v;
-      }
-      __syncthreads();
-      uint32_t qf[MT == 1 ? kSteps : 1][4];
-      const auto q_frag = [&](uint32_t(&f)[4], int mt, int kk) {
-        const int m = lane >> 3, r = mt * 16 + (m & 1) * 8 + (lane & 7);
-        ldsm4(f, q_addr + chunk_at<D>(r, 2 * kk + (m >> 1)));
-      };
-      if constexpr (MT == 1) {
-#pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) q_frag(qf[kk], 0, kk);
-      }
       int32_t rpos[MT][2];  // positions of this thread's rows
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -400,6 +383,31 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       };
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) issue_next();
+
+      // ---- queries (the first keys are on their way): shared memory, then fragments
+      for (int i = threadIdx.x; i < C::kRows * kChunks; i += kWarps * 32) {
+        const int r = i / kChunks, c = i % kChunks;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < u.rows) {
+          int64_t token;
+          int head, pos;
+          row_place(p, u, r, &token, &head, &pos);
+          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                              token * p.q_stride_token + head * p.q_stride_head +
+                                              c * 8);
+        }
+        *reinterpret_cast<uint4*>(q_smem + chunk_at<D>(r, c)) = v;
+      }
+      __syncthreads();
+      uint32_t qf[MT == 1 ? kSteps : 1][4];
+      const auto q_frag = [&](uint32_t(&f)[4], int mt, int kk) {
+        const int m = lane >> 3, r = mt * 16 + (m & 1) * 8 + (lane & 7);
+        ldsm4(f, q_addr + chunk_at<D>(r, 2 * kk + (m >> 1)));
+      };
+      if constexpr (MT == 1) {
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) q_frag(qf[kk], 0, kk);
+      }
 
       // ---- fragments: addresses of the 16-key blocks' chunks within a sub-tile, for step & 3
       const int g = lane >> 3, r7 = lane & 7;
