@@ -62,7 +62,7 @@ __device__ __forceinline__ int entry_request(const int32_t* req_entry, int n, in
 // that begins there.
 __device__ int4 cut_at(const AttendParams& p, int c) {
   const int64_t all = p.entry_cost[p.req_entry[p.num_reqs]] * p.num_kv_heads;
-  const int64_t pos = cut_position(p, all, c);
+  const int64_t pos = cut_position(all, cutters(p, all, 0), c);
   if (pos >= all) return make_int4(0, 0, 0, p.num_reqs);
   int lo = 0, hi = p.num_reqs - 1;
   while (lo < hi) {
@@ -72,8 +72,8 @@ __device__ int4 cut_at(const AttendParams& p, int c) {
   const int32_t e0 = p.req_entry[lo], e1 = p.req_entry[lo + 1];
   const int64_t base = p.entry_cost[e0], cost = p.entry_cost[e1] - base;
   const int64_t rest = pos - base * p.num_kv_heads;
-  const int32_t head = static_cast<int32_t>(rest / cost);
-  const int64_t at = base + rest % cost;
+  const int32_t head = static_cast<int32_t>(quotient(rest, cost));
+  const int64_t at = base + rest - head * cost;
   int32_t a = e0, b = e1 - 1;
   while (a < b) {
     const int32_t mid = (a + b + 1) >> 1;
@@ -134,9 +134,10 @@ __device__ __forceinline__ int32_t selected_tiles(const AttendParams& p) {
 }
 __device__ __forceinline__ int2 selected_cut(const AttendParams& p, int64_t units, int c) {
   const int64_t cost = selected_tiles(p) + p.unit_overhead;
-  const int64_t pos = cut_position(p, units * cost, c);
-  const int32_t off = static_cast<int32_t>(pos % cost) - p.unit_overhead;
-  return make_int2(static_cast<int32_t>(pos / cost), off > 0 ? off : 0);
+  const int64_t all = units * cost, pos = cut_position(all, cutters(p, all, units), c);
+  const int64_t unit = quotient(pos, cost);
+  const int32_t off = static_cast<int32_t>(pos - unit * cost) - p.unit_overhead;
+  return make_int2(static_cast<int32_t>(unit), off > 0 ? off : 0);
 }
 __device__ __forceinline__ int64_t selected_units(const AttendParams& p) {
   return static_cast<int64_t>(p.num_tokens) * ((p.group + p.rows - 1) / p.rows) * p.num_kv_heads;
@@ -218,8 +219,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
     if (p.self_plan) {
       __shared__ int64_t sums[32];
       __shared__ int4 cuts[2];
-      self_plan<kWarps * 32>(p, cta, reinterpret_cast<int64_t*>(smem), sums, cuts);
-      walk = PieceWalk(cuts[0], cuts[1]);
+      __shared__ ReqShape first;
+      self_plan<kWarps * 32>(p, cta, reinterpret_cast<int64_t*>(smem), sums, cuts, &first);
+      walk = PieceWalk(p, cuts[0], cuts[1], first);
     } else {
       walk = PieceWalk(p.bound[cta], p.bound[cta + 1]);
     }
@@ -667,12 +669,12 @@ __host__ __device__ constexpr int combine_rows(int32_t rows) { return rows > 64 
 // joined in the order of the CTAs, so the result does not depend on timing.
 // Bound by latency: four dependent loads (one token of 8 units over 34 CTAs:
 // TIMING).
-template <typename T, int D, bool kSel>
+template <typename T, int D, bool kSel, int kRows>
 __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(const AttendParams p) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int rows = combine_rows(p.rows);
-  const int r0 = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * rows;
+  const int r0 = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * kRows;
   constexpr int kV = D / 32;
+  using Vec = typename std::conditional<kV == 4, float4, float2>::type;
   pdl_wait();
   pdl_trigger();
   Piece u;
@@ -708,60 +710,89 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(cons
     u.rows = min(p.rows, q.nq * p.group - u.row0);
     u.ahead = 0;
   }
-  for (int r = r0; r < min(r0 + rows, u.rows); ++r) {
-    // the first piece is the last of CTA c, the others the first of theirs
-    const int64_t slot0 = 2 * static_cast<int64_t>(c) + 1;
-    const float2 ml0 = p.part_ml[slot0 * p.rows + r];
-    float mx = ml0.x, sum = ml0.y, v[kV];
-    const float* src0 = p.part_o + (slot0 * p.rows + r) * D + lane * kV;
+  if (r0 >= u.rows) return;
+  // (rows past the unit's last are worked out from the last one's and not written)
+  const auto row_of = [&](int k) { return min(r0 + k, u.rows - 1); };
+  const auto piece = [&](int64_t slot, int k) {
+    return *reinterpret_cast<const Vec*>(p.part_o + (slot * p.rows + row_of(k)) * D + lane * kV);
+  };
+  // the first piece is the last of CTA c, the others the first of theirs
+  const int64_t slot0 = 2 * static_cast<int64_t>(c) + 1;
+  float mx[kRows], sum[kRows], v[kRows][kV];
 #pragma unroll
-    for (int e = 0; e < kV; ++e) v[e] = src0[e];
-    for (int c0 = c + 1; c0 < p.grid; c0 += 32) {
-      const int cc = c0 + lane;
-      bool in = false, empty = false;
-      if (cc < p.grid) {
-        const int4 a = cut(cc), b = cut(cc + 1);
-        in = same(a, next) && a.z > 0;
-        empty = same(b, next) && b.z == a.z;
-      }
-      const uint32_t all = __ballot_sync(0xffffffffu, in);
-      uint32_t full = __ballot_sync(0xffffffffu, in && !empty);
+  for (int k = 0; k < kRows; ++k) {
+    const float2 ml = p.part_ml[slot0 * p.rows + row_of(k)];
+    const Vec x = piece(slot0, k);
+    mx[k] = ml.x;
+    sum[k] = ml.y;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) v[k][e] = reinterpret_cast<const float*>(&x)[e];
+  }
+  for (int c0 = c + 1; c0 < p.grid; c0 += 32) {
+    const int cc = c0 + lane;
+    bool in = false, empty = false;
+    if (cc < p.grid) {
+      const int4 a = cut(cc), b = cut(cc + 1);
+      in = same(a, next) && a.z > 0;
+      empty = same(b, next) && b.z == a.z;
+    }
+    const uint32_t all = __ballot_sync(0xffffffffu, in);
+    const uint32_t full = __ballot_sync(0xffffffffu, in && !empty);
+    float f[kRows];  // the lane's piece's factors
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (in && !empty) ml = p.part_ml[2 * static_cast<int64_t>(cc) * p.rows + r];
+      if (in && !empty) ml = p.part_ml[2 * static_cast<int64_t>(cc) * p.rows + row_of(k)];
       float top = ml.x;
 #pragma unroll
       for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      top = fmaxf(top, mx);
+      top = fmaxf(top, mx[k]);
       const float base = top == -INFINITY ? 0.f : top;
-      const float keep = exp2_approx(mx - base), f = exp2_approx(ml.x - base);
-      float add = f * ml.y;
+      const float keep = exp2_approx(mx[k] - base);
+      f[k] = exp2_approx(ml.x - base);
+      float add = f[k] * ml.y;
 #pragma unroll
       for (int d = 16; d; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
-      sum = sum * keep + add;
-      mx = top;
+      sum[k] = sum[k] * keep + add;
+      mx[k] = top;
 #pragma unroll
-      for (int e = 0; e < kV; ++e) v[e] *= keep;
-      const int n = full ? 32 - __clz(full) : 0;
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        if (!(full >> i & 1)) continue;
-        const float w = __shfl_sync(0xffffffffu, f, i);
-        const float* src =
-            p.part_o + (2 * static_cast<int64_t>(c0 + i) * p.rows + r) * D + lane * kV;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) v[e] += w * src[e];
-      }
-      if (all != 0xffffffffu) break;
+      for (int e = 0; e < kV; ++e) v[k][e] *= keep;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int n = full ? 32 - __clz(full) : 0;
+    // the loads of several pieces side by side (where there is none: the first again, unused)
+    constexpr int kAtOnce = 8 / kRows;
+    for (int i = 0; i < n; i += kAtOnce) {
+      Vec x[kAtOnce][kRows];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a)
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+          x[a][k] = piece(full >> (i + a) & 1 ? 2 * static_cast<int64_t>(c0 + i + a) : slot0, k);
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a)
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const float w = __shfl_sync(0xffffffffu, f[k], i + a);
+          if (full >> (i + a) & 1) {
+#pragma unroll
+            for (int e = 0; e < kV; ++e) v[k][e] += w * reinterpret_cast<const float*>(&x[a][k])[e];
+          }
+        }
+    }
+    if (all != 0xffffffffu) break;
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (r0 + k >= u.rows) break;
+    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
     int64_t token;
     int head, pos;
-    row_place(p, u, r, &token, &head, &pos);
+    row_place(p, u, r0 + k, &token, &head, &pos);
     const int64_t out = token * p.num_heads + head;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + out * D + lane * kV);
 #pragma unroll
-    for (int e = 0; e < kV; e += 2) dst[e / 2] = pack2<T>(v[e] * inv, v[e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[out] = (mx + log2f(sum)) * kLn2;
+    for (int e = 0; e < kV; e += 2) dst[e / 2] = pack2<T>(v[k][e] * inv, v[k][e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[out] = (mx[k] + log2f(sum[k])) * kLn2;
   }
 }
 
@@ -793,9 +824,10 @@ idx_status launch_combine_as(const AttendParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(p.indices
-                         ? cudaLaunchKernelEx(&cfg, attend_combine_kernel<T, D, true>, p)
-                         : cudaLaunchKernelEx(&cfg, attend_combine_kernel<T, D, false>, p));
+  const auto kernel = p.indices                  ? attend_combine_kernel<T, D, true, 1>
+                      : combine_rows(p.rows) > 1 ? attend_combine_kernel<T, D, false, 4>
+                                                 : attend_combine_kernel<T, D, false, 1>;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 }  // namespace

@@ -154,6 +154,11 @@ struct PieceWalk {
   PieceWalk() = default;
   __device__ __forceinline__ PieceWalk(const int4& from, const int4& to)
       : cur(from), end(to), done(false), stale(true) {}
+  // with the first request's shape at hand
+  __device__ __forceinline__ PieceWalk(const AttendParams& p, const int4& from, const int4& to,
+                                       const ReqShape& first)
+      : cur(from), end(to), shape(first), entries(request_entries(p, first)), done(false),
+        stale(false) {}
 
   __device__ __forceinline__ bool next(const AttendParams& p, Piece* u) {
     if (done || cur.w >= p.num_reqs) return false;
@@ -253,11 +258,28 @@ __host__ __device__ constexpr int rows_tile_keys(int head_dim) { return head_dim
 constexpr int kTileTc = 128;   // keys of a tensor-memory kernel's tile: two pages
 constexpr int kRowsTc = 256;   // its query rows: two accumulators of 128
 
-// Position of cut c in the sequence of all the work, `all` long: equal shares of
-// at least min_cost for as many CTAs as that allows.
-__device__ __forceinline__ int64_t cut_position(const AttendParams& p, int64_t all, int c) {
-  const int64_t n = max(min(all / p.min_cost, static_cast<int64_t>(p.grid)), int64_t{1});
-  return c >= n ? all : all / n * c + all % n * c / n;
+// a / b for a >= 0, b > 0, in 32 bits where both fit (a fifth of the time).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// CTAs that take part in work of cost `all` in `units` units: as many as have
+// min_cost each, and where it costs at most a quarter of them, a number that
+// cuts equal units alike or not at all (a cut costs a join, a CTA's second piece
+// 7 us without copies in flight).
+__device__ __forceinline__ int64_t cutters(const AttendParams& p, int64_t all, int64_t units) {
+  const int64_t most = max(min(quotient(all, p.min_cost), static_cast<int64_t>(p.grid)), int64_t{1});
+  if (units < 1 || units > most) return most;
+  const int64_t n = quotient(most, units) * units;
+  return 4 * n >= 3 * most ? n : most;
+}
+
+// Position of cut c of n.
+__device__ __forceinline__ int64_t cut_position(int64_t all, int64_t n, int c) {
+  if (c >= n) return all;
+  const int64_t q = quotient(all, n);
+  return q * c + quotient((all - q * n) * c, n);
 }
 
 // Inclusive sum of v over the block's threads; *total gets the sum of all.
@@ -287,9 +309,10 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
 // The same from the costs of whole requests (cost[b]: exclusive prefix of
 // their units' costs for one kv head), which a CTA works out for itself
 // when there are few requests.
-__device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost, int c) {
-  const int64_t all = cost[p.num_reqs] * p.num_kv_heads;
-  const int64_t pos = cut_position(p, all, c);
+__device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost, int64_t units,
+                                      int c) {
+  const int64_t all = cost[p.num_reqs] * p.num_kv_heads, n = cutters(p, all, units);
+  const int64_t pos = cut_position(all, n, c);
   if (pos >= all) return make_int4(0, 0, 0, p.num_reqs);
   int lo = 0, hi = p.num_reqs - 1;
   while (lo < hi) {
@@ -297,16 +320,31 @@ __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost
     if (cost[mid] * p.num_kv_heads <= pos) lo = mid; else hi = mid - 1;
   }
   const int64_t one = cost[lo + 1] - cost[lo], rest = pos - cost[lo] * p.num_kv_heads;
-  const int32_t head = static_cast<int32_t>(rest / one);
-  int64_t off = rest % one;
+  int32_t head = static_cast<int32_t>(quotient(rest, one));
+  int64_t off = rest - head * one;
   const ReqShape r = request_shape(p, lo, false);
-  int32_t u = 0;
+  int32_t u = 0, tiles;
   for (;; ++u) {
-    const int32_t n = unit_tiles(p, r, u).count + p.unit_overhead;
-    if (off < n) break;
-    off -= n;
+    tiles = unit_tiles(p, r, u).count;
+    if (off < tiles + p.unit_overhead) break;
+    off -= tiles + p.unit_overhead;
   }
-  return make_int4(u, head, static_cast<int32_t>(max(off - p.unit_overhead, int64_t{0})), lo);
+  // a cut near a unit's end moves there (by at most a sixteenth of a CTA's work)
+  int32_t t = static_cast<int32_t>(max(off - p.unit_overhead, int64_t{0}));
+  const int64_t near = quotient(all, n) / 16;
+  if (t <= near) t = 0;
+  if (t > 0 && tiles - t <= near) {
+    t = 0;
+    if (++u == request_entries(p, r)) {
+      u = 0;
+      if (++head == p.num_kv_heads) {
+        head = 0;
+        do ++lo;
+        while (lo < p.num_reqs && cost[lo + 1] == cost[lo]);
+      }
+    }
+  }
+  return make_int4(u, head, t, lo);
 }
 
 // Requests, and entries of each, up to which the CTAs plan for themselves: one
@@ -314,10 +352,12 @@ __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost
 // (4 us).
 constexpr int kSelfPlanReqs = 512, kSelfPlanEntries = 8;
 
-// The cuts at both ends of a CTA's range, by its kThreads threads; `cost` has
-// room for num_reqs + 1. p.bound gets them too, for the join.
+// The cuts at both ends of a CTA's range and its first request's shape, by its
+// kThreads threads; `cost` has room for num_reqs + 1. p.bound gets them too, for the join.
 template <int kThreads>
-__device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t* sums, int4* cuts) {
+__device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t* sums, int4* cuts,
+                          ReqShape* first) {
+  constexpr int kEntryShift = 40;  // one scan for both sums: costs below, entries above
   int64_t carry = 0, total;
   for (int b0 = 0; b0 < p.num_reqs; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
@@ -326,16 +366,19 @@ __device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t
       const ReqShape r = request_shape(p, b, cta == 0);
       const int32_t e = request_entries(p, r);
       for (int32_t i = 0; i < e; ++i) n += unit_tiles(p, r, i).count + p.unit_overhead;
+      n += static_cast<int64_t>(e) << kEntryShift;
     }
     const int64_t incl = carry + block_scan<kThreads>(n, sums, &total);
-    if (b < p.num_reqs) cost[b + 1] = incl;
+    if (b < p.num_reqs) cost[b + 1] = incl & ((int64_t{1} << kEntryShift) - 1);
     carry += total;
   }
+  const int64_t units = (carry >> kEntryShift) * p.num_kv_heads;
   if (threadIdx.x == 0) cost[0] = 0;
   __syncthreads();
   if (threadIdx.x < 2) {
-    const int4 at = cut_at_request(p, cost, cta + threadIdx.x);
+    const int4 at = cut_at_request(p, cost, units, cta + threadIdx.x);
     cuts[threadIdx.x] = at;
+    if (threadIdx.x == 0 && at.w < p.num_reqs) *first = request_shape(p, at.w, false);
     if (threadIdx.x == 0 || cta == p.grid - 1) p.bound[cta + threadIdx.x] = at;
   }
   __syncthreads();

@@ -52,16 +52,18 @@ struct Variant {
   int32_t rows, tile_log2, grid, overhead, min_cost;
 };
 
-Variant rows_variant(int mt, int head_dim) {
+// (At least two tiles a CTA; four with a list: 64-key tiles, one token over 1000 keys 12.7 us
+// with four, 11.5 with two; lists of 512 11.5 and 13.4, where four leaves them uncut.)
+Variant rows_variant(int mt, int head_dim, bool selected) {
   return Variant{mt, 16 * mt, rows_tile_keys(head_dim) == 64 ? 6 : 7,
-                 kRowsCtasPerSm * device_sm_count(), 1, 4};
+                 kRowsCtasPerSm * device_sm_count(), 1, selected ? 4 : 2};
 }
 
 Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 2, 4}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
   size_t most = 0;
-  for (const Variant& v : {rows_variant(1, head_dim), rows_variant(2, head_dim), tc_variant()}) {
+  for (const Variant& v : {rows_variant(1, head_dim, true), rows_variant(2, head_dim, true), tc_variant()}) {
     const size_t n = attend_ws(num_reqs, entry_bound(num_tokens, num_reqs, group, v.rows), v.grid,
                                v.rows, head_dim)
                          .total;
@@ -189,7 +191,7 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
   // 17 rows on the tensor-memory kernel is faster (24 requests of 8000 keys, 8 kv heads of 128:
   // 15 rows 132 against 140 us, 20 rows 173 against 142).
   const bool tc = longest * p.group > 16 && attend_tc_takes(p, a->head_dim);
-  const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim);
+  const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim, false);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
@@ -213,7 +215,7 @@ idx_status indexer_attend_selected(const idx_attend* a, void* stream) {
   p.indices_stride = a->indices_stride;
   p.topk = a->topk;
   p.same_strides = p.k_stride_page == p.v_stride_page && p.k_stride_token == p.v_stride_token;
-  const Variant v = rows_variant(p.group <= 16 ? 1 : 2, a->head_dim);
+  const Variant v = rows_variant(p.group <= 16 ? 1 : 2, a->head_dim, true);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
