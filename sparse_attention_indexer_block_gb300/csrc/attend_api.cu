@@ -59,7 +59,7 @@ Variant rows_variant(int mt, int head_dim, bool selected) {
                  kRowsCtasPerSm * device_sm_count(), 1, selected ? 4 : 2};
 }
 
-Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 2, 4}; }
+Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 3, 4}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
   size_t most = 0;

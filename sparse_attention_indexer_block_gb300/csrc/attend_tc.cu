@@ -258,7 +258,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
+  // All of tensor memory is this block's, so it begins at address 0 (a constant makes the
+  // products' issue cheaper).
+  constexpr uint32_t tmem = 0;
+  if (bars.tmem_base != 0) {
+    if (threadIdx.x == 0) set_error(p.dev_error, IDX_DEV_INTERNAL);
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(bars.tmem_base, kTmemCols);
+    return;
+  }
   pdl_wait();
   pdl_trigger();
   PieceWalk walk(p.bound[blockIdx.x], p.bound[blockIdx.x + 1]);
@@ -553,7 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= alpha;
         }
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
+          // (rare: short code, which would push the rest out of the instruction cache)
+#pragma unroll(D == 128 ? 1 : 2)
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
             tmem_ld32(o_col + c * 32, o);
