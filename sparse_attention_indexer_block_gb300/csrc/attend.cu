@@ -177,6 +177,168 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return r * (D * 2) + ((c ^ (r & 7)) << 4);
 }
 
+// Whether the token at pos sees key k.
+__device__ __forceinline__ bool sees(const AttendParams& p, int32_t pos, int32_t k) {
+  return k <= pos && (k < p.sinks || pos - k < p.window);
+}
+
+// One sub-tile of kSub keys (K at shared address kt, V kSubBytes on) against 16
+// * MT query rows by one warp: scores, running maxima m and sums l, and the
+// accumulators o. k_at, v_at: the lane's fragment addresses within a 16-key
+// block for step & 3; q_of(f, mt, kk): query fragments; valid: bit per key (a
+// list's); all: every row sees every key; s0: the first key's position; rpos: the
+// positions of the lane's rows.
+template <typename T, int D, int MT, bool kSel, typename QOf>
+__device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8_t* smem, uint32_t kt,
+                                              const uint32_t (&k_at)[4], const uint32_t (&v_at)[4],
+                                              const QOf& q_of, uint32_t valid, bool all, int32_t s0,
+                                              const int32_t (&rpos)[MT][2],
+                                              float (&o)[MT][D / 8][4], float (&m)[MT][2],
+                                              float (&l)[MT][2]) {
+  using C = RowsCfg<D, MT>;
+  constexpr int kSteps = D / 16, kSub = C::kSub, kTiles8 = kSub / 8;  // 8-key column blocks
+  const int lane = threadIdx.x & 31;
+  // (two sums per block of scores where there are few, to shorten the chain of products)
+  constexpr int kSplit = kTiles8 == 2 ? 2 : 1;
+  float s[kSplit][MT][kTiles8][4];
+#pragma unroll
+  for (int f = 0; f < kSplit; ++f)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[f][mt][n][e] = 0.f;
+#pragma unroll
+  for (int kk = 0; kk < kSteps; ++kk) {
+    uint32_t qa[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      q_of(qa[mt], mt, kk);
+    }
+#pragma unroll
+    for (int b = 0; b < kSub / 16; ++b) {
+      uint32_t f[4];
+      ldsm4(f, kt + k_at[kk & 3] + (kk >> 2) * 128 + b * 16 * (D * 2));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma16816<T>(s[kk % kSplit][mt][2 * b], qa[mt], f[0], f[1]);
+        mma16816<T>(s[kk % kSplit][mt][2 * b + 1], qa[mt], f[2], f[3]);
+      }
+    }
+  }
+  uint32_t pa[MT][kSub / 16][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float alpha[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the row's scores of keys 8 n + 2 (lane % 4) + e
+      float x[kTiles8][2];
+#pragma unroll
+      for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = s[0][mt][n][2 * h + e];
+          if (kSplit == 2) y += s[kSplit - 1][mt][n][2 * h + e];
+          x[n][e] = y * p.scale_log2;
+        }
+      if (!all) {
+#pragma unroll
+        for (int n = 0; n < kTiles8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = n * 8 + 2 * (lane & 3) + e;
+            if (!(kSel ? (valid >> key) & 1 : sees(p, rpos[mt][h], s0 + key)))
+              x[n][e] = -INFINITY;
+          }
+      }
+      float mx = fmaxf(x[0][0], x[0][1]);
+#pragma unroll
+      for (int n = 1; n < kTiles8; ++n) mx = max3(mx, x[n][0], x[n][1]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max3(mx, __shfl_xor_sync(0xffffffffu, mx, 2), m[mt][h]);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      alpha[h] = exp2_approx(m[mt][h] - base);
+      m[mt][h] = mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < kTiles8; ++n) {
+        const float a = exp2_approx(x[n][0] - base), b = exp2_approx(x[n][1] - base);
+        sum += a + b;
+        // the weights are rounded to T for the second product (half a step of T each);
+        // their sum is of the unrounded ones
+        pa[mt][n >> 1][2 * (n & 1) + h] = pack2<T>(a, b);
+      }
+      l[mt][h] = l[mt][h] * alpha[h] + sum;
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[mt][n][0] *= alpha[0];
+        o[mt][n][1] *= alpha[0];
+        o[mt][n][2] *= alpha[1];
+        o[mt][n][3] *= alpha[1];
+      }
+    }
+  }
+  const auto v_frag = [&](uint32_t(&f)[4], int b, int cc) {
+    ldsm4_t(f, kt + v_at[cc & 3] + (cc >> 2) * 128 + b * 16 * (D * 2));
+  };
+  // A key that some rows see and others do not: a weight of 0 times an infinity or NaN
+  // would reach the rows that do not, so such values are left out of the product and
+  // added to the rows that see them. (A list's keys are seen by all rows or none, and
+  // read as zeros where they are seen by none.)
+  bool odd = false;
+  if (!kSel && !all) {
+#pragma unroll 1
+    for (int b = 0; b < kSub / 16; ++b)
+#pragma unroll
+      for (int cc = 0; cc < kSteps; ++cc) {
+        uint32_t f[4];
+        v_frag(f, b, cc);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= nonfinite_bits<T>(f[e]) != 0;
+      }
+    odd = __any_sync(0xffffffffu, odd);
+  }
+#pragma unroll
+  for (int b = 0; b < kSub / 16; ++b)
+#pragma unroll
+    for (int cc = 0; cc < kSteps; ++cc) {
+      uint32_t f[4];
+      v_frag(f, b, cc);
+      if (odd) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = clear_nonfinite<T>(f[e]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma16816<T>(o[mt][2 * cc], pa[mt][b], f[0], f[1]);
+        mma16816<T>(o[mt][2 * cc + 1], pa[mt][b], f[2], f[3]);
+      }
+    }
+  if (odd) {
+    const T* v = reinterpret_cast<const T*>(smem + (kt + C::kSubBytes - smem_u32(smem)));
+#pragma unroll 1
+    for (int key = 0; key < kSub; ++key)
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x =
+              static_cast<float>(v[chunk_at<D>(key, n) / 2 + 2 * (lane & 3) + e]);
+          if (!isfinite(x)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (sees(p, rpos[mt][h], s0 + key)) o[mt][n][2 * h + e] += x;
+          }
+        }
+  }
+}
+
 // Per unit of 16 * MT query rows of one kv head: the four warps take a quarter
 // of every tile's keys each (16 at D = 128, 32 at D = 64), with a ring of kStages sub-tiles of K and V per
 // warp that its own lanes fill with 16-byte asynchronous copies (so no warp
@@ -189,8 +351,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   using C = RowsCfg<D, MT>;
   constexpr int kChunks = D / 8;         // 16-byte chunks of a row
   constexpr int kSteps = D / 16;
-  constexpr int kSub = C::kSub, kTiles8 = kSub / 8;  // keys of a sub-tile; 8-key column blocks
-  constexpr int kTile = kWarps * kSub;
+  constexpr int kSub = C::kSub, kTile = kWarps * kSub;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
   __shared__ uint32_t s_valid[kWarps][kStages];
@@ -419,8 +580,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
         k_at[q] = chunk_at<D>((g >> 1) * 8 + r7, 2 * q + (g & 1));
         v_at[q] = C::kSubBytes + chunk_at<D>((g & 1) * 8 + r7, 2 * q + (g >> 1));
       }
-      const auto sees = [&](int32_t pos, int32_t k) {
-        return k <= pos && (k < p.sinks || pos - k < p.window);
+      const auto q_of = [&](uint32_t(&f)[4], int mt, int kk) {
+        if constexpr (MT == 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = qf[kk][e];
+        } else {
+          q_frag(f, mt, kk);
+        }
       };
       int stage = 0;
       for (int j = u.t0; j < u.t1; ++j) {
@@ -439,151 +605,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
           all = s0 + kSub - 1 <= p_lo && (s0 > w_hi || s0 + kSub <= p.sinks);
         }
         if (any) {
-          const uint32_t kt = ring + stage * C::kStageBytes;
-          // (two sums per block of scores where there are few, to shorten the chain of products)
-          constexpr int kSplit = kTiles8 == 2 ? 2 : 1;
-          float s[kSplit][MT][kTiles8][4];
-#pragma unroll
-          for (int f = 0; f < kSplit; ++f)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int n = 0; n < kTiles8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[f][mt][n][e] = 0.f;
-#pragma unroll
-          for (int kk = 0; kk < kSteps; ++kk) {
-            uint32_t qa[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              if constexpr (MT == 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) qa[mt][e] = qf[kk][e];
-              } else {
-                q_frag(qa[mt], mt, kk);
-              }
-            }
-#pragma unroll
-            for (int b = 0; b < kSub / 16; ++b) {
-              uint32_t f[4];
-              ldsm4(f, kt + k_at[kk & 3] + (kk >> 2) * 128 + b * 16 * (D * 2));
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<T>(s[kk % kSplit][mt][2 * b], qa[mt], f[0], f[1]);
-                mma16816<T>(s[kk % kSplit][mt][2 * b + 1], qa[mt], f[2], f[3]);
-              }
-            }
-          }
-          uint32_t pa[MT][kSub / 16][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float alpha[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // the row's scores of keys 8 n + 2 (lane % 4) + e
-              float x[kTiles8][2];
-#pragma unroll
-              for (int n = 0; n < kTiles8; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float y = s[0][mt][n][2 * h + e];
-                  if (kSplit == 2) y += s[kSplit - 1][mt][n][2 * h + e];
-                  x[n][e] = y * p.scale_log2;
-                }
-              if (!all) {
-#pragma unroll
-                for (int n = 0; n < kTiles8; ++n)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const int key = n * 8 + 2 * (lane & 3) + e;
-                    if (!(kSel ? (valid >> key) & 1 : sees(rpos[mt][h], s0 + key)))
-                      x[n][e] = -INFINITY;
-                  }
-              }
-              float mx = fmaxf(x[0][0], x[0][1]);
-#pragma unroll
-              for (int n = 1; n < kTiles8; ++n) mx = max3(mx, x[n][0], x[n][1]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = max3(mx, __shfl_xor_sync(0xffffffffu, mx, 2), m[mt][h]);
-              const float base = mx == -INFINITY ? 0.f : mx;
-              alpha[h] = exp2_approx(m[mt][h] - base);
-              m[mt][h] = mx;
-              float sum = 0.f;
-#pragma unroll
-              for (int n = 0; n < kTiles8; ++n) {
-                const float a = exp2_approx(x[n][0] - base), b = exp2_approx(x[n][1] - base);
-                sum += a + b;
-                // the weights are rounded to T for the second product (half a step of T each);
-                // their sum is of the unrounded ones
-                pa[mt][n >> 1][2 * (n & 1) + h] = pack2<T>(a, b);
-              }
-              l[mt][h] = l[mt][h] * alpha[h] + sum;
-            }
-            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-              for (int n = 0; n < D / 8; ++n) {
-                o[mt][n][0] *= alpha[0];
-                o[mt][n][1] *= alpha[0];
-                o[mt][n][2] *= alpha[1];
-                o[mt][n][3] *= alpha[1];
-              }
-            }
-          }
-          const auto v_frag = [&](uint32_t(&f)[4], int b, int cc) {
-            ldsm4_t(f, kt + v_at[cc & 3] + (cc >> 2) * 128 + b * 16 * (D * 2));
-          };
-          // A key that some rows see and others do not: a weight of 0 times an infinity or NaN
-          // would reach the rows that do not, so such values are left out of the product and
-          // added to the rows that see them. (A list's keys are seen by all rows or none, and
-          // read as zeros where they are seen by none.)
-          bool odd = false;
-          if (!kSel && !all) {
-#pragma unroll 1
-            for (int b = 0; b < kSub / 16; ++b)
-#pragma unroll
-              for (int cc = 0; cc < kSteps; ++cc) {
-                uint32_t f[4];
-                v_frag(f, b, cc);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd |= nonfinite_bits<T>(f[e]) != 0;
-              }
-            odd = __any_sync(0xffffffffu, odd);
-          }
-#pragma unroll
-          for (int b = 0; b < kSub / 16; ++b)
-#pragma unroll
-            for (int cc = 0; cc < kSteps; ++cc) {
-              uint32_t f[4];
-              v_frag(f, b, cc);
-              if (odd) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = clear_nonfinite<T>(f[e]);
-              }
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<T>(o[mt][2 * cc], pa[mt][b], f[0], f[1]);
-                mma16816<T>(o[mt][2 * cc + 1], pa[mt][b], f[2], f[3]);
-              }
-            }
-          if (odd) {
-            const T* v = reinterpret_cast<const T*>(smem + (kt + C::kSubBytes - smem_u32(smem)));
-#pragma unroll 1
-            for (int key = 0; key < kSub; ++key)
-#pragma unroll
-              for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float x =
-                      static_cast<float>(v[chunk_at<D>(key, n) / 2 + 2 * (lane & 3) + e]);
-                  if (!isfinite(x)) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                      for (int h = 0; h < 2; ++h)
-                        if (sees(rpos[mt][h], s0 + key)) o[mt][n][2 * h + e] += x;
-                  }
-                }
-          }
+          score_subtile<T, D, MT, kSel>(p, smem, ring + stage * C::kStageBytes, k_at, v_at, q_of,
+                                        valid, all, s0, rpos, o, m, l);
         }
         __syncwarp();
         stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -653,6 +676,186 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   }
 }
 
+// The selected form with a warp per unit of 16 query rows, for many tokens: no
+// unit is cut, no warp waits for another, and a warp's ring goes on from one unit
+// to the next, whose list and pages are looked up while the last one is scored
+// (a CTA per unit stands still for 4 us between units). 8000 tokens, one kv head
+// of 128, lists of 128: 76 us against 130 with a CTA per unit. Bound by the
+// latency of a sub-tile's dependent products with two warps a scheduler (1.1 us
+// for 8 KB), then by the reads of K and V rows from L2.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32, 2) attend_lists_kernel(const AttendParams p) {
+  using C = RowsCfg<D, 1>;
+  constexpr int kChunks = D / 8, kSteps = D / 16, kSub = C::kSub, kPerPass = 32 / kChunks;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_valid[kWarps][kStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * C::kStageBytes);
+  pdl_wait();
+  pdl_trigger();
+  const int blocks = (p.group + 15) / 16;
+  const int64_t units = selected_units(p);
+  const int64_t all_warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int32_t unit0 = static_cast<int32_t>(cut_position(units, all_warps, static_cast<int>(w)));
+  const int32_t unit1 = static_cast<int32_t>(cut_position(units, all_warps, static_cast<int>(w) + 1));
+  if (unit0 >= unit1) return;
+  const int32_t tiles = (p.topk + kSub - 1) / kSub;
+
+  // The request of a token, looked up when the last one's tokens end.
+  struct Found {
+    int32_t req = -1, begin = 0, end = 0;
+    __device__ __forceinline__ void find(const AttendParams& p, int32_t token) {
+      if (token >= begin && token < end) return;
+      req = token_request(p, token);
+      begin = req < 0 ? token : p.query_start_loc[req];
+      end = req < 0 ? token + 1 : p.query_start_loc[req + 1];
+    }
+  };
+
+  // ---- copies, ahead of the scores: list entries two sub-tiles before their copies are issued,
+  // pages one
+  Found ahead;
+  int32_t unit_in = unit0, tile_in = 0, head_in = 0;
+  const int32_t* list = nullptr;
+  const int32_t* bt = nullptr;
+  const auto enter = [&] {
+    const int32_t tb = unit_in / p.num_kv_heads, token = tb / blocks;
+    head_in = unit_in - tb * p.num_kv_heads;
+    ahead.find(p, token);
+    list = p.indices + static_cast<int64_t>(token) * p.indices_stride;
+    bt = p.block_table + static_cast<int64_t>(max(ahead.req, 0)) * p.bt_stride;
+  };
+  enter();
+  int32_t idx1 = -1, head1 = 0, idx0 = -1, page0 = -1, head0 = 0;
+  const int32_t* bt1 = bt;
+  bool there1 = false, there0 = false;
+  // moves every sub-tile one step on: its list entries, then its pages
+  const auto look = [&] {
+    idx0 = idx1;
+    head0 = head1;
+    there0 = there1;
+    page0 = idx1 >= 0 && idx1 < p.bt_width * kPageTokens ? bt1[idx1 / kPageTokens] : -1;
+    there1 = unit_in < unit1;
+    idx1 = -1;
+    if (there1) {
+      const int at = tile_in * kSub + (lane & (kSub - 1));
+      if (ahead.req >= 0 && at < p.topk) idx1 = list[at];
+      head1 = head_in;
+      bt1 = bt;
+      if (++tile_in == tiles) {
+        tile_in = 0;
+        if (++unit_in < unit1) enter();
+      }
+    }
+  };
+  const int c = lane % kChunks, h0 = lane / kChunks;
+  const uint32_t lane_at = chunk_at<D>(h0, c);
+  int stage_in = 0;
+  const auto issue = [&] {
+    if (there0) {
+      const uint32_t dst = ring + stage_in * C::kStageBytes;
+      const bool ok = idx0 >= 0 && page0 >= 0 && page0 < p.num_pages;
+      if (idx0 >= 0 && !ok) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+      uint32_t valid = __ballot_sync(0xffffffffu, ok);
+      if (kSub < 32) valid &= (1u << (kSub & 31)) - 1;
+      if (lane == 0) s_valid[warp][stage_in] = valid;
+      const int64_t pg = ok ? page0 : 0;
+      const int32_t tok = ok ? idx0 & (kPageTokens - 1) : 0;
+      const int64_t k_row = pg * p.k_stride_page + tok * p.k_stride_token;
+      const int64_t v_row = p.same_strides ? k_row : pg * p.v_stride_page + tok * p.v_stride_token;
+      const T* const k_lane = static_cast<const T*>(p.k) + head0 * p.k_stride_head + c * 8;
+      const T* const v_lane = static_cast<const T*>(p.v) + head0 * p.v_stride_head + c * 8;
+#pragma unroll
+      for (int i = 0; i < kSub / kPerPass; ++i) {
+        const int key = i * kPerPass + h0;
+        const int64_t ka = __shfl_sync(0xffffffffu, k_row, key);
+        const int64_t va = p.same_strides ? ka : __shfl_sync(0xffffffffu, v_row, key);
+        const bool v = (valid >> key) & 1;
+        const uint32_t at =
+            dst + i * kPerPass * (D * 2) + (lane_at ^ (((i * kPerPass) & 7) << 4));
+        cp_async16(at, k_lane + ka, v);
+        cp_async16(at + C::kSubBytes, v_lane + va, v);
+      }
+    }
+    cp_commit();
+    stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+    look();
+  };
+  look();
+  look();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue();
+
+  uint32_t k_at[4], v_at[4];
+  const int g = lane >> 3, r7 = lane & 7;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    k_at[q] = chunk_at<D>((g >> 1) * 8 + r7, 2 * q + (g & 1));
+    v_at[q] = C::kSubBytes + chunk_at<D>((g & 1) * 8 + r7, 2 * q + (g >> 1));
+  }
+  const int32_t rpos[1][2] = {};  // (a list's keys are seen by every row)
+  Found here;
+  int stage = 0;
+  for (int32_t unit = unit0; unit < unit1; ++unit) {
+    const int32_t tb = unit / p.num_kv_heads, kv_head = unit - tb * p.num_kv_heads;
+    const int32_t token = tb / blocks, row0 = (tb - token * blocks) * 16;
+    here.find(p, token);
+    // ---- queries straight into fragments: rows lane / 4 and 8 on, column pairs
+    uint32_t qf[kSteps][4];
+    const int row = lane >> 2, rows = min(16, p.group - row0);
+    const T* const q = static_cast<const T*>(p.q) + token * p.q_stride_token +
+                       static_cast<int64_t>(kv_head * p.group + row0) * p.q_stride_head + 2 * (lane & 3);
+#pragma unroll
+    for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = row + (e & 1) * 8;
+        qf[kk][e] = r < rows ? *reinterpret_cast<const uint32_t*>(q + r * p.q_stride_head + kk * 16 +
+                                                                  (e >> 1) * 8)
+                             : 0u;
+      }
+    const auto q_of = [&](uint32_t(&f)[4], int, int kk) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = qf[kk][e];
+    };
+    float o[1][D / 8][4], m[1][2] = {{-INFINITY, -INFINITY}}, l[1][2] = {};
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[0][n][e] = 0.f;
+    for (int j = 0; j < tiles; ++j) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      issue();  // into the sub-tile that the last round read
+      const uint32_t valid = s_valid[warp][stage];
+      if (valid)
+        score_subtile<T, D, 1, true>(p, smem, ring + stage * C::kStageBytes, k_at, v_at, q_of, valid,
+                                     valid == (0xffffffffu >> (32 - kSub)), 0, rpos, o, m, l);
+      __syncwarp();
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    if (here.req < 0) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float sum = l[0][h];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int r = row + 8 * h;
+      if (r < rows) {
+        const int64_t at = static_cast<int64_t>(token) * p.num_heads + kv_head * p.group + row0 + r;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + at * D) + (lane & 3);
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          dst[n * 4] = pack2<T>(o[0][n][2 * h] * inv, o[0][n][2 * h + 1] * inv);
+        if ((lane & 3) == 0 && p.lse) p.lse[at] = (m[0][h] + log2f(sum)) * kLn2;
+      }
+    }
+  }
+  cp_wait<0>();
+}
+
 // ---------------------------------------------------------------------------
 // join of the pieces of units that several CTAs share
 // ---------------------------------------------------------------------------
@@ -667,8 +870,8 @@ __host__ __device__ constexpr int combine_rows(int32_t rows) { return rows > 64 
 // at 32 following CTAs' cuts at once, then at their pieces' maxima and sums, so
 // that the accumulators' loads do not wait for one another; the pieces are
 // joined in the order of the CTAs, so the result does not depend on timing.
-// Bound by latency: four dependent loads (one token of 8 units over 34 CTAs:
-// TIMING).
+// Bound by latency: four dependent loads (one request of 8000 keys, 8 units
+// of 31 pieces: 3 us; piece by piece 10).
 template <typename T, int D, bool kSel, int kRows>
 __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(const AttendParams p) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
@@ -807,6 +1010,16 @@ idx_status launch_rows_as(const AttendParams& p, cudaStream_t s) {
 }
 
 template <typename T, int D>
+idx_status launch_lists_as(const AttendParams& p, cudaStream_t s) {
+  using C = RowsCfg<D, 1>;
+  const auto kernel = attend_lists_kernel<T, D>;
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = allow_smem<C::kRing, 0>(kernel, configured);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(launch_pdl(kernel, p.grid, kWarps * 32, C::kRing, s, p));
+}
+
+template <typename T, int D>
 idx_status launch_rows_d(const AttendParams& p, int mt, cudaStream_t s) {
   if (!p.indices) return launch_rows_as<T, D, 1, false>(p, s);
   return mt == 1 ? launch_rows_as<T, D, 1, true>(p, s) : launch_rows_as<T, D, 2, true>(p, s);
@@ -843,6 +1056,13 @@ idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, in
                           : launch_rows_d<__half, 128>(p, mt, s);
   return head_dim == 64 ? launch_rows_d<__nv_bfloat16, 64>(p, mt, s)
                         : launch_rows_d<__nv_bfloat16, 128>(p, mt, s);
+}
+
+idx_status launch_attend_lists(const AttendParams& p, int head_dim, bool half, cudaStream_t s) {
+  if (half)
+    return head_dim == 64 ? launch_lists_as<__half, 64>(p, s) : launch_lists_as<__half, 128>(p, s);
+  return head_dim == 64 ? launch_lists_as<__nv_bfloat16, 64>(p, s)
+                        : launch_lists_as<__nv_bfloat16, 128>(p, s);
 }
 
 idx_status launch_attend_combine(const AttendParams& p, int head_dim, bool half, cudaStream_t s) {

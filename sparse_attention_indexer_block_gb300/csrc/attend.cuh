@@ -410,6 +410,7 @@ idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, in
 // (the caches' strides have to suit a tensor map: attend_tc_takes)
 bool attend_tc_takes(const AttendParams& p, int head_dim);
 idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
+idx_status launch_attend_lists(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 idx_status launch_attend_combine(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 
 }  // namespace saib

@@ -59,6 +59,24 @@ Variant rows_variant(int mt, int head_dim, bool selected) {
                  kRowsCtasPerSm * device_sm_count(), 1, selected ? 4 : 2};
 }
 
+// Whether a list's units go to a warp each or to a CTA each, by what they take on a GB300 in
+// tenths of a warp's time for a sub-tile (1 us; 16 keys at D = 128, 32 at 64): a warp takes 1.1 a
+// sub-tile and 2 a unit, rounds of units one after another; a CTA's four warps share the
+// sub-tiles but stand still for 4 between units, and up to `grid` units are cut evenly. (us, warp /
+// CTA, D = 128, 8 kv heads: 2400 tokens with lists of 32: 64 / 206, 512: 594 / 610; 256 tokens,
+// 128: 25 / 42, 2048: 288 / 219; 64 tokens, 512: 40 / 33, 2048: 144 / 69; one kv head, 8000
+// tokens, 512: 260 / 278; D = 64: 141 / 160, 2048: 526 / 450.)
+bool warp_per_list(const AttendParams& p, int head_dim, const Variant& v) {
+  const int64_t sub = (p.topk + rows_tile_keys(head_dim) / 4 - 1) / (rows_tile_keys(head_dim) / 4);
+  const int64_t one = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads;
+  const int64_t by_warp = one * ((p.group + 15) / 16), by_cta = one * ((p.group + v.rows - 1) / v.rows);
+  const int64_t warps = 4 * v.grid;
+  const int64_t warp_time = (by_warp + warps - 1) / warps * (11 * sub + 20) + 40;
+  const int64_t cta_time = by_cta <= v.grid ? 10 * by_cta * sub / warps + 130
+                                            : by_cta * (10 * sub / 4 + 40) / v.grid + 80;
+  return warp_time < cta_time;
+}
+
 Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 3, 4}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
@@ -219,6 +237,11 @@ idx_status indexer_attend_selected(const idx_attend* a, void* stream) {
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
+  if (warp_per_list(p, a->head_dim, v)) {
+    p.rows = 16;
+    p.tile_log2 = a->head_dim == 64 ? 5 : 4;
+    return launch_attend_lists(p, a->head_dim, half, s);
+  }
   if ((st = launch_attend_rows(p, a->head_dim, half, v.mt, s)) != IDX_OK) return st;
   return launch_attend_combine(p, a->head_dim, half, s);
 }
