@@ -375,16 +375,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
     first_tile = a.y;
     last_tile = b.y;
   }
-  PieceWalk walk;
+  PieceWalk<false> walk;
   if constexpr (!kSel) {
     if (p.self_plan) {
       __shared__ int64_t sums[32];
       __shared__ int4 cuts[2];
       __shared__ ReqShape first;
       self_plan<kWarps * 32>(p, cta, reinterpret_cast<int64_t*>(smem), sums, cuts, &first);
-      walk = PieceWalk(p, cuts[0], cuts[1], first);
+      walk = PieceWalk<false>(p, cuts[0], cuts[1], first);
     } else {
-      walk = PieceWalk(p.bound[cta], p.bound[cta + 1]);
+      walk = PieceWalk<false>(p, p.bound[cta], p.bound[cta + 1]);
     }
   }
 

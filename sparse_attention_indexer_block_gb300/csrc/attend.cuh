@@ -144,56 +144,84 @@ __device__ __forceinline__ void row_place(const AttendParams& p, const Piece& u,
   *pos = u.ahead + i;
 }
 
-// The pieces of a CTA's range in the paged form, in order.
+// The pieces of a CTA's range in the paged form, in order; with kFirstLast, a
+// first piece that begins inside its unit comes last. (The CTAs of one request
+// and kv head then all begin at its first keys and read them at the same time:
+// from HBM once, from L2 otherwise.)
+template <bool kFirstLast>
 struct PieceWalk {
   int4 cur, end;
   ReqShape shape;   // of request cur.w
   int32_t entries;  // its entries
   bool done, stale;
+  int later;        // kFirstLast: 2 to be passed over, 1 to come, 0 none
 
   PieceWalk() = default;
-  __device__ __forceinline__ PieceWalk(const int4& from, const int4& to)
-      : cur(from), end(to), done(false), stale(true) {}
+  __device__ __forceinline__ PieceWalk(const AttendParams& p, const int4& from, const int4& to)
+      : cur(from), end(to), done(from.w >= p.num_reqs), stale(true),
+        later(kFirstLast && from.z > 0 && !(from.x == to.x && from.y == to.y && from.w == to.w) ? 2
+                                                                                              : 0) {}
   // with the first request's shape at hand
   __device__ __forceinline__ PieceWalk(const AttendParams& p, const int4& from, const int4& to,
                                        const ReqShape& first)
-      : cur(from), end(to), shape(first), entries(request_entries(p, first)), done(false),
-        stale(false) {}
+      : PieceWalk(p, from, to) {
+    shape = first;
+    entries = request_entries(p, first);
+    stale = false;
+  }
 
   __device__ __forceinline__ bool next(const AttendParams& p, Piece* u) {
-    if (done || cur.w >= p.num_reqs) return false;
-    const bool last = cur.w == end.w && cur.y == end.y && cur.x == end.x;
-    if (last && end.z <= cur.z) return false;
-    if (stale) {
-      shape = request_shape(p, cur.w, false);
-      entries = request_entries(p, shape);
-      stale = false;
-    }
-    u->req = cur.w;
-    u->head = cur.y;
-    u->row0 = cur.x * p.rows;
-    u->rows = min(p.rows, shape.nq * p.group - u->row0);
-    u->q0 = shape.q0;
-    u->ahead = shape.keys - shape.nq;
-    u->tiles = unit_tiles(p, shape, cur.x);
-    u->t0 = cur.z;
-    u->t1 = last ? end.z : u->tiles.count;
-    done = last;
-    if (!last) {
-      cur.z = 0;
-      if (++cur.x == entries) {
-        cur.x = 0;
-        if (++cur.y == p.num_kv_heads) {
-          cur.y = 0;
-          do {
-            if (++cur.w == p.num_reqs) break;
-            shape = request_shape(p, cur.w, false);
-            entries = request_entries(p, shape);
-          } while (entries == 0);
+    for (;;) {
+      if (done) {
+        if (!kFirstLast || later != 1) return false;
+        cur = p.bound[blockIdx.x];
+        end = make_int4(cur.x, cur.y, INT32_MAX, cur.w);
+        stale = true;
+        later = 0;
+      }
+      const bool last = cur.w == end.w && cur.y == end.y && cur.x == end.x;
+      if (last && end.z <= cur.z) {
+        done = true;
+        continue;
+      }
+      if (stale) {
+        shape = request_shape(p, cur.w, false);
+        entries = request_entries(p, shape);
+        stale = false;
+      }
+      u->req = cur.w;
+      u->head = cur.y;
+      u->row0 = cur.x * p.rows;
+      u->rows = min(p.rows, shape.nq * p.group - u->row0);
+      u->q0 = shape.q0;
+      u->ahead = shape.keys - shape.nq;
+      u->tiles = unit_tiles(p, shape, cur.x);
+      u->t0 = cur.z;
+      u->t1 = last ? min(end.z, u->tiles.count) : u->tiles.count;
+      done = last;
+      if (!last) {
+        cur.z = 0;
+        if (++cur.x == entries) {
+          cur.x = 0;
+          if (++cur.y == p.num_kv_heads) {
+            cur.y = 0;
+            do {
+              if (++cur.w == p.num_reqs) {
+                done = true;
+                break;
+              }
+              shape = request_shape(p, cur.w, false);
+              entries = request_entries(p, shape);
+            } while (entries == 0);
+          }
         }
       }
+      if (kFirstLast && later == 2) {
+        later = 1;
+        continue;
+      }
+      return true;
     }
-    return true;
   }
 };
 

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  PieceWalk walk(p.bound[blockIdx.x], p.bound[blockIdx.x + 1]);
+  PieceWalk<true> walk(p, p.bound[blockIdx.x], p.bound[blockIdx.x + 1]);
   Piece u;
 
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
