@@ -578,12 +578,13 @@ def _need_i32(name, what, t, *shape):
     """An int32 tensor of that shape (None: any size), contiguous in its last dimension."""
     if not isinstance(t, torch.Tensor) or t.dtype is not _I32T:
         _refuse(name, f"{what} must be an int32 tensor")
-    if t.dim() != len(shape):
-        _refuse(name, f"{what} has shape {tuple(t.shape)}")
-    for a, n in zip(t.shape, shape):
+    got = t.shape
+    if len(got) != len(shape):
+        _refuse(name, f"{what} has shape {tuple(got)}")
+    for a, n in zip(got, shape):
         if n is not None and a != n:
-            _refuse(name, f"{what} has shape {tuple(t.shape)}")
-    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
+            _refuse(name, f"{what} has shape {tuple(got)}")
+    if not t.is_contiguous() and t.stride(-1) != 1 and got[-1] > 1:
         _refuse(name, f"{what} must be contiguous in its last dimension")
 
 
@@ -793,6 +794,15 @@ def _pools(name, pools, num_pages):
     return out, num_pages
 
 
+def _ok(name, st):
+    if st:
+        _check(name, st)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _need_rows(name, block_table, seq_lens, ref_counts):
     width, stride = _need_table(name, block_table)
     _need_i32(name, "seq_lens", seq_lens, block_table.shape[0])
@@ -807,13 +817,13 @@ def indexer_copy_pages(pools, src, dst, dev_error=None, stream=None):
     if not pools:
         _refuse(name, "no pools")
     _need_i32(name, "src", src, None)
-    _need_i32(name, "dst", dst, int(src.shape[0]))
+    _need_i32(name, "dst", dst, src.shape[0])
     _need_error(name, dev_error)
     arr, pages = _pools(name, pools, None)
     index = _need_device(name, src, dst, dev_error, *pools)
     with _On(index, stream) as s:
-        _check(name, load().indexer_copy_pages(arr, len(pools), pages, _ptr(src), _ptr(dst),
-                                               int(src.shape[0]), _ptr(dev_error), s))
+        _ok(name, load().indexer_copy_pages(arr, len(pools), pages, _at(src), _at(dst),
+                                               src.shape[0], _at(dev_error), s))
 
 
 def indexer_fork_pages(pools, block_table, seq_lens, ref_counts, parents, children, copy_src=None,
@@ -825,13 +835,13 @@ def indexer_fork_pages(pools, block_table, seq_lens, ref_counts, parents, childr
     name = "indexer_fork_pages"
     rows_n, width, bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
     _need_i32(name, "parents", parents, None)
-    n = int(parents.shape[0])
+    n = parents.shape[0]
     _need_i32(name, "children", children, n)
     for what, t in (("copy_src", copy_src), ("copy_dst", copy_dst)):
         if t is not None:
             _need_i32(name, what, t, n)
     _need_error(name, dev_error)
-    arr, pages = _pools(name, pools, int(ref_counts.shape[0]))
+    arr, pages = _pools(name, pools, ref_counts.shape[0])
     index = _need_device(name, block_table, seq_lens, ref_counts, parents, children, copy_src, copy_dst,
                          dev_error, *pools)
     with _On(index, stream) as s:
@@ -839,9 +849,9 @@ def indexer_fork_pages(pools, block_table, seq_lens, ref_counts, parents, childr
             copy_src = torch.empty_like(parents)
         if copy_dst is None:
             copy_dst = torch.empty_like(parents)
-        _check(name, load().indexer_fork_pages(
-            arr, len(pools), pages, _ptr(block_table), bt_stride, width, rows_n,
-            _ptr(seq_lens), _ptr(ref_counts), _ptr(parents), _ptr(children), n, _ptr(copy_src), _ptr(copy_dst), _ptr(dev_error), s))
+        _ok(name, load().indexer_fork_pages(
+            arr, len(pools), pages, _at(block_table), bt_stride, width, rows_n,
+            _at(seq_lens), _at(ref_counts), _at(parents), _at(children), n, _at(copy_src), _at(copy_dst), _at(dev_error), s))
     return copy_src, copy_dst
 
 
@@ -854,10 +864,10 @@ def indexer_free_pages(block_table, seq_lens, ref_counts, rows, dev_error=None, 
     _need_error(name, dev_error)
     index = _need_device(name, block_table, seq_lens, ref_counts, rows, dev_error)
     with _On(index, stream) as s:
-        _check(name, load().indexer_free_pages(
-            _ptr(block_table), bt_stride, width, rows_n,
-            _ptr(seq_lens), _ptr(ref_counts), int(ref_counts.shape[0]), _ptr(rows),
-            int(rows.shape[0]), _ptr(dev_error), s))
+        _ok(name, load().indexer_free_pages(
+            _at(block_table), bt_stride, width, rows_n,
+            _at(seq_lens), _at(ref_counts), ref_counts.shape[0], _at(rows),
+            rows.shape[0], _at(dev_error), s))
 
 
 @functools.lru_cache(maxsize=256)
@@ -875,7 +885,7 @@ def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, 
     [1] on the device: pages in use)."""
     name = "indexer_compact_pages"
     rows_n, width, bt_stride = _need_rows(name, block_table, seq_lens, ref_counts)
-    pages = int(ref_counts.shape[0])
+    pages = ref_counts.shape[0]
     if remap is not None:
         _need_i32(name, "remap", remap, pages)
     if num_live is not None:
@@ -892,8 +902,8 @@ def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, 
         if workspace is None:
             workspace = torch.empty(_compact_workspace_bytes(pages), dtype=torch.uint8,
                                     device=ref_counts.device)
-        _check(name, lib.indexer_compact_pages(
-            arr, len(pools), pages, _ptr(block_table), bt_stride, width, rows_n,
-            _ptr(seq_lens), _ptr(ref_counts), _ptr(remap), _ptr(num_live), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
-            _ptr(dev_error), s))
+        _ok(name, lib.indexer_compact_pages(
+            arr, len(pools), pages, _at(block_table), bt_stride, width, rows_n,
+            _at(seq_lens), _at(ref_counts), _at(remap), _at(num_live), _at(workspace), workspace.numel() * workspace.element_size(),
+            _at(dev_error), s))
     return remap, num_live
