@@ -60,9 +60,9 @@ Variant rows_variant(int mt, int head_dim, bool selected) {
 }
 
 // Whether a list's units go to a warp each or to a CTA each, by what they take on a GB300 in
-// tenths of a warp's time for a sub-tile (1 us; 16 keys at D = 128, 32 at 64): a warp takes 1.1 a
-// sub-tile and 2 a unit, rounds of units one after another; a CTA's four warps share the
-// sub-tiles but stand still for 4 between units, and up to `grid` units are cut evenly. (us, warp /
+// tenths of a microsecond: a warp takes 1.1 us a sub-tile (16 keys at D = 128, 32 at 64) and 1.7 a
+// unit, rounds of units one after another; a CTA's four warps share the sub-tiles at 0.9 each, but
+// stand still for 2.6 between units, and up to `grid` units are cut evenly. (us, warp /
 // CTA, D = 128, 8 kv heads: 2400 tokens with lists of 32: 64 / 206, 512: 594 / 610; 256 tokens,
 // 128: 25 / 42, 2048: 288 / 219; 64 tokens, 512: 40 / 33, 2048: 144 / 69; one kv head, 8000
 // tokens, 512: 260 / 278; D = 64: 141 / 160, 2048: 526 / 450.)
@@ -71,9 +71,9 @@ bool warp_per_list(const AttendParams& p, int head_dim, const Variant& v) {
   const int64_t one = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads;
   const int64_t by_warp = one * ((p.group + 15) / 16), by_cta = one * ((p.group + v.rows - 1) / v.rows);
   const int64_t warps = 4 * v.grid;
-  const int64_t warp_time = (by_warp + warps - 1) / warps * (11 * sub + 20) + 40;
+  const int64_t warp_time = (by_warp + warps - 1) / warps * (11 * sub + 17) + 40;
   const int64_t cta_time = by_cta <= v.grid ? 10 * by_cta * sub / warps + 130
-                                            : by_cta * (10 * sub / 4 + 40) / v.grid + 80;
+                                            : by_cta * (9 * sub / 4 + 26) / v.grid + 80;
   return warp_time < cta_time;
 }
 
