@@ -27,6 +27,9 @@ template <int D>
 struct TcCfg {
   // Tensor memory: scores of slot i at 128 i, its weights over them, its accumulator at kColO + D i
   static constexpr int kColO = 256;
+  // The second product begins with the first half of a tile's keys; at D = 64 it is too short to be
+  // worth another wait of the products' warp.
+  static constexpr bool kEarly = D == 128;
   static constexpr int kSlotBytes = kSlotRows * D * 2;
   static constexpr int kQ = 2 * kSlotBytes;
   static constexpr int kStage = kTileTc * D * 2;
@@ -44,7 +47,7 @@ struct TcBars {
   uint64_t k_full[5], k_empty[5];
   uint64_t v_full[5], v_empty[5], v_ok[5];  // v_ok: edge tiles cleared (or none)
   uint64_t s_full[2], o_full[2];
-  uint64_t p_full[2][2];           // halves of the weights: keys 0-63 and 64-127 of the tile
+  uint64_t p_full[2][2];           // weights of keys 0-63 (kEarly) and of all
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag;
@@ -340,7 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------- products
       // The whole warp walks; one elected lane issues. (Descriptors from warp-uniform values
       // with constant steps: computed by a single diverged thread, they cost 140 cycles a
-      // product to issue, against 64 to execute.)
+      // product to issue, against 64 to execute.) What this warp does between a wait and its
+      // products delays every chain behind it, so the lanes vote on their waits once a tile: after
+      // a wait that gave up, the tile's products still run, on whatever is there.
       constexpr uint32_t kDescQK = f16_idesc<T>(128, kTileTc, false);
       constexpr uint32_t kDescPV = f16_idesc<T>(128, D, true);
       const uint64_t q_desc = sw128_kmajor_desc(q_addr), k_desc = sw128_kmajor_desc(k_addr);
@@ -373,46 +378,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n <= 0) continue;
         const int slots = u.rows > kSlotRows ? 2 : 1;
         issued = true;
-        if (!(ok = wait_warp(&bars.q_full, q_phase))) break;
+        ok = wait(&bars.q_full, q_phase) && ok;
         q_phase ^= 1;
-        // the scores of tile j for one slot; the last slot frees K (and the queries)
-        const auto scores = [&](int j, int slot) -> bool {
-          if (slot == 0 && !wait_warp(&bars.k_full[ka.stage], ka.phase)) return false;
-          if (elect_one()) {
-            qk(slot, ka.stage);
-            if (slot == slots - 1) {
-              mma_commit(&bars.k_empty[ka.stage]);
-              if (j == n - 1) mma_commit(&bars.q_empty);
-            }
+        ok = wait(&bars.k_full[ka.stage], ka.phase) && ok;
+        // the scores of a tile; its last slot frees K, the last tile's the queries
+        const auto scores = [&](int slot, bool last_tile) {
+          qk(slot, ka.stage);
+          if (slot == slots - 1) {
+            mma_commit(&bars.k_empty[ka.stage]);
+            if (last_tile) mma_commit(&bars.q_empty);
           }
-          __syncwarp();
-          if (slot == slots - 1) ka.step();
-          return true;
         };
-        for (int slot = 0; ok && slot < slots; ++slot) ok = scores(0, slot);
-        for (int j = 0; ok && j < n; ++j) {
+        if (elect_one()) {
+          scores(0, n == 1);
+          if (slots == 2) scores(1, n == 1);
+        }
+        ka.step();
+        for (int j = 0; j < n; ++j) {
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
           const int sv = va.stage;
           const bool more = j + 1 < n;
-          if (!(ok = wait_warp(&bars.v_ok[sv], va.phase))) break;
+          ok = wait(&bars.v_ok[sv], va.phase) && ok;
           va.step();
           for (int slot = 0; slot < slots; ++slot) {
             const uint32_t parity = (p_phase >> slot) & 1;
             p_phase ^= 1u << slot;
-            if (!(ok = wait_warp(&bars.p_full[slot][0], parity))) break;
-            tc_fence_after();
-            if (elect_one()) pv(slot, sv, 0, j == 0);
-            __syncwarp();
-            if (!(ok = wait_warp(&bars.p_full[slot][1], parity))) break;
+            if (C::kEarly) {
+              ok = wait(&bars.p_full[slot][0], parity) && ok;
+              tc_fence_after();
+              if (elect_one()) pv(slot, sv, 0, j == 0);
+            }
+            if (more && slot == 0) ok = wait(&bars.k_full[ka.stage], ka.phase) && ok;
+            ok = wait(&bars.p_full[slot][1], parity) && ok;
             tc_fence_after();
             if (elect_one()) {
+              if (!C::kEarly) pv(slot, sv, 0, j == 0);
               pv(slot, sv, 1, j == 0);
-              if (!more) mma_commit(&bars.o_full[slot]);
+              if (more) scores(slot, j + 2 == n);
+              else mma_commit(&bars.o_full[slot]);
               if (slot == slots - 1) mma_commit(&bars.v_empty[sv]);
             }
-            __syncwarp();
-            if (more && !(ok = scores(j + 1, slot))) break;
           }
+          if (more) ka.step();
         }
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (issued) {
         // every product completes before tensor memory is released
@@ -591,11 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[i] = pack2<T>(a, b);
           }
           tmem_st32(s_col + c * 32, w);
-          // (the second product begins with the first half of the keys)
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.p_full[slot][c]);
+          if (C::kEarly || c == 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.p_full[slot][c]);
+          }
         }
         const float2 sum = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
         l += sum.x + sum.y;
