@@ -435,9 +435,11 @@ inline cudaError_t allow_smem(Kernel* kernel, std::atomic<bool>* configured) {
 // Launchers.
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s);
 idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, int mt, cudaStream_t s);
-// (the caches' strides have to suit a tensor map: attend_tc_takes)
-bool attend_tc_takes(const AttendParams& p, int head_dim);
-idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
+// The chunk kernel's tensor maps of the caches; false when their strides suit none.
+bool attend_tc_maps(const AttendParams& p, int head_dim, bool half, CUtensorMap* kmap,
+                    CUtensorMap* vmap);
+idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, cudaStream_t s);
 idx_status launch_attend_lists(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 idx_status launch_attend_combine(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 

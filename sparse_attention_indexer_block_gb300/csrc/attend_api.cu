@@ -208,15 +208,17 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
   // The row-block kernel holds 16 rows at once and reads K and V again for the next 16; from
   // 17 rows on the tensor-memory kernel is faster (24 requests of 8000 keys, 8 kv heads of 128:
   // 15 rows 132 against 140 us, 20 rows 173 against 142).
-  const bool tc = longest * p.group > 16 && attend_tc_takes(p, a->head_dim);
+  const bool half = a->dtype == IDX_FP16;
+  CUtensorMap kmap, vmap;
+  const bool tc =
+      longest * p.group > 16 && attend_tc_maps(p, a->head_dim, half, &kmap, &vmap);
   const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim, false);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool half = a->dtype == IDX_FP16;
   p.self_plan = !tc && a->num_reqs <= kSelfPlanReqs &&
                 longest * p.group <= kSelfPlanEntries * int64_t{v.rows};
   if (!p.self_plan && (st = launch_attend_plan(p, s)) != IDX_OK) return st;
-  st = tc ? launch_attend_tc(p, a->head_dim, half, s)
+  st = tc ? launch_attend_tc(p, a->head_dim, half, kmap, vmap, s)
           : launch_attend_rows(p, a->head_dim, half, v.mt, s);
   if (st != IDX_OK) return st;
   return launch_attend_combine(p, a->head_dim, half, s);

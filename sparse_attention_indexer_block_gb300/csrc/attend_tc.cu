@@ -733,20 +733,21 @@ bool map_stride_ok(int64_t stride, int64_t entries) {
 
 }  // namespace
 
-bool attend_tc_takes(const AttendParams& p, int) {
+bool attend_tc_maps(const AttendParams& p, int head_dim, bool half, CUtensorMap* kmap,
+                    CUtensorMap* vmap) {
   return map_stride_ok(p.k_stride_token, 2) && map_stride_ok(p.v_stride_token, 2) &&
          map_stride_ok(p.k_stride_head, p.num_kv_heads) &&
          map_stride_ok(p.v_stride_head, p.num_kv_heads) &&
-         map_stride_ok(p.k_stride_page, p.num_pages) && map_stride_ok(p.v_stride_page, p.num_pages);
+         map_stride_ok(p.k_stride_page, p.num_pages) &&
+         map_stride_ok(p.v_stride_page, p.num_pages) &&
+         encode_map(kmap, p.k, half, head_dim, p.k_stride_token, p.k_stride_head, p.k_stride_page,
+                    p.num_kv_heads, p.num_pages) &&
+         encode_map(vmap, p.v, half, head_dim, p.v_stride_token, p.v_stride_head, p.v_stride_page,
+                    p.num_kv_heads, p.num_pages);
 }
 
-idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, cudaStream_t s) {
-  CUtensorMap kmap, vmap;
-  if (!encode_map(&kmap, p.k, half, head_dim, p.k_stride_token, p.k_stride_head, p.k_stride_page,
-                  p.num_kv_heads, p.num_pages) ||
-      !encode_map(&vmap, p.v, half, head_dim, p.v_stride_token, p.v_stride_head, p.v_stride_page,
-                  p.num_kv_heads, p.num_pages))
-    return IDX_ERR_CUDA;
+idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, cudaStream_t s) {
   if (half)
     return head_dim == 64 ? launch_tc_as<__half, 64>(p, kmap, vmap, s)
                           : launch_tc_as<__half, 128>(p, kmap, vmap, s);

@@ -390,3 +390,106 @@ def test_offsets_past_32_bits():
     idx = _lists(b, 64)
     ref = b.reference(indices=idx)
     b.check(b.attend_selected(idx), ref)
+
+
+# ---- more of the chunk kernel's (over 16 rows a kv head) and the many-token lists' edges
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("ql,kl,heads,kv", [
+    ([200, 0, 90, 1], [150, 10, 0, 500], 8, 2),          # fewer keys than tokens, no tokens, no keys
+    ([0, 0, 257, 0], [5, 0, 257, 9], 16, 2),
+    ([17, 33, 64, 65], [17, 4000, 64, 191], 16, 16),     # a kv head each: units of few rows
+    ([128, 129], [128, 1290], 2, 1),                     # exactly one block of 256 rows, and two rows more
+    ([1, 1, 1, 500], [3000, 1, 0, 640], 24, 2),          # single tokens beside a chunk
+])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3), (1, 200)])
+def test_chunk_batches(ql, kl, heads, kv, window, sinks, dim):
+    b = Batch(ql, kl, heads, kv, dim, BF, seed=31)
+    b.check(b.attend(window=window, sinks=sinks), b.reference(window=window, sinks=sinks))
+
+
+@pytest.mark.parametrize("ql,kl", [([1, 2], [300, 70]), ([150, 3], [400, 70])])
+def test_padded_caches(ql, kl):
+    """Pages with slack between tokens, heads and pages: strides that are multiples of 8 values and
+    of nothing else; and a cache of one head shared by all (a stride of 0)."""
+    b = Batch(ql, kl, 8, 2, 64, FP, seed=32)
+    want = b.reference()
+    pages = b.k.shape[0]
+    for cache in ("k", "v"):
+        wide = torch.full((pages * (65 * 2 * 72) + 8,), float("nan"), dtype=FP, device=DEV)
+        view = wide[8:].as_strided((pages, PAGE, 2, 64), (65 * 2 * 72 - 8 * (cache == "k"), 2 * 72, 72, 1))
+        view.copy_(getattr(b, cache))
+        setattr(b, cache, view)
+    b.check(b.attend(), want)
+    idx = _lists(b, 30)
+    b.check(b.attend_selected(idx), b.reference(indices=idx))
+    b.k, b.v = b.k[:, :, :1].expand(-1, -1, 2, -1), b.v[:, :, :1].expand(-1, -1, 2, -1)
+    assert b.k.stride(2) == 0
+    b.check(b.attend(window=50, sinks=1), b.reference(window=50, sinks=1))
+
+
+def test_chunk_rows_outside_every_request_are_left_alone():
+    b = Batch([60, 30], [100, 80], 8, 2, 64, BF, seed=33)
+    want = b.reference()
+    q = torch.zeros((100, 8, 64), dtype=BF, device=DEV)
+    q[4:94] = b.q
+    out, lse = torch.full_like(q, 7.0), torch.full((100, 8), 7.0, device=DEV)
+    saib.indexer_attend_paged(q, b.k, b.v, b.table, b.lens, b.start + 4, 60, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out[:4] == 7).all() and (out[94:] == 7).all() and (lse[:4] == 7).all() and (lse[94:] == 7).all()
+    b.check((out[4:94], lse[4:94]), want)
+
+
+def test_chunk_reports_bad_lengths_and_pages():
+    b = Batch([60, 30], [200, 180], 8, 2, 64, BF, seed=34)
+    want = b.reference()
+    table = b.table.clone()
+    table[1, 1] = b.k.shape[0]
+    cases = [("lens", torch.tensor([200, b.width * 64 + 1], dtype=torch.int32, device=DEV), 2 | 1),
+             ("lens", torch.tensor([200, -3], dtype=torch.int32, device=DEV), 2),
+             ("start", torch.tensor([0, 60, 990], dtype=torch.int32, device=DEV), 2),
+             ("start", torch.tensor([0, 60, 20], dtype=torch.int32, device=DEV), 2),
+             ("table", table, 1)]
+    for name, value, bits in cases:
+        keep = getattr(b, name)
+        setattr(b, name, value)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out, _ = saib.indexer_attend_paged(b.q, b.k, b.v, b.table, b.lens, b.start, 60, dev_error=err)
+        torch.cuda.synchronize()
+        setattr(b, name, keep)
+        got = int(err.item())
+        assert got & bits and not got & ~bits, (name, got)
+        assert ((out[:60].double() - want[0][:60]).abs() <= want[2][:60]).all()   # the sound request
+    b.check(b.attend(), want)
+
+
+@pytest.mark.parametrize("heads,kv,topk,dtype,dim", [(8, 2, 100, BF, 128), (40, 1, 33, FP, 64), (6, 3, 17, BF, 64),
+                                                    (16, 1, 260, FP, 128), (4, 4, 1, BF, 128)])
+def test_lists_of_many_tokens(heads, kv, topk, dtype, dim):
+    b = Batch([700, 0, 300, 5], [900, 10, 300, 3], heads, kv, dim, dtype, seed=35)
+    idx = _lists(b, topk, empty_rows=(0, 3, 699, 700, 1004))
+    b.check(b.attend_selected(idx), b.reference(indices=idx))
+
+
+def test_lists_of_many_tokens_outside_requests_and_bad_entries():
+    b = Batch([400, 300], [500, 300], 4, 2, 64, BF, seed=36)
+    idx = _lists(b, 20)
+    want = b.reference(indices=idx)
+    q = torch.zeros((900, 4, 64), dtype=BF, device=DEV)
+    q[100:800] = b.q
+    lists = torch.full((900, 20), 3, dtype=torch.int32, device=DEV)
+    lists[100:800] = idx
+    out, lse = torch.full_like(q, 7.0), torch.full((900, 4), 7.0, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    saib.indexer_attend_selected(q, b.k, b.v, b.table, lists, b.start + 100, out=out, lse=lse, dev_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert (out[:100] == 7).all() and (out[800:] == 7).all() and (lse[:100] == 7).all() and (lse[800:] == 7).all()
+    b.check((out[100:800], lse[100:800]), want)
+    lists[100, 4] = b.width * PAGE          # past the table
+    lists[799, 0] = 5 * PAGE                # an unused column: page -7
+    saib.indexer_attend_selected(q, b.k, b.v, b.table, lists, b.start + 100, out=out, lse=lse, dev_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 1
+    b.check((out[101:799], lse[101:799]), tuple(w[1:699] for w in want))
