@@ -8,7 +8,7 @@ namespace saib {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kWarps = 4;        // of a row-block CTA
 constexpr int kStages = 3;       // sub-tiles in flight per warp
 
