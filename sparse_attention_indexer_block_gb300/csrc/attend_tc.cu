@@ -18,6 +18,7 @@ constexpr int kRegsLaunch = 168, kRegsFeed = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsFeed + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kOddUnits = 8;
+constexpr int kPieces = 4;  // pieces that the walk may be ahead
 // A row's running maximum is raised (and its accumulator rescaled) only when a
 // score exceeds it by this many units of log 2: the weights then stay below
 // 2^8, which both 16-bit types hold with the same relative precision.
@@ -49,6 +50,8 @@ struct TcBars {
   uint64_t s_full[2], o_full[2];
   uint64_t p_full[2][2];           // weights of keys 0-63 (kEarly) and of all
   uint64_t done;
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
+  Piece piece[kPieces];  // what the CTA works on, in order; req -1: no more
   uint32_t tmem_base;
   int abort_flag;
   uint32_t odd[kOddUnits];  // 1 + the last unit whose edge tiles held infinities or NaNs
@@ -125,6 +128,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+
+// 2^x, kept in the order of the source.
+__device__ __forceinline__ float exp2_ordered(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // True in one lane of a converged warp.
@@ -252,6 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.o_full[i], 1);
     }
     mbar_init(&bars.done, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&bars.piece_full[i], 1);
+      mbar_init(&bars.piece_empty[i], kThreads / 32 - 1);
+    }
     bars.abort_flag = 0;
     for (uint32_t i = 0; i < kOddUnits; ++i) bars.odd[i] = 0;
     fence_barrier_init();
@@ -272,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  PieceWalk<true> walk(p, p.bound[blockIdx.x], p.bound[blockIdx.x + 1]);
   Piece u;
 
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -281,6 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of a whole warp, which goes on together or not at all
   const auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+
+  // The next piece, for a whole warp; false when there is none (or the wait gave up). The walk
+  // costs some 2000 cycles a piece (loads and divisions that depend on one another), so the loading
+  // thread, which is ahead of all others, does it for them.
+  Ring<kPieces> pieces;
+  const auto next_piece = [&]() -> bool {
+    if (!wait_warp(&bars.piece_full[pieces.stage], pieces.phase)) return false;
+    u = bars.piece[pieces.stage];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.piece_empty[pieces.stage]);
+    pieces.step();
+    return u.req >= 0;
   };
 
   if (warp < 4) {
@@ -292,8 +318,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring<VS> va;
         int64_t tiles = 0;  // K issued
         int64_t v_tiles = 0;
+        int filled = 0;  // places of the ring of pieces
         bool ok = true;
-        while (ok && walk.next(p, &u)) {
+        PieceWalk<true> walk(p, p.bound[blockIdx.x], p.bound[blockIdx.x + 1]);
+        while (ok) {
+          if (!walk.next(p, &u)) u.req = -1;
+          if (filled < kPieces) ++filled;
+          else if (!(ok = wait(&bars.piece_empty[pieces.stage], pieces.phase ^ 1))) break;
+          bars.piece[pieces.stage] = u;
+          mbar_arrive(&bars.piece_full[pieces.stage]);
+          pieces.step();
+          if (u.req < 0) break;
           const int32_t* bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
           const auto pages_of = [&](int j) -> int2 {
             if (j >= u.t1) return make_int2(-1, -1);
@@ -373,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_f16_ts(d, a + kk * 8, b + kk * (2048 >> 4), kDescPV, !first || kk > 0);
         }
       };
-      while (ok && walk.next(p, &u)) {
+      while (ok && next_piece()) {
         const int n = u.t1 - u.t0;
         if (n <= 0) continue;
         const int slots = u.rows > kSlotRows ? 2 : 1;
@@ -438,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<VS> va;
       uint32_t unit = 0, q_phase = 0;
       bool ok = true;
-      while (ok && walk.next(p, &u)) {
+      while (ok && next_piece()) {
         const int n = u.t1 - u.t0;
         if (n <= 0) continue;
         if (unit > 0) {
@@ -522,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
     uint32_t s_phase = 0, o_phase = 0, unit = 0;
     bool ok = true;
-    while (ok && walk.next(p, &u)) {
+    while (ok && next_piece()) {
       const int n = u.t1 - u.t0;
       const uint32_t this_unit = unit;
       if (n > 0) ++unit;
@@ -589,15 +624,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c) {
           uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float(&v)[32] = s[2 * c + (i >> 4)];
-            const int e = (i & 15) * 2;
-            const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(v[e], v[e + 1]), scale2, sub2));
-            const float a = exp2_approx(x.x), b = exp2_approx(x.y);
-            sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(a, b));
-            // the weights are rounded to T for the second product (half a step of T
-            // each); their sum is of the unrounded ones
-            w[i] = pack2<T>(a, b);
+          for (int g = 0; g < 32; g += 8) {
+            float2 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float(&v)[32] = s[2 * c + ((g + i) >> 4)];
+              const int e = ((g + i) & 15) * 2;
+              x[i] = unpack_f32x2(fma_f32x2(pack_f32x2(v[e], v[e + 1]), scale2, sub2));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              x[i].x = exp2_ordered(x[i].x);
+              x[i].y = exp2_ordered(x[i].y);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x[i].x, x[i].y));
+              // the weights are rounded to T for the second product (half a step of T
+              // each); their sum is of the unrounded ones
+              w[g + i] = pack2<T>(x[i].x, x[i].y);
+            }
           }
           tmem_st32(s_col + c * 32, w);
           if (C::kEarly || c == 1) {
