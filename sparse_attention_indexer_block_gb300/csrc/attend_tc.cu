@@ -26,11 +26,15 @@ constexpr float kLazyRaise = 8.f;
 
 template <int D>
 struct TcCfg {
-  // Tensor memory: scores of slot i at 128 i, its weights over them, its accumulator at kColO + D i
+  // At D = 64 the accumulators leave room for the weights beside the scores: the next tile's scores
+  // are then computed while this one's weights are (2 x 8192 tokens, 64/8 heads: 1056 -> 996 us;
+  // units of 128 rows 99 -> 87 us). At D = 128 the weights lie over the scores, and the second
+  // product begins with the first half of a tile's keys.
+  static constexpr bool kAhead = D == 64;
+  // Tensor memory: scores of slot i at 128 i, its accumulator at kColO + D i, its weights at
+  // kColP + kStepP i
   static constexpr int kColO = 256;
-  // The second product begins with the first half of a tile's keys; at D = 64 it is too short to be
-  // worth another wait of the products' warp.
-  static constexpr bool kEarly = D == 128;
+  static constexpr int kColP = kAhead ? kColO + 2 * D : 0, kStepP = kAhead ? 64 : 128;
   static constexpr int kSlotBytes = kSlotRows * D * 2;
   static constexpr int kQ = 2 * kSlotBytes;
   static constexpr int kStage = kTileTc * D * 2;
@@ -47,8 +51,9 @@ struct TcBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[5], k_empty[5];
   uint64_t v_full[5], v_empty[5], v_ok[5];  // v_ok: edge tiles cleared (or none)
-  uint64_t s_full[2], o_full[2];
-  uint64_t p_full[2][2];           // weights of keys 0-63 (kEarly) and of all
+  uint64_t s_full[2], o_full[2];   // o_full: a unit's last product, with kAhead every tile's
+  uint64_t s_read[2];              // kAhead: scores are in registers
+  uint64_t p_half[2], p_full[2];   // weights of keys 0-63 (not with kAhead) and of all
   uint64_t done;
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   Piece piece[kPieces];  // what the CTA works on, in order; req -1: no more
@@ -128,13 +133,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
-}
-
-// 2^x, kept in the order of the source.
-__device__ __forceinline__ float exp2_ordered(float x) {
-  float y;
-  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // True in one lane of a converged warp.
@@ -217,9 +215,10 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u,
 
 // One CTA per SM walks its range of units. Per unit and tile,
 //   S = Q K^T (two slots of 128 rows), P = exp2(S * scale - m), O += P V
-// with S, O in tensor memory and P written over S as the second product's A
-// operand, so that scores and weights never leave the SM:
-//   warp 0      TMA: the tile's two K and two V pages into a ring of stages
+// with S, O in tensor memory and P written over S (D = 64: beside it) as the
+// second product's A operand, so that scores and weights never leave the SM:
+//   warp 0      walks the CTA's pieces and hands them to the other warps; TMA:
+//               the tile's two K and two V pages into rings of stages
 //   warp 1      one thread issues the products: while one slot's softmax runs,
 //               the other slot's products keep the tensor pipe busy
 //   warps 2, 3  load a unit's queries; clear infinities and NaNs in the edge
@@ -227,8 +226,10 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u,
 //   warps 4-7, 8-11  softmax of slot 0, 1: a thread per row, running maximum
 //               raised lazily, row sums in fp32, accumulators written out
 // Tiles of 128 keys read K and V once per 256 rows; with fewer rows than 129 in
-// a unit slot 1 idles. Bound by the tensor pipe for long chunks: 512 cycles per
-// product and slot and tile at D = 128, the exponentials another 512.
+// a unit slot 1 idles. A tile of both slots costs the tensor pipe 2048 cycles at
+// D = 128 and some 1200 at D = 64, the exponentials 1050; it takes 2900 and 2050,
+// for a row's chain of scores, maximum, exponentials and products is longer than
+// either, and two slots do not hide all of it.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
@@ -257,9 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i][0], 4);
-      mbar_init(&bars.p_full[i][1], 4);
+      mbar_init(&bars.p_half[i], 4);
+      mbar_init(&bars.p_full[i], 4);
       mbar_init(&bars.o_full[i], 1);
+      mbar_init(&bars.s_read[i], 4);
     }
     mbar_init(&bars.done, 1);
     for (int i = 0; i < kPieces; ++i) {
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = sw128_mnmajor_desc(v_addr, C::kHalf);
       Ring<KS> ka;
       Ring<VS> va;
-      uint32_t q_phase = 0, p_phase = 0;  // (bit i: slot i)
+      uint32_t q_phase = 0, p_phase = 0, r_phase = 0;  // (bit i: slot i)
       bool ok = true, issued = false;
       const auto qk = [&](int slot, int stage) {
         const uint32_t d = tmem + slot * 128;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&bars.s_full[slot]);
       };
       const auto pv = [&](int slot, int stage, int half, bool first) {
-        const uint32_t d = tmem + C::kColO + slot * D, a = tmem + slot * 128;
+        const uint32_t d = tmem + C::kColO + slot * D, a = tmem + C::kColP + slot * C::kStepP;
         const uint64_t b = v_desc + stage * (C::kStage >> 4);
 #pragma unroll
         for (int i = 0; i < kTileTc / 32; ++i) {
@@ -426,35 +428,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (elect_one()) {
           scores(0, n == 1);
-          if (slots == 2) scores(1, n == 1);
+          if (!C::kAhead && slots == 2) scores(1, n == 1);
+        }
+        __syncwarp();
+        if (C::kAhead && slots == 2) {
+          // half a tile later than slot 0's: the exponentials of one slot then fall into the other's
+          // waits (1048 us when both begin together)
+          ok = wait(&bars.s_read[0], r_phase & 1) && ok;
+          tc_fence_after();
+          if (elect_one()) scores(1, n == 1);
+          __syncwarp();
         }
         ka.step();
-        for (int j = 0; j < n; ++j) {
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          const int sv = va.stage;
-          const bool more = j + 1 < n;
-          ok = wait(&bars.v_ok[sv], va.phase) && ok;
-          va.step();
-          for (int slot = 0; slot < slots; ++slot) {
-            const uint32_t parity = (p_phase >> slot) & 1;
+        if constexpr (C::kAhead) {
+          // Slot 1 is half a tile behind: scores of slot 0's next tile, products of slot 1's last
+          // weights, scores of its next tile, products of slot 0's weights.
+          const auto next_scores = [&](int slot, bool last_tile) {
+            ok = wait(&bars.s_read[slot], (r_phase >> slot) & 1) && ok;
+            r_phase ^= 1u << slot;
+            tc_fence_after();
+            if (elect_one()) scores(slot, last_tile);
+            __syncwarp();
+          };
+          const auto products = [&](int slot, int stage, bool first) {
+            ok = wait(&bars.p_full[slot], (p_phase >> slot) & 1) && ok;
             p_phase ^= 1u << slot;
-            if (C::kEarly) {
-              ok = wait(&bars.p_full[slot][0], parity) && ok;
-              tc_fence_after();
-              if (elect_one()) pv(slot, sv, 0, j == 0);
-            }
-            if (more && slot == 0) ok = wait(&bars.k_full[ka.stage], ka.phase) && ok;
-            ok = wait(&bars.p_full[slot][1], parity) && ok;
             tc_fence_after();
             if (elect_one()) {
-              if (!C::kEarly) pv(slot, sv, 0, j == 0);
-              pv(slot, sv, 1, j == 0);
-              if (more) scores(slot, j + 2 == n);
-              else mma_commit(&bars.o_full[slot]);
-              if (slot == slots - 1) mma_commit(&bars.v_empty[sv]);
+              pv(slot, stage, 0, first);
+              pv(slot, stage, 1, first);
+              mma_commit(&bars.o_full[slot]);
+              if (slot == slots - 1) mma_commit(&bars.v_empty[stage]);
             }
+            __syncwarp();
+          };
+          int sv = 0;
+          for (int j = 0; j < n; ++j) {
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const bool more = j + 1 < n;
+            if (more) {
+              ok = wait(&bars.k_full[ka.stage], ka.phase) && ok;
+              next_scores(0, j + 2 == n);
+            }
+            if (slots == 2) {
+              if (j > 0) products(1, sv, j == 1);
+              if (more) next_scores(1, j + 2 == n);
+            }
+            if (more) ka.step();
+            sv = va.stage;
+            ok = wait(&bars.v_ok[sv], va.phase) && ok;
+            va.step();
+            products(0, sv, j == 0);
           }
-          if (more) ka.step();
+          if ((ok = __all_sync(0xffffffffu, ok)) && slots == 2) products(1, sv, n == 1);
+          // (the last scores were read before their weights came)
+          r_phase ^= slots == 2 ? 3u : 1u;
+        } else {
+          for (int j = 0; j < n; ++j) {
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const int sv = va.stage;
+            const bool more = j + 1 < n;
+            ok = wait(&bars.v_ok[sv], va.phase) && ok;
+            va.step();
+            for (int slot = 0; slot < slots; ++slot) {
+              const uint32_t parity = (p_phase >> slot) & 1;
+              p_phase ^= 1u << slot;
+              ok = wait(&bars.p_half[slot], parity) && ok;
+              tc_fence_after();
+              if (elect_one()) pv(slot, sv, 0, j == 0);
+              __syncwarp();
+              if (more && slot == 0) ok = wait(&bars.k_full[ka.stage], ka.phase) && ok;
+              ok = wait(&bars.p_full[slot], parity) && ok;
+              tc_fence_after();
+              if (elect_one()) {
+                pv(slot, sv, 1, j == 0);
+                if (more) scores(slot, j + 2 == n);
+                else mma_commit(&bars.o_full[slot]);
+                if (slot == slots - 1) mma_commit(&bars.v_empty[sv]);
+              }
+              __syncwarp();
+            }
+            if (more) ka.step();
+          }
         }
         ok = __all_sync(0xffffffffu, ok);
       }
@@ -554,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = slot * kSlotRows + (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = lanes + slot * 128, o_col = lanes + C::kColO + slot * D;
+    const uint32_t p_col = lanes + C::kColP + slot * C::kStepP;
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
     uint32_t s_phase = 0, o_phase = 0, unit = 0;
     bool ok = true;
@@ -576,6 +632,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
         tmem_ld_wait();
+        if (C::kAhead) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.s_read[slot]);
+        }
         if (edge_tile(p, u.tiles, tile)) {
           // bit i of a word: key s0 + i is seen (i <= hi and (i > lo or i < first))
           const int32_t s0 = tile * kTileTc;
@@ -604,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = top;
           l *= alpha;
         }
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        const auto rescale = [&] {
+          if (j == 0 || !__any_sync(0xffffffffu, alpha != 1.f)) return;
           // (rare: short code, which would push the rest out of the instruction cache)
 #pragma unroll(D == 128 ? 1 : 2)
           for (int c = 0; c < D / 32; ++c) {
@@ -616,43 +678,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * alpha);
             tmem_st32(o_col + c * 32, w);
           }
-        }
+        };
+        if (!C::kAhead) rescale();
         const float sub = m == -INFINITY ? 0.f : -m;
         const uint64_t sub2 = pack_f32x2(sub, sub);
         uint64_t sum2[2] = {0, 0};
+        uint32_t w2[2][32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
+          uint32_t(&w)[32] = w2[c];
 #pragma unroll
-          for (int g = 0; g < 32; g += 8) {
-            float2 x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float(&v)[32] = s[2 * c + ((g + i) >> 4)];
-              const int e = ((g + i) & 15) * 2;
-              x[i] = unpack_f32x2(fma_f32x2(pack_f32x2(v[e], v[e + 1]), scale2, sub2));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              x[i].x = exp2_ordered(x[i].x);
-              x[i].y = exp2_ordered(x[i].y);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x[i].x, x[i].y));
-              // the weights are rounded to T for the second product (half a step of T
-              // each); their sum is of the unrounded ones
-              w[g + i] = pack2<T>(x[i].x, x[i].y);
-            }
+          for (int i = 0; i < 32; ++i) {
+            const float(&v)[32] = s[2 * c + (i >> 4)];
+            const int e = (i & 15) * 2;
+            const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(v[e], v[e + 1]), scale2, sub2));
+            const float a = exp2_approx(x.x), b = exp2_approx(x.y);
+            sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(a, b));
+            // the weights are rounded to T for the second product (half a step of T
+            // each); their sum is of the unrounded ones
+            w[i] = pack2<T>(a, b);
           }
-          tmem_st32(s_col + c * 32, w);
-          if (C::kEarly || c == 1) {
+          if (C::kAhead) {
+            if (c == 0) continue;
+            if (j > 0) {
+              // the last tile's products are done with its weights and with the accumulator
+              if (!(ok = wait_warp(&bars.o_full[slot], o_phase))) break;
+              o_phase ^= 1;
+              tc_fence_after();
+              rescale();
+            }
+            tmem_st32(p_col, w2[0]);
+          }
+          tmem_st32(p_col + c * 32, w);
+          if (!C::kAhead || c == 1) {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.p_full[slot][c]);
+            if (lane == 0) mbar_arrive(c ? &bars.p_full[slot] : &bars.p_half[slot]);
           }
         }
+        if (C::kAhead && !ok) break;
         const float2 sum = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
         l += sum.x + sum.y;
       }
