@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto rescale = [&] {
           if (j == 0 || !__any_sync(0xffffffffu, alpha != 1.f)) return;
           // (rare: short code, which would push the rest out of the instruction cache)
-#pragma unroll(D == 128 ? 1 : 2)
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
             tmem_ld32(o_col + c * 32, o);
