@@ -27,8 +27,8 @@ constexpr float kLazyRaise = 8.f;
 template <int D>
 struct TcCfg {
   // At D = 64 the accumulators leave room for the weights beside the scores: the next tile's scores
-  // are then computed while this one's weights are (2 x 8192 tokens, 64/8 heads: 1056 -> 996 us;
-  // units of 128 rows 99 -> 87 us). At D = 128 the weights lie over the scores, and the second
+  // are then computed while this one's weights are (2 x 8192 tokens, 64/8 heads: 1056 ->
+  // 1030 us; windowed prefill 146 -> 140 us; units of 128 rows 99 -> 82 us). At D = 128 the weights lie over the scores, and the second
   // product begins with the first half of a tile's keys.
   static constexpr bool kAhead = D == 64;
   // Tensor memory: scores of slot i at 128 i, its accumulator at kColO + D i, its weights at
@@ -426,17 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (last_tile) mma_commit(&bars.q_empty);
           }
         };
-        if (elect_one()) {
-          scores(0, n == 1);
-          if (!C::kAhead && slots == 2) scores(1, n == 1);
-        }
-        __syncwarp();
-        if (C::kAhead && slots == 2) {
-          // half a tile later than slot 0's: the exponentials of one slot then fall into the other's
-          // waits (1048 us when both begin together)
-          ok = wait(&bars.s_read[0], r_phase & 1) && ok;
-          tc_fence_after();
-          if (elect_one()) scores(1, n == 1);
+        // (This and the loops over slots below stay rolled: the code of all roles shares the
+        // instruction cache. Unrolled, a window of 1024 + 16 takes 367 us instead of 356 at D = 64.)
+#pragma unroll 1
+        for (int slot = 0; slot < slots; ++slot) {
+          if (C::kAhead && slot == 1) {
+            // half a tile later than slot 0's: the exponentials of one slot then fall into the
+            // other's waits (5 % faster than beginning together)
+            ok = wait(&bars.s_read[0], r_phase & 1) && ok;
+            tc_fence_after();
+          }
+          if (elect_one()) scores(slot, n == 1);
           __syncwarp();
         }
         ka.step();
@@ -463,24 +463,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           };
           int sv = 0;
-          for (int j = 0; j < n; ++j) {
+          // (the last round has slot 1's products alone)
+          for (int j = 0; j < n + slots - 1; ++j) {
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             const bool more = j + 1 < n;
-            if (more) {
-              ok = wait(&bars.k_full[ka.stage], ka.phase) && ok;
-              next_scores(0, j + 2 == n);
-            }
-            if (slots == 2) {
-              if (j > 0) products(1, sv, j == 1);
-              if (more) next_scores(1, j + 2 == n);
+            if (more) ok = wait(&bars.k_full[ka.stage], ka.phase) && ok;
+#pragma unroll 1
+            for (int half = 0; half < slots; ++half) {
+              if (more) next_scores(half, j + 2 == n);
+              const int of = half + 1 == slots ? j : j - 1;  // the tile whose weights are due
+              if (of == j && j < n) {
+                sv = va.stage;
+                ok = wait(&bars.v_ok[sv], va.phase) && ok;
+                va.step();
+              }
+              if (of >= 0 && of < n) products(slots - 1 - half, sv, of == 0);
             }
             if (more) ka.step();
-            sv = va.stage;
-            ok = wait(&bars.v_ok[sv], va.phase) && ok;
-            va.step();
-            products(0, sv, j == 0);
           }
-          if ((ok = __all_sync(0xffffffffu, ok)) && slots == 2) products(1, sv, n == 1);
           // (the last scores were read before their weights came)
           r_phase ^= slots == 2 ? 3u : 1u;
         } else {
@@ -490,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = j + 1 < n;
             ok = wait(&bars.v_ok[sv], va.phase) && ok;
             va.step();
+#pragma unroll 1
             for (int slot = 0; slot < slots; ++slot) {
               const uint32_t parity = (p_phase >> slot) & 1;
               p_phase ^= 1u << slot;
