@@ -339,6 +339,38 @@ __device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8
   }
 }
 
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address, in the cluster's window, of a shared-memory address of this block in block `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Per unit of 16 * MT query rows of one kv head: the four warps take a quarter
 // of every tile's keys each (16 at D = 128, 32 at D = 64), with a ring of kStages sub-tiles of K and V per
 // warp that its own lanes fill with 16-byte asynchronous copies (so no warp
@@ -346,7 +378,12 @@ __device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8
 // maximum and sum per row; the warps' results are joined through shared memory
 // at the end of the piece. Bound by HBM (or L2) bytes of K and V when few rows
 // share a key: 4 * D bytes of a key feed 4 * D * 16 * MT multiply-adds.
-template <typename T, int D, int MT, bool kSel>
+//
+// kCluster, for calls of few short units: nothing is planned, every unit (the
+// units of every request and kv head) belongs to a cluster whose blocks take equal
+// ranges of its tiles and join their results in each other's shared memory, so
+// that one launch does all.
+template <typename T, int D, int MT, bool kSel, bool kCluster>
 __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const AttendParams p) {
   using C = RowsCfg<D, MT>;
   constexpr int kChunks = D / 8;         // 16-byte chunks of a row
@@ -355,6 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
   __shared__ uint32_t s_valid[kWarps][kStages];
+  __shared__ float2 s_part[kCluster ? C::kRows : 1];  // maximum and sum of the block's rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cta = blockIdx.x;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * C::kStageBytes);
@@ -367,7 +405,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   // this CTA's range of the units
   int64_t unit = 0, unit_end = 0;
   int32_t first_tile = 0, last_tile = 0, req_token = -1, req = -1;
-  if constexpr (kSel) {
+  const int rank = kCluster ? cluster_rank() : 0;
+  const int64_t mine = kCluster ? cta / p.cluster : 0;  // this cluster's unit, or request and kv head
+  ReqShape shape{};
+  if constexpr (kCluster) {
+    if (kSel) {
+      unit = mine;
+      unit_end = mine + 1;
+    } else {
+      req = static_cast<int32_t>(mine / p.num_kv_heads);
+      shape = request_shape(p, req, cta == req * p.num_kv_heads * p.cluster);
+      unit_end = request_entries(p, shape);
+    }
+  } else if constexpr (kSel) {
     const int64_t units = selected_units(p);
     const int2 a = selected_cut(p, units, cta), b = selected_cut(p, units, cta + 1);
     unit = a.x;
@@ -376,7 +426,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
     last_tile = b.y;
   }
   PieceWalk<false> walk;
-  if constexpr (!kSel) {
+  if constexpr (!kSel && !kCluster) {
     if (p.self_plan) {
       __shared__ int64_t sums[32];
       __shared__ int4 cuts[2];
@@ -411,8 +461,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       u.t1 = last ? last_tile : u.tiles.count;
       ++unit;
       first_tile = 0;
+    } else if constexpr (kCluster) {
+      if (unit >= unit_end) break;
+      const int32_t entry = static_cast<int32_t>(unit++);
+      u.req = req;
+      u.head = static_cast<int32_t>(mine % p.num_kv_heads);
+      u.row0 = entry * p.rows;
+      u.rows = min(p.rows, shape.nq * p.group - u.row0);
+      u.q0 = shape.q0;
+      u.ahead = shape.keys - shape.nq;
+      u.tiles = unit_tiles(p, shape, entry);
     } else {
       if (!walk.next(p, &u)) break;
+    }
+    if constexpr (kCluster) {
+      u.t0 = u.tiles.count * rank / p.cluster;
+      u.t1 = u.tiles.count * (rank + 1) / p.cluster;
     }
     const bool whole = u.whole();
 
@@ -636,6 +700,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
                 make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
         }
       __syncthreads();
+      const auto write_row = [&](int r, int d, float mx, float sum, const float4& v) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        int64_t token;
+        int head, pos;
+        row_place(p, u, r, &token, &head, &pos);
+        const int64_t at = token * p.num_heads + head;
+        const uint2 b = make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * D + d) = b;
+        if (d == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
+      };
       for (int i = threadIdx.x; i < u.rows * (D / 4); i += kWarps * 32) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float mx = -INFINITY;
@@ -655,20 +729,57 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
           v.z += f * a.z;
           v.w += f * a.w;
         }
-        if (whole) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          int64_t token;
-          int head, pos;
-          row_place(p, u, r, &token, &head, &pos);
-          const int64_t at = token * p.num_heads + head;
-          const uint2 b = make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
-          *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * D + d) = b;
-          if (d == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
+        if constexpr (kCluster) {
+          // (where the thread's first summand was)
+          *reinterpret_cast<float4*>(join + r * kPitch + d) = v;
+          if (d == 0) s_part[r] = make_float2(mx, sum);
+        } else if (whole) {
+          write_row(r, d, mx, sum, v);
         } else {
           const int64_t slot = 2 * static_cast<int64_t>(cta) + (u.t0 == 0 ? 1 : 0);
           *reinterpret_cast<float4*>(p.part_o + (slot * p.rows + r) * D + d) = v;
           if (d == 0) p.part_ml[slot * p.rows + r] = make_float2(mx, sum);
         }
+      }
+      if constexpr (kCluster) {
+        // ---- join of the cluster's blocks, in their order; each writes a share of the unit
+        cluster_sync();
+        for (int i = rank * (kWarps * 32) + threadIdx.x; i < u.rows * (D / 4);
+             i += p.cluster * (kWarps * 32)) {
+          const int r = i / (D / 4), d = i % (D / 4) * 4;
+          const uint32_t part_at = smem_u32(&s_part[r]), o_at = smem_u32(join + r * kPitch + d);
+          float bm[kMostCluster], bl[kMostCluster];
+          float4 bo[kMostCluster];
+#pragma unroll
+          for (int b = 0; b < kMostCluster; ++b) {
+            bm[b] = -INFINITY;
+            bl[b] = 0.f;
+            bo[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (b < p.cluster) {
+              const uint32_t at = cluster_addr(part_at, b);
+              bm[b] = cluster_load(at);
+              bl[b] = cluster_load(at + 4);
+              bo[b] = cluster_load4(cluster_addr(o_at, b));
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < kMostCluster; ++b) mx = fmaxf(mx, bm[b]);
+          const float base = mx == -INFINITY ? 0.f : mx;
+          float sum = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int b = 0; b < kMostCluster; ++b) {
+            const float f = exp2_approx(bm[b] - base);
+            sum += f * bl[b];
+            v.x += f * bo[b].x;
+            v.y += f * bo[b].y;
+            v.z += f * bo[b].z;
+            v.w += f * bo[b].w;
+          }
+          write_row(r, d, mx, sum, v);
+        }
+        cluster_sync();  // (the results are read before their memory is used again)
       }
       __syncthreads();
     }
@@ -1002,11 +1113,33 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(cons
 template <typename T, int D, int MT, bool kSel>
 idx_status launch_rows_as(const AttendParams& p, cudaStream_t s) {
   using C = RowsCfg<D, MT>;
-  const auto kernel = attend_rows_kernel<T, D, MT, kSel>;
+  const auto kernel = attend_rows_kernel<T, D, MT, kSel, false>;
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_pdl(kernel, p.grid, kWarps * 32, C::kSmem, s, p));
+}
+
+template <typename T, int D, bool kSel>
+idx_status launch_cluster_as(const AttendParams& p, cudaStream_t s) {
+  using C = RowsCfg<D, 1>;
+  const auto kernel = attend_rows_kernel<T, D, 1, kSel, true>;
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
+  if (e != cudaSuccess) return cuda_status(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 template <typename T, int D>
@@ -1021,6 +1154,8 @@ idx_status launch_lists_as(const AttendParams& p, cudaStream_t s) {
 
 template <typename T, int D>
 idx_status launch_rows_d(const AttendParams& p, int mt, cudaStream_t s) {
+  if (p.cluster)
+    return p.indices ? launch_cluster_as<T, D, true>(p, s) : launch_cluster_as<T, D, false>(p, s);
   if (!p.indices) return launch_rows_as<T, D, 1, false>(p, s);
   return mt == 1 ? launch_rows_as<T, D, 1, true>(p, s) : launch_rows_as<T, D, 2, true>(p, s);
 }

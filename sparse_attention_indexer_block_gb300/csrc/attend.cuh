@@ -55,6 +55,7 @@ struct AttendParams {
   int32_t max_entries;
   int32_t self_plan;               // the CTAs work `bound` out for themselves
   int32_t min_cost;                // least work of a CTA, in tiles
+  int32_t cluster;                 // row-block kernel: blocks that share a unit; 0: a plan cuts
   int32_t grid;                    // CTAs of the row-block launch
   int32_t rows;                    // query rows of a unit
   int32_t tile_log2;               // keys of a tile
@@ -379,6 +380,7 @@ __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost
 // scan of the requests' costs each, against a launch of the planning kernel
 // (4 us).
 constexpr int kSelfPlanReqs = 512, kSelfPlanEntries = 8;
+constexpr int kMostCluster = 8;
 
 // The cuts at both ends of a CTA's range and its first request's shape, by its
 // kThreads threads; `cost` has room for num_reqs + 1. p.bound gets them too, for the join.

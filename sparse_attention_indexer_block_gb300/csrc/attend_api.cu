@@ -77,6 +77,20 @@ bool warp_per_list(const AttendParams& p, int head_dim, const Variant& v) {
   return warp_time < cta_time;
 }
 
+// Blocks of a cluster that share each of `units` units of at most `tiles` tiles, with no plan, no
+// partial results in memory and no second launch; 0 where cutting all tiles evenly over the device
+// is faster. A block takes 0.9 us a tile and 4; the cut's blocks take fewer tiles, but 11 more (for a
+// list, whose units are cut late, 15). us, cut / cluster, D = 128, 8 kv heads: one request of 1000
+// keys 11.5 / 6.2, 6000: 16.0 / 14.5, 12 000: 18.6 / 24.3; 16 of 1000: 19.1 / 13.3, of 3000: 40 /
+// 35; 4 tokens with lists of 512: 18.1 / 6.2, 32 with 2048: 37 / 32. `most` bounds a block's tiles
+// where lengths may differ, for only the cut evens them out.
+int cluster_blocks(int64_t units, int64_t tiles, int64_t slack, int64_t most, const Variant& v) {
+  int c = kMostCluster;
+  while (c > 1 && (units * c > v.grid || c >= 2 * tiles)) c /= 2;
+  const int64_t one = (tiles + c - 1) / c;
+  return units * c <= v.grid && one <= most && one <= tiles * units / v.grid + slack ? c : 0;
+}
+
 Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 3, 4}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
@@ -215,6 +229,18 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
   const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim, false);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!tc && longest * p.group <= v.rows) {
+    // (a window's tiles: those of the sinks, and the window and the new tokens, cut at both ends)
+    const int64_t tile = int64_t{1} << v.tile_log2;
+    const int64_t all = (a->bt_width * int64_t{kPageTokens} + tile - 1) / tile;
+    const int64_t seen = p.sinks_tiles + (p.window + longest + tile - 1) / tile + 1;
+    const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads;
+    p.cluster = cluster_blocks(units, std::min(all, seen), 10, 16, v);
+    if (p.cluster) {
+      p.grid = static_cast<int32_t>(units * p.cluster);
+      return launch_attend_rows(p, a->head_dim, half, v.mt, s);
+    }
+  }
   p.self_plan = !tc && a->num_reqs <= kSelfPlanReqs &&
                 longest * p.group <= kSelfPlanEntries * int64_t{v.rows};
   if (!p.self_plan && (st = launch_attend_plan(p, s)) != IDX_OK) return st;
@@ -239,12 +265,18 @@ idx_status indexer_attend_selected(const idx_attend* a, void* stream) {
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool half = a->dtype == IDX_FP16;
-  if (warp_per_list(p, a->head_dim, v)) {
+  if (v.mt == 1) {
+    const int64_t tile = int64_t{1} << v.tile_log2;
+    const int64_t units = static_cast<int64_t>(a->num_tokens) * p.num_kv_heads;
+    p.cluster = cluster_blocks(units, (a->topk + tile - 1) / tile, 14, INT32_MAX, v);
+    if (p.cluster) p.grid = static_cast<int32_t>(units * p.cluster);
+  }
+  if (!p.cluster && warp_per_list(p, a->head_dim, v)) {
     p.rows = 16;
     p.tile_log2 = a->head_dim == 64 ? 5 : 4;
     return launch_attend_lists(p, a->head_dim, half, s);
   }
-  if ((st = launch_attend_rows(p, a->head_dim, half, v.mt, s)) != IDX_OK) return st;
+  if ((st = launch_attend_rows(p, a->head_dim, half, v.mt, s)) != IDX_OK || p.cluster) return st;
   return launch_attend_combine(p, a->head_dim, half, s);
 }
 

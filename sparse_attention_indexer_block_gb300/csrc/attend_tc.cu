@@ -27,9 +27,9 @@ constexpr float kLazyRaise = 8.f;
 template <int D>
 struct TcCfg {
   // At D = 64 the accumulators leave room for the weights beside the scores: the next tile's scores
-  // are then computed while this one's weights are (2 x 8192 tokens, 64/8 heads: 1056 ->
-  // 1030 us; windowed prefill 146 -> 140 us; units of 128 rows 99 -> 82 us). At D = 128 the weights lie over the scores, and the second
-  // product begins with the first half of a tile's keys.
+  // are then computed while this one's weights are (2 x 8192 tokens, 64/8 heads: 1056 -> 1030 us;
+  // windowed prefill 146 -> 140 us; units of 128 rows 99 -> 82 us). At D = 128 the weights lie over
+  // the scores, and the second product begins with the first half of a tile's keys.
   static constexpr bool kAhead = D == 64;
   // Tensor memory: scores of slot i at 128 i, its accumulator at kColO + D i, its weights at
   // kColP + kStepP i
