@@ -588,7 +588,7 @@ typedef struct idx_attend {
   const int32_t* indices;         /* [num_tokens, topk], row stride indices_stride (selected form) */
   void* out;
   float* lse;                     /* nullable, [num_tokens, num_heads] */
-  void* workspace;                /* 256-byte aligned */
+  void* workspace;                /* 256-byte aligned (nullable: see below) */
   size_t workspace_bytes;
   uint32_t* dev_error;            /* nullable */
   int64_t q_stride_token, q_stride_head;
@@ -606,7 +606,9 @@ typedef struct idx_attend {
 } idx_attend;
 
 /* Bytes of workspace either attention call needs at most for these sizes, on
- * the current CUDA device. */
+ * the current CUDA device. Calls of few short units (small decode steps) need
+ * none: a call with a null workspace of 0 bytes returns IDX_ERR_WORKSPACE, before
+ * any work, when it does need one. */
 idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, int32_t num_heads,
                                           int32_t num_kv_heads, int32_t head_dim, size_t* bytes);
 

@@ -566,7 +566,8 @@ def indexer_decode_topk_noalloc(q, weights, index_cache, block_table, row_seq_le
 # What they allocate (outputs, workspaces) belongs to the stream they run on.
 # ---------------------------------------------------------------------------
 
-_INVALID, _UNSUPPORTED = 1, 2
+_INVALID, _UNSUPPORTED, _WORKSPACE = 1, 2, 3
+_FEW_UNITS = 304  # (request or token, kv head) pairs: calls of more always use a workspace
 _I32T, _F32T = torch.int32, torch.float32
 
 
@@ -579,11 +580,12 @@ def _need_i32(name, what, t, *shape):
     if not isinstance(t, torch.Tensor) or t.dtype is not _I32T:
         _refuse(name, f"{what} must be an int32 tensor")
     got = t.shape
-    if len(got) != len(shape):
-        _refuse(name, f"{what} has shape {tuple(got)}")
-    for a, n in zip(got, shape):
-        if n is not None and a != n:
+    if got != shape:
+        if len(got) != len(shape):
             _refuse(name, f"{what} has shape {tuple(got)}")
+        for a, n in zip(got, shape):
+            if n is not None and a != n:
+                _refuse(name, f"{what} has shape {tuple(got)}")
     if not t.is_contiguous() and t.stride(-1) != 1 and got[-1] > 1:
         _refuse(name, f"{what} must be contiguous in its last dimension")
 
@@ -628,7 +630,7 @@ class _On:
     def __init__(self, index, stream):
         self.guard = None
         self.index = index
-        if stream is None and torch.cuda.current_device() == index:
+        if stream is None and torch._C._cuda_getDevice() == index:
             return
         device = torch.device("cuda", index)
         if stream is None:
@@ -722,19 +724,28 @@ def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, i
             out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
         if lse is None:
             lse = torch.empty((tokens, heads), dtype=_F32T, device=q.device)
+        call = getattr(load(), name)
+
+        def run(at, size):
+            return call(_ATTEND_BYTES.pack(
+                q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                0 if seq_lens is None else seq_lens.data_ptr(), query_start_loc.data_ptr(),
+                0 if indices is None else indices.data_ptr(), out.data_ptr(), lse.data_ptr(), at, size,
+                0 if dev_error is None else dev_error.data_ptr(),
+                qt, qh, kp, kt, kh, vp, vt, vh, pages, bt_stride, idx_stride, bt_width, reqs, tokens,
+                heads, kv_heads, dim, _ATTEND_TYPES[dtype], max_query_len, window, sinks, topk,
+                dim ** -0.5 if scale is None else scale), s)
+
+        st = _WORKSPACE
         if workspace is None:
-            workspace = torch.empty(_attend_workspace_bytes(index, tokens, reqs, heads, kv_heads, dim),
-                                    dtype=torch.uint8, device=q.device)
-        a = _ATTEND_BYTES.pack(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-            0 if seq_lens is None else seq_lens.data_ptr(), query_start_loc.data_ptr(),
-            0 if indices is None else indices.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            0 if dev_error is None else dev_error.data_ptr(),
-            qt, qh, kp, kt, kh, vp, vt, vh, pages, bt_stride, idx_stride, bt_width, reqs, tokens,
-            heads, kv_heads, dim, _ATTEND_TYPES[dtype], max_query_len, window, sinks, topk,
-            dim ** -0.5 if scale is None else scale)
-        st = getattr(load(), name)(a, s)
+            # (small steps need no workspace: the call says so)
+            if (reqs if indices is None else tokens) * kv_heads <= _FEW_UNITS:
+                st = run(0, 0)
+            if st == _WORKSPACE:
+                workspace = torch.empty(_attend_workspace_bytes(index, tokens, reqs, heads, kv_heads, dim),
+                                        dtype=torch.uint8, device=q.device)
+        if workspace is not None:
+            st = run(workspace.data_ptr(), workspace.numel() * workspace.element_size())
         if st:
             _check(name, st)
     return out, lse

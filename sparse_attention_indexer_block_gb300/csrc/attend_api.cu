@@ -130,7 +130,8 @@ idx_status check_attend(const idx_attend* a) {
       !stride_ok(a->k_stride_head) || !stride_ok(a->v_stride_page) ||
       !stride_ok(a->v_stride_token) || !stride_ok(a->v_stride_head))
     return IDX_ERR_INVALID_ARG;
-  if (!a->workspace || !aligned(a->workspace, 256)) return IDX_ERR_INVALID_ARG;
+  if ((!a->workspace && a->workspace_bytes) || !aligned(a->workspace, 256))
+    return IDX_ERR_INVALID_ARG;
   return IDX_OK;
 }
 
@@ -166,7 +167,7 @@ AttendParams attend_params(const idx_attend* a) {
   return p;
 }
 
-idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& v) {
+void set_variant(AttendParams* p, const Variant& v) {
   p->rows = v.rows;
   p->tile_log2 = v.tile_log2;
   p->sinks_tiles = static_cast<int32_t>((static_cast<int64_t>(p->sinks) + (1 << v.tile_log2) - 1) >>
@@ -174,6 +175,10 @@ idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& 
   p->grid = v.grid;
   p->unit_overhead = v.overhead;
   p->min_cost = v.min_cost;
+}
+
+idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& v) {
+  if (p->cluster && !a->workspace) return IDX_OK;
   p->max_entries =
       static_cast<int32_t>(entry_bound(a->num_tokens, a->num_reqs, p->group, v.rows));
   const AttendWs w = attend_ws(a->num_reqs, p->max_entries, v.grid, v.rows, a->head_dim);
@@ -227,8 +232,7 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
   const bool tc =
       longest * p.group > 16 && attend_tc_maps(p, a->head_dim, half, &kmap, &vmap);
   const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim, false);
-  if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  set_variant(&p, v);
   if (!tc && longest * p.group <= v.rows) {
     // (a window's tiles: those of the sinks, and the window and the new tokens, cut at both ends)
     const int64_t tile = int64_t{1} << v.tile_log2;
@@ -236,11 +240,11 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
     const int64_t seen = p.sinks_tiles + (p.window + longest + tile - 1) / tile + 1;
     const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads;
     p.cluster = cluster_blocks(units, std::min(all, seen), 10, 16, v);
-    if (p.cluster) {
-      p.grid = static_cast<int32_t>(units * p.cluster);
-      return launch_attend_rows(p, a->head_dim, half, v.mt, s);
-    }
+    if (p.cluster) p.grid = static_cast<int32_t>(units * p.cluster);
   }
+  if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.cluster) return launch_attend_rows(p, a->head_dim, half, v.mt, s);
   p.self_plan = !tc && a->num_reqs <= kSelfPlanReqs &&
                 longest * p.group <= kSelfPlanEntries * int64_t{v.rows};
   if (!p.self_plan && (st = launch_attend_plan(p, s)) != IDX_OK) return st;
@@ -262,15 +266,16 @@ idx_status indexer_attend_selected(const idx_attend* a, void* stream) {
   p.topk = a->topk;
   p.same_strides = p.k_stride_page == p.v_stride_page && p.k_stride_token == p.v_stride_token;
   const Variant v = rows_variant(p.group <= 16 ? 1 : 2, a->head_dim, true);
-  if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool half = a->dtype == IDX_FP16;
+  set_variant(&p, v);
   if (v.mt == 1) {
     const int64_t tile = int64_t{1} << v.tile_log2;
     const int64_t units = static_cast<int64_t>(a->num_tokens) * p.num_kv_heads;
     p.cluster = cluster_blocks(units, (a->topk + tile - 1) / tile, 14, INT32_MAX, v);
     if (p.cluster) p.grid = static_cast<int32_t>(units * p.cluster);
   }
+  if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool half = a->dtype == IDX_FP16;
   if (!p.cluster && warp_per_list(p, a->head_dim, v)) {
     p.rows = 16;
     p.tile_log2 = a->head_dim == 64 ? 5 : 4;

@@ -98,3 +98,12 @@ def test_given_outputs_and_a_captured_step():
         graph.replay()
     side.synchronize()
     b.check((out, lse), want)
+
+
+def test_a_given_workspace_changes_nothing():
+    b = Batch([1, 2], [500, 70], 8, 2, 128, BF, seed=341)
+    idx = _lists(b, 200)
+    ws = saib.attend_workspace(3, 2, 8, 2, 128, DEV)
+    for a, c in ((b.attend(), b.attend(workspace=ws)),
+                 (b.attend_selected(idx), b.attend_selected(idx, workspace=ws))):
+        assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])

@@ -223,3 +223,12 @@ def test_binding_refuses_page_tensors():
     for call in calls:
         with pytest.raises(saib.IndexerError):
             call()
+
+
+def test_a_call_that_needs_a_workspace_says_so(lib):
+    """A null workspace of 0 bytes: refused before any work unless the call needs none."""
+    none = dict(workspace=None, workspace_bytes=0)
+    assert lib.indexer_attend_paged(C.byref(_args(max_query_len=100, **none)), None) == WORKSPACE
+    assert lib.indexer_attend_paged(C.byref(_args(num_reqs=5000, num_tokens=5000, **none)), None) == WORKSPACE
+    assert lib.indexer_attend_paged(C.byref(_args(bt_width=4000, bt_stride=4000, **none)), None) == WORKSPACE
+    assert lib.indexer_attend_selected(C.byref(_args(num_tokens=5000, **none)), None) == WORKSPACE
