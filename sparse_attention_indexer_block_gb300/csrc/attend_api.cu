@@ -91,6 +91,8 @@ int cluster_blocks(int64_t units, int64_t tiles, int64_t slack, int64_t most, co
   return units * c <= v.grid && one <= most && one <= tiles * units / v.grid + slack ? c : 0;
 }
 
+constexpr int64_t kLittleTiles = 12;  // a block's
+
 Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 3, 4}; }
 
 size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
@@ -233,19 +235,25 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
       longest * p.group > 16 && attend_tc_maps(p, a->head_dim, half, &kmap, &vmap);
   const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim, false);
   set_variant(&p, v);
+  // (a window's tiles: those of the sinks, and the window and the new tokens, cut at both ends)
+  const int64_t tile = int64_t{1} << v.tile_log2;
+  const int64_t tiles =
+      std::min((a->bt_width * int64_t{kPageTokens} + tile - 1) / tile,
+               p.sinks_tiles + (p.window + longest + tile - 1) / tile + 1);
   if (!tc && longest * p.group <= v.rows) {
-    // (a window's tiles: those of the sinks, and the window and the new tokens, cut at both ends)
-    const int64_t tile = int64_t{1} << v.tile_log2;
-    const int64_t all = (a->bt_width * int64_t{kPageTokens} + tile - 1) / tile;
-    const int64_t seen = p.sinks_tiles + (p.window + longest + tile - 1) / tile + 1;
     const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads;
-    p.cluster = cluster_blocks(units, std::min(all, seen), 10, 16, v);
+    p.cluster = cluster_blocks(units, tiles, 10, 16, v);
     if (p.cluster) p.grid = static_cast<int32_t>(units * p.cluster);
   }
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.cluster) return launch_attend_rows(p, a->head_dim, half, v.mt, s);
-  p.self_plan = !tc && a->num_reqs <= kSelfPlanReqs &&
+  // The chunk kernel's blocks plan for themselves when there is little work: a launch less is 4 us
+  // less of the host's time, which is what such calls take (100 tokens of a first prompt: 33 us a
+  // call, then 29; on the device 256 tokens 20.9, then 15.7). The cuts of the planning kernel are
+  // finer (26 requests of up to 9000 keys 130 us, else 134).
+  const bool little = int64_t{p.max_entries} * p.num_kv_heads * tiles <= kLittleTiles * v.grid;
+  p.self_plan = (!tc || little) && a->num_reqs <= kSelfPlanReqs &&
                 longest * p.group <= kSelfPlanEntries * int64_t{v.rows};
   if (!p.self_plan && (st = launch_attend_plan(p, s)) != IDX_OK) return st;
   st = tc ? launch_attend_tc(p, a->head_dim, half, kmap, vmap, s)

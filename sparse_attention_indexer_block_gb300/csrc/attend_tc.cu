@@ -57,6 +57,7 @@ struct TcBars {
   uint64_t done;
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   Piece piece[kPieces];  // what the CTA works on, in order; req -1: no more
+  int4 cut_end;          // kSelfPlan: where this CTA's range ends
   uint32_t tmem_base;
   int abort_flag;
   uint32_t odd[kOddUnits];  // 1 + the last unit whose edge tiles held infinities or NaNs
@@ -230,7 +231,10 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u,
 // D = 128 and some 1200 at D = 64, the exponentials 1050; it takes 2900 and 2050,
 // for a row's chain of scores, maximum, exponentials and products is longer than
 // either, and two slots do not hide all of it.
-template <typename T, int D>
+//
+// kSelfPlan: the blocks work out their ranges themselves. (A kernel of its own: with the code in
+// one, the others take 5 % longer.)
+template <typename T, int D, bool kSelfPlan>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
@@ -288,6 +292,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
+  if constexpr (kSelfPlan) {
+    __shared__ int64_t sums[32];
+    __shared__ int4 cuts[2];
+    __shared__ ReqShape first;
+    // (the costs lie where the queries will: written by these threads too, not by TMA; the cuts
+    // are in p.bound as well)
+    self_plan<kThreads>(p, blockIdx.x, reinterpret_cast<int64_t*>(smem), sums, cuts, &first);
+    if (threadIdx.x == 0) bars.cut_end = cuts[1];
+  }
   Piece u;
 
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -322,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t v_tiles = 0;
         int filled = 0;  // places of the ring of pieces
         bool ok = true;
-        PieceWalk<true> walk(p, p.bound[blockIdx.x], p.bound[blockIdx.x + 1]);
+        PieceWalk<true> walk(p, p.bound[blockIdx.x],
+                             kSelfPlan ? bars.cut_end : p.bound[blockIdx.x + 1]);
         while (ok) {
           if (!walk.next(p, &u)) u.req = -1;
           if (filled < kPieces) ++filled;
@@ -827,16 +841,23 @@ bool encode_map(CUtensorMap* map, const void* base, bool half, int head_dim, int
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kSelfPlan>
 idx_status launch_tc_as(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         cudaStream_t s) {
   using C = TcCfg<D>;
-  const auto kernel = attend_tc_kernel<T, D>;
+  const auto kernel = attend_tc_kernel<T, D, kSelfPlan>;
   // (the register split hands out what the launch holds, no more)
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = allow_smem<C::kSmem, kRegsLaunch>(kernel, configured);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_pdl(kernel, p.grid, kThreads, C::kSmem, s, p, kmap, vmap));
+}
+
+template <typename T, int D>
+idx_status launch_tc_d(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                       cudaStream_t s) {
+  return p.self_plan ? launch_tc_as<T, D, true>(p, kmap, vmap, s)
+                     : launch_tc_as<T, D, false>(p, kmap, vmap, s);
 }
 
 bool map_stride_ok(int64_t stride, int64_t entries) {
@@ -861,10 +882,10 @@ bool attend_tc_maps(const AttendParams& p, int head_dim, bool half, CUtensorMap*
 idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, cudaStream_t s) {
   if (half)
-    return head_dim == 64 ? launch_tc_as<__half, 64>(p, kmap, vmap, s)
-                          : launch_tc_as<__half, 128>(p, kmap, vmap, s);
-  return head_dim == 64 ? launch_tc_as<__nv_bfloat16, 64>(p, kmap, vmap, s)
-                        : launch_tc_as<__nv_bfloat16, 128>(p, kmap, vmap, s);
+    return head_dim == 64 ? launch_tc_d<__half, 64>(p, kmap, vmap, s)
+                          : launch_tc_d<__half, 128>(p, kmap, vmap, s);
+  return head_dim == 64 ? launch_tc_d<__nv_bfloat16, 64>(p, kmap, vmap, s)
+                        : launch_tc_d<__nv_bfloat16, 128>(p, kmap, vmap, s);
 }
 
 }  // namespace saib
