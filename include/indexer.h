@@ -574,7 +574,8 @@ idx_status indexer_decode_topk_noalloc(const void* q, const float* weights,
  * head). out contiguous [num_tokens, num_heads, head_dim].
  *
  * Token slots past a request's length, and pages past it, may hold anything:
- * they are not read, or not used.
+ * they are not read, or not used. The same goes for pages, and their table
+ * entries, of which a window hides every key from all of the request's tokens.
  */
 enum { IDX_BF16 = 0, IDX_FP16 = 1 };
 

@@ -561,7 +561,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
             }
           } else {
             const int32_t s0 = first_key(j);
-            if (!ok && s0 <= p_hi) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+            // (what the table says of a page that no row sees may be out of date)
+            if (!ok && s0 <= p_hi && (s0 + kSub - 1 > w_lo || s0 < p.sinks))
+              set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
             const int64_t pg = ok ? page : 0;
             const int32_t tok = (s0 & (kPageTokens - 1)) + h0;
             const T* kp = k_lane + (pg * p.k_stride_page + tok * p.k_stride_token);

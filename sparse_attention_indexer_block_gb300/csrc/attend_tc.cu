@@ -352,13 +352,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the second page may lie past the request's last)
             return make_int2(bt[c], (c + 1) * kPageTokens <= u.tiles.p_hi ? bt[c + 1] : -1);
           };
+          // Whether some row of the unit sees a key of page c. Of the others nothing is loaded:
+          // their keys are masked, and what the table says of them may be out of date.
+          const int32_t before = max(u.tiles.p_lo, 0) - p.window;
+          const auto needed = [&](int32_t c) -> bool {
+            const int32_t s = c * kPageTokens;
+            return s <= u.tiles.p_hi && (s + kPageTokens - 1 > before || s < p.sinks);
+          };
           int2 next = pages_of(u.t0);
           for (int j = u.t0; ok && j < u.t1; ++j) {
             const int2 pg = next;
             next = pages_of(j + 1);
-            const bool a = pg.x >= 0 && pg.x < p.num_pages, b = pg.y >= 0 && pg.y < p.num_pages;
-            if (!a || (!b && (u.tiles.tile(j) * 2 + 1) * kPageTokens <= u.tiles.p_hi))
-              set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+            const int32_t first = u.tiles.tile(j) * 2;
+            const bool use_a = needed(first), use_b = needed(first + 1);
+            const bool a = use_a && pg.x >= 0 && pg.x < p.num_pages;
+            const bool b = use_b && pg.y >= 0 && pg.y < p.num_pages;
+            if (a != use_a || b != use_b) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
             const uint32_t bytes = (static_cast<uint32_t>(a) + b) * kPageTokens * D * 2;
             const auto fill = [&](uint32_t dst, const CUtensorMap* map, uint64_t* bar) {
               if (bytes) mbar_arrive_expect_tx(bar, bytes);
