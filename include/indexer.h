@@ -620,8 +620,9 @@ idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, 
  * a request with Q new tokens and L keys is at position p = L - Q + i and sees
  * key s when s <= p and, with a window, p - s < window or s < sinks. (L < Q
  * leaves rows of negative position, which see nothing.) Lengths outside the
- * table set IDX_DEV_BAD_LEN and are clamped; a page that is read and lies
- * outside the cache sets IDX_DEV_BAD_BLOCK.
+ * table set IDX_DEV_BAD_LEN and are clamped; a page that is needed and lies
+ * outside the cache sets IDX_DEV_BAD_BLOCK, and its keys and values count as
+ * zeros.
  */
 idx_status indexer_attend_paged(const idx_attend* a, void* stream);
 

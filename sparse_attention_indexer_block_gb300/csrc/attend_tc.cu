@@ -361,13 +361,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           int2 next = pages_of(u.t0);
           for (int j = u.t0; ok && j < u.t1; ++j) {
-            const int2 pg = next;
+            int2 pg = next;
             next = pages_of(j + 1);
             const int32_t first = u.tiles.tile(j) * 2;
-            const bool use_a = needed(first), use_b = needed(first + 1);
-            const bool a = use_a && pg.x >= 0 && pg.x < p.num_pages;
-            const bool b = use_b && pg.y >= 0 && pg.y < p.num_pages;
-            if (a != use_a || b != use_b) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+            const bool a = needed(first), b = needed(first + 1);
+            // a page outside the cache is read as the one past its last, of which every value is
+            // out of the map's bounds: zeros
+            const auto place = [&](int32_t page, bool use) -> int32_t {
+              if (page >= 0 && page < p.num_pages) return page;
+              if (use) set_error(p.dev_error, IDX_DEV_BAD_BLOCK);
+              return static_cast<int32_t>(p.num_pages);
+            };
+            pg.x = place(pg.x, a);
+            pg.y = place(pg.y, b);
             const uint32_t bytes = (static_cast<uint32_t>(a) + b) * kPageTokens * D * 2;
             const auto fill = [&](uint32_t dst, const CUtensorMap* map, uint64_t* bar) {
               if (bytes) mbar_arrive_expect_tx(bar, bytes);

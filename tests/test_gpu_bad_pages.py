@@ -1,5 +1,5 @@
-"""Pages that lie outside the cache, on the GPU: one that a window hides from every token is neither
-used nor reported."""
+"""Pages that lie outside the cache, on the GPU: the keys of one that is needed count as zeros and
+are reported, one that a window hides from every token is neither used nor reported."""
 import pytest
 import torch
 
@@ -8,6 +8,8 @@ from test_gpu_attend import BF, DEV, FP, PAGE, Batch, _lib  # noqa: F401
 from test_gpu_attend_units import _wide
 
 pytestmark = pytest.mark.gpu
+
+BAD_BLOCK = 1
 
 
 def _call(b, table, **kw):
@@ -26,6 +28,34 @@ def _hidden(first, column, window, sinks):
 # new tokens, keys, whether the table is so wide that units are cut by a plan
 BATCHES = [([1, 2], [900, 1000], False), ([1, 2], [900, 1000], True), ([70, 90], [900, 1000], False),
            ([300, 200], [5000, 1000], False), ([1] * 30 + [400], [900] * 30 + [3000], False)]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (600, 10)])
+@pytest.mark.parametrize("dtype,dim", [(BF, 128), (FP, 64)])
+@pytest.mark.parametrize("batch", range(len(BATCHES)))
+def test_keys_of_a_page_outside_the_cache_are_zeros(batch, dtype, dim, window, sinks):
+    ql, kl, wide = BATCHES[batch]
+    b = Batch(ql, kl, 8, 2, dim, dtype, seed=400 + batch)
+    if wide:
+        _wide(b)
+    page = int((set(range(b.k.shape[0])) - set(b.table.flatten().tolist())).pop())
+    b.k[page], b.v[page] = 0, 0
+    last = len(kl) - 1
+    for column in (0, 8, 9, (kl[last] - 1) // PAGE):
+        keep = b.table[last, column].item()
+        b.table[last, column] = page
+        want = b.reference(window=window, sinks=sinks)
+        b.table[last, column] = keep
+        for bad in (-1, b.k.shape[0], 2 ** 31 - 1, -2 ** 31):
+            table = b.table.clone()
+            table[last, column] = bad
+            first = None
+            for _ in range(2):
+                out, lse, err = _call(b, table, window=window, sinks=sinks)
+                assert err == (0 if _hidden(kl[last] - ql[last], column, window, sinks) else BAD_BLOCK)
+                b.check((out, lse), want)
+                assert first is None or torch.equal(out, first)
+                first = out
 
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (70, 0), (70, 5), (129, 70), (64, 64)])
