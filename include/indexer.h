@@ -667,8 +667,10 @@ idx_status indexer_copy_pages(const idx_page_pool* pools, int32_t num_pools, int
  * table follow. A parent may have several children; no row is parent and child.
  * copy_src, copy_dst (int32 [n]) get the copies made, in the order of i, then
  * -1. When free pages run out, IDX_DEV_NO_PAGE is set and the children left
- * over hold the full pages only (their lengths cut to them). num_pools may be 0
- * (then the caller makes the copies).
+ * over hold the full pages only (their lengths cut to them). A page outside the
+ * pools sets IDX_DEV_BAD_BLOCK; a child whose parent's partial last page is one
+ * holds the full pages only, too. num_pools may be 0 (then the caller makes the
+ * copies).
  */
 idx_status indexer_fork_pages(const idx_page_pool* pools, int32_t num_pools, int64_t num_pages,
                               int32_t* block_table, int64_t bt_stride, int32_t bt_width,

@@ -194,18 +194,38 @@ __global__ void __launch_bounds__(kScanThreads)
     }
     return;
   }
+  // Pages of child i's parent, whether its last one is a partial one (to be copied), and whether
+  // that one lies outside the pools; `report`: sets the error bits.
+  struct Parent {
+    int32_t pages = 0, last = 0;
+    bool ok = false, part = false, bad = false;
+    __device__ __forceinline__ bool copied() const { return part && !bad; }
+  };
+  const auto parent_of = [&](int32_t i, bool report) -> Parent {
+    Parent q;
+    if (i >= n) return q;
+    q.ok = rows_ok(parents[i], children[i]);
+    if (!q.ok) {
+      if (report) set_error(t.err, IDX_DEV_BAD_ROW);
+      return q;
+    }
+    q.pages = row_pages(t, t.seq_lens[parents[i]], &q.part);
+    if (q.part) {
+      q.last = t.block_table[parents[i] * t.bt_stride + q.pages - 1];
+      q.bad = q.last < 0 || q.last >= t.num_pages;
+      if (q.bad && report) set_error(t.err, IDX_DEV_BAD_BLOCK);
+    }
+    return q;
+  };
   __shared__ int sums[32];
   int need_all = 0, total;
   for (int32_t i0 = 0; i0 < n; i0 += kScanThreads) {
     const int32_t i = i0 + threadIdx.x;
-    bool part = false;
     if (i < n) {
       copy_src[i] = -1;
       copy_dst[i] = -1;
-      if (rows_ok(parents[i], children[i])) row_pages(t, t.seq_lens[parents[i]], &part);
-      else set_error(t.err, IDX_DEV_BAD_ROW);
     }
-    block_exclusive(part, sums, &total);
+    block_exclusive(parent_of(i, true).copied(), sums, &total);
     need_all += total;
   }
   // the lowest free pages, in order, into copy_dst
@@ -233,28 +253,21 @@ __global__ void __launch_bounds__(kScanThreads)
   int base = 0;
   for (int32_t i0 = 0; i0 < n; i0 += kScanThreads) {
     const int32_t i = i0 + threadIdx.x;
-    const bool ok = i < n && rows_ok(parents[i], children[i]);
-    bool part = false;
-    int32_t pages = 0, len = 0;
-    if (ok) {
-      len = t.seq_lens[parents[i]];
-      pages = row_pages(t, len, &part);
-    }
-    const int k = base + block_exclusive(part, sums, &total);
+    const Parent q = parent_of(i, false);
+    const int k = base + block_exclusive(q.copied(), sums, &total);
     base += total;
-    if (ok) {
-      if (!part) len = pages * kPageTokens;
-      if (part && k >= found) {
-        set_error(t.err, IDX_DEV_NO_PAGE);
-        len = (pages - 1) * kPageTokens;
-      } else if (part) {
-        const int32_t fresh = copy_dst[k];
-        copy_src[k] = t.block_table[parents[i] * t.bt_stride + pages - 1];
-        t.block_table[children[i] * t.bt_stride + pages - 1] = fresh;
-        t.ref_counts[fresh] = 1;
-      }
-      t.seq_lens[children[i]] = len;
+    if (!q.ok) continue;
+    int32_t len = q.part ? t.seq_lens[parents[i]] : q.pages * kPageTokens;
+    if (q.copied() && k < found) {
+      const int32_t fresh = copy_dst[k];
+      copy_src[k] = q.last;
+      t.block_table[children[i] * t.bt_stride + q.pages - 1] = fresh;
+      t.ref_counts[fresh] = 1;
+    } else if (q.part) {
+      if (!q.bad) set_error(t.err, IDX_DEV_NO_PAGE);
+      len = (q.pages - 1) * kPageTokens;
     }
+    t.seq_lens[children[i]] = len;
   }
 }
 

@@ -1,11 +1,14 @@
 """Pages that lie outside the cache, on the GPU: the keys of one that is needed count as zeros and
-are reported, one that a window hides from every token is neither used nor reported."""
+are reported, one that a window hides from every token is neither used nor reported, and a fork
+whose parent's partial last page is one keeps the full pages only."""
+import numpy as np
 import pytest
 import torch
 
 import sparse_attention_indexer_block_gb300 as saib
 from test_gpu_attend import BF, DEV, FP, PAGE, Batch, _lib  # noqa: F401
 from test_gpu_attend_units import _wide
+from test_gpu_pages import Pool, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +83,40 @@ def test_pages_hidden_by_a_window_may_be_gone(batch, dtype, dim, window, sinks):
         got, glse, err = _call(b, table, window=window, sinks=sinks)
         assert err == 0
         assert torch.equal(got, out) and torch.equal(glse, lse)
+
+
+@pytest.mark.parametrize("pools", [3, 0])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, "pages", 2 ** 31 - 1])
+def test_fork_from_a_bad_last_page(bad, pools):
+    p = Pool([100, 200, 64, 7], 2, seed=21, rows=9, pools=pools)
+    bad = p.pages if bad == "pages" else bad
+    p.table[1, 3] = bad                    # 200 keys: three full pages and a part
+    p.up()
+    # rows 0 and 3 take the two free pages, though the bad one comes between them
+    src, dst, want, short = p.fork([0, 3], [4, 6])
+    assert not short
+    p.table[5, :3] = p.table[1, :3]        # by hand: the full pages only
+    np.add.at(p.refs, p.table[1, :3], 1)
+    p.lens[5] = 3 * PAGE
+    got = saib.indexer_fork_pages(p.pools, p.t, p.l, p.r, _i32([0, 1, 3]), _i32([4, 5, 6]), dev_error=p.err)
+    assert p.error() == BAD_BLOCK
+    p.same()
+    assert got[0].tolist() == src + [-1] and got[1].tolist() == dst + [-1]
+    for a, w in zip(p.pools, want):
+        assert torch.equal(a, w)
+
+
+def test_fork_from_bad_last_pages_when_pages_run_out():
+    p = Pool([100, 200, 7], 1, seed=22, rows=8, pools=1)
+    p.table[1, 3] = -5
+    p.up()
+    src, dst, want, short = p.fork([0, 2], [3, 6])     # one free page for two
+    assert short
+    p.table[4, :3] = p.table[1, :3]
+    np.add.at(p.refs, p.table[1, :3], 1)
+    p.lens[4] = 3 * PAGE
+    got = saib.indexer_fork_pages(p.pools, p.t, p.l, p.r, _i32([0, 1, 2]), _i32([3, 4, 6]), dev_error=p.err)
+    assert p.error() == BAD_BLOCK | 64
+    p.same()
+    assert got[0].tolist() == src + [-1] and got[1].tolist() == dst + [-1]
+    assert torch.equal(p.pools[0], want[0])
