@@ -257,7 +257,9 @@ __device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8
 #pragma unroll
       for (int n = 1; n < kTiles8; ++n) mx = max3(mx, x[n][0], x[n][1]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max3(mx, __shfl_xor_sync(0xffffffffu, mx, 2), m[mt][h]);
+      const float far = __shfl_xor_sync(0xffffffffu, mx, 2);
+      mx = kTopWeight<T> == 0.f ? max3(mx, far, m[mt][h])
+                                : fmaxf(fmaxf(mx, far) - kTopWeight<T>, m[mt][h]);
       const float base = mx == -INFINITY ? 0.f : mx;
       alpha[h] = exp2_approx(m[mt][h] - base);
       m[mt][h] = mx;
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
         const int64_t at = token * p.num_heads + head;
         const uint2 b = make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * D + d) = b;
-        if (d == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
+        if (d == 0 && p.lse) p.lse[at] = row_lse<static_cast<int>(kTopWeight<T>)>(mx, sum);
       };
       for (int i = threadIdx.x; i < u.rows * (D / 4); i += kWarps * 32) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -963,7 +965,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_lists_kernel(const Atte
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
           dst[n * 4] = pack2<T>(o[0][n][2 * h] * inv, o[0][n][2 * h + 1] * inv);
-        if ((lane & 3) == 0 && p.lse) p.lse[at] = (m[0][h] + log2f(sum)) * kLn2;
+        if ((lane & 3) == 0 && p.lse)
+          p.lse[at] = row_lse<static_cast<int>(kTopWeight<T>)>(m[0][h], sum);
       }
     }
   }
@@ -991,6 +994,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(cons
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int r0 = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * kRows;
   constexpr int kV = D / 32;
+  // (four rows a warp: the chunk kernel's)
+  constexpr int kTop = static_cast<int>(kRows > 1 ? kTopWeightTc<T> : kTopWeight<T>);
   using Vec = typename std::conditional<kV == 4, float4, float2>::type;
   pdl_wait();
   pdl_trigger();
@@ -1109,7 +1114,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(cons
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + out * D + lane * kV);
 #pragma unroll
     for (int e = 0; e < kV; e += 2) dst[e / 2] = pack2<T>(v[k][e] * inv, v[k][e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[out] = (mx[k] + log2f(sum[k])) * kLn2;
+    if (lane == 0 && p.lse) p.lse[out] = row_lse<kTop>(mx[k], sum[k]);
   }
 }
 

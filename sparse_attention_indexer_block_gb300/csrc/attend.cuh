@@ -281,6 +281,29 @@ __device__ __forceinline__ void cp_wait() {
 
 constexpr float kLn2 = 0.693147180559945309f;
 
+// A row's weights are exp2(x - m) with m, which the kernels keep and pass on as its maximum, the
+// largest score less kTopWeight: the largest weight is 2^kTopWeight. bf16 has the exponents of fp32
+// and needs no more than 1. fp16 has no values below 2^-24: beside a weight of 1, those below 2^-25
+// are lost to the second product, though not to the sum (65 536 keys 17.5 nats below one more: most
+// of their 1.6e-3 of the output). Beside 2^15 they are lost below 2^-40 of the largest.
+template <typename T>
+constexpr float kTopWeight = std::is_same<T, __half>::value ? 15.f : 0.f;
+
+// The chunk kernel raises m (and rescales the row's accumulator) only when a weight would pass the
+// last one's largest by 2^8: bf16's then stay below 2^8, with the same relative precision, and
+// fp16's, whose largest is first 2^7, below 2^15.
+constexpr float kLazyRaise = 8.f;
+template <typename T>
+constexpr float kTopWeightTc = kTopWeight<T> == 0.f ? 0.f : kTopWeight<T> - kLazyRaise;
+
+// lse of a row whose weights exp2(x - m) sum up to l (scaled by 2^-kTop, as m is moved by it: then
+// nothing is added to the logarithm's error).
+template <int kTop>
+__device__ __forceinline__ float row_lse(float m, float l) {
+  constexpr float kDown = 1.f / static_cast<float>(1 << kTop);
+  return ((m + static_cast<float>(kTop)) + log2f(l * kDown)) * kLn2;
+}
+
 // Keys of a tile of the row-block kernel: 4 KB of K per warp either way.
 __host__ __device__ constexpr int rows_tile_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
 

@@ -19,10 +19,6 @@ static_assert(128 * kRegsFeed + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "r
 constexpr int kTmemCols = 512;
 constexpr uint32_t kOddUnits = 8;
 constexpr int kPieces = 4;  // pieces that the walk may be ahead
-// A row's running maximum is raised (and its accumulator rescaled) only when a
-// score exceeds it by this many units of log 2: the weights then stay below
-// 2^8, which both 16-bit types hold with the same relative precision.
-constexpr float kLazyRaise = 8.f;
 
 template <int D>
 struct TcCfg {
@@ -688,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 2; i < 32; i += 2) mx[c] = max3(mx[c], s[c][i], s[c][i + 1]);
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const float top =
+            fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2 - kTopWeightTc<T>;
         float alpha = 1.f;
         if (top > m + kLazyRaise) {
           alpha = exp2_approx(m - top);
@@ -803,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (r < u.rows) {
         if (!whole) p.part_ml[part] = make_float2(m, l);
-        else if (p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
+        else if (p.lse) p.lse[at] = row_lse<static_cast<int>(kTopWeightTc<T>)>(m, l);
       }
       if (odd) {
         __threadfence_block();  // (the row was written by four lanes)
