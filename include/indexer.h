@@ -599,7 +599,7 @@ typedef struct idx_attend {
   int32_t bt_width, num_reqs, num_tokens, num_heads, num_kv_heads;
   int32_t head_dim;               /* 64 or 128 */
   int32_t dtype;                  /* of q, k, v and out: IDX_BF16 or IDX_FP16 */
-  int32_t max_query_len;          /* longest request's new tokens (a hint; 0: unknown) */
+  int32_t max_query_len;          /* longest request's new tokens (a hint; 0: num_tokens) */
   int32_t window;                 /* 0: none (paged form) */
   int32_t sinks;                  /* first keys a window leaves visible (paged form) */
   int32_t topk;                   /* entries of a row's list (selected form) */

@@ -225,7 +225,8 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
     p.window = std::min(a->window, kMostKeys);
     p.sinks = a->sinks;
   }
-  const int64_t longest = a->max_query_len > 0 ? a->max_query_len : a->num_tokens;
+  const int64_t longest =
+      a->max_query_len > 0 ? std::min(a->max_query_len, a->num_tokens) : a->num_tokens;
   // The row-block kernel holds 16 rows at once and reads K and V again for the next 16; from
   // 17 rows on the tensor-memory kernel is faster (24 requests of 8000 keys, 8 kv heads of 128:
   // 15 rows 132 against 140 us, 20 rows 173 against 142).
