@@ -606,8 +606,8 @@ typedef struct idx_attend {
   float scale;                    /* > 0 */
 } idx_attend;
 
-/* Bytes of workspace either attention call needs at most for these sizes, on
- * the current CUDA device. Calls of few short units (small decode steps) need
+/* Bytes of workspace that either attention call needs, on the current CUDA
+ * device, when none of its sizes is larger than these. Calls of few short units (small decode steps) need
  * none: a call with a null workspace of 0 bytes returns IDX_ERR_WORKSPACE, before
  * any work, when it does need one. */
 idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, int32_t num_heads,

@@ -95,10 +95,12 @@ constexpr int64_t kLittleTiles = 12;  // a block's
 
 Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 3, 4}; }
 
-size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t group, int64_t head_dim) {
+// What the largest call of at most these sizes needs. Fewer kv heads make larger groups and so more
+// entries (8 bytes each): one kv head is counted with.
+size_t most_workspace(int64_t num_tokens, int64_t num_reqs, int64_t num_heads, int64_t head_dim) {
   size_t most = 0;
   for (const Variant& v : {rows_variant(1, head_dim, true), rows_variant(2, head_dim, true), tc_variant()}) {
-    const size_t n = attend_ws(num_reqs, entry_bound(num_tokens, num_reqs, group, v.rows), v.grid,
+    const size_t n = attend_ws(num_reqs, entry_bound(num_tokens, num_reqs, num_heads, v.rows), v.grid,
                                v.rows, head_dim)
                          .total;
     most = n > most ? n : most;
@@ -209,7 +211,7 @@ idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, 
   if ((head_dim != 64 && head_dim != 128) ||
       static_cast<int64_t>(num_tokens) * num_heads > kMostRows)
     return IDX_ERR_UNSUPPORTED;
-  *bytes = most_workspace(num_tokens, num_reqs, num_heads / num_kv_heads, head_dim);
+  *bytes = most_workspace(num_tokens, num_reqs, num_heads, head_dim);
   return IDX_OK;
 }
 
