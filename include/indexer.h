@@ -599,7 +599,7 @@ typedef struct idx_attend {
   int32_t bt_width, num_reqs, num_tokens, num_heads, num_kv_heads;
   int32_t head_dim;               /* 64 or 128 */
   int32_t dtype;                  /* of q, k, v and out: IDX_BF16 or IDX_FP16 */
-  int32_t max_query_len;          /* longest request's new tokens (a hint; 0: num_tokens) */
+  int32_t max_query_len;          /* longest request's new tokens (a hint for speed; 0: num_tokens) */
   int32_t window;                 /* 0: none (paged form) */
   int32_t sinks;                  /* first keys a window leaves visible (paged form) */
   int32_t topk;                   /* entries of a row's list (selected form) */
@@ -607,9 +607,9 @@ typedef struct idx_attend {
 } idx_attend;
 
 /* Bytes of workspace that either attention call needs, on the current CUDA
- * device, when none of its sizes is larger than these. Calls of few short units (small decode steps) need
- * none: a call with a null workspace of 0 bytes returns IDX_ERR_WORKSPACE, before
- * any work, when it does need one. */
+ * device, when none of its sizes is larger than these. Calls of few short units
+ * (small decode steps) need none: a call with a null workspace of 0 bytes returns
+ * IDX_ERR_WORKSPACE, before any work, when it does need one. */
 idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, int32_t num_heads,
                                           int32_t num_kv_heads, int32_t head_dim, size_t* bytes);
 

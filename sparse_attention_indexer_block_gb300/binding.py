@@ -762,7 +762,9 @@ def indexer_attend_paged(q, k_cache, v_cache, block_table, seq_lens, query_start
     contiguous), block_table int32 [requests, width], seq_lens int32 [requests]
     (keys, the new ones among them), query_start_loc int32 [requests + 1].
     window > 0: a token sees the last `window` keys up to its own, and the
-    first `sinks` keys. max_query_len is a hint (0: unknown); scale defaults to
+    first `sinks` keys. max_query_len (new tokens of the longest request) is a
+    hint that chooses the kernel, for small and windowed steps the faster one;
+    0 and anything above the tokens count as all of them. scale defaults to
     dim ** -0.5. Returns (out like q, lse float32 [tokens, heads])."""
     return _attend("indexer_attend_paged", q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
                    None, scale, out, lse, workspace, dev_error, stream, max_query_len, window, sinks)
