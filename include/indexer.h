@@ -182,6 +182,26 @@ idx_status indexer_insert_keys(const void* k, const int64_t* slot_mapping, int64
                                int32_t head_dim, uint8_t* index_cache, int64_t num_pages,
                                uint32_t* dev_error, void* stream);
 
+/*
+ * Index-key insert into an MXFP4 cache (the layout and the sources at
+ * indexer_decode_topk_mxfp4, which reads it). Token i's keys k bf16 [num_tokens,
+ * 128], row stride k_stride (elements, a multiple of 8, >= 128), go to slot
+ * slot_mapping[i] by the MX shared-exponent rule, per block of 32 with largest
+ * magnitude a: E = max(floor(log2 a) - 2 + 127, 0) (0 where a == 0), codes =
+ * e2m1 round-to-nearest-even of k / 2^(E - 127), saturating at 6; a block of
+ * zeros gets codes 0. A NaN counts as 0; an infinity is written as 6 * 2^126 (E =
+ * 253). values (nullable, bf16 [num_tokens, 128], contiguous) gets the values that
+ * the entries stand for, exactly (but for that of an infinity, which is one
+ * again), and zeros for tokens that are not written. Slots as in
+ * indexer_insert_keys: a negative one is padding, one >= num_pages * 64 ORs
+ * IDX_DEV_BAD_BLOCK, both are skipped. k, values and index_cache 16-byte
+ * aligned, slot_mapping 8.
+ */
+idx_status indexer_insert_keys_mxfp4(const void* k, int64_t k_stride, const int64_t* slot_mapping,
+                                     int64_t num_tokens, int32_t head_dim, uint8_t* index_cache,
+                                     int64_t num_pages, void* values, uint32_t* dev_error,
+                                     void* stream);
+
 /* Bytes of workspace indexer_decode_topk / indexer_decode_logits need for
  * num_reqs requests of next_n rows each, on the current CUDA device. */
 idx_status indexer_decode_workspace_bytes(int32_t num_reqs, int32_t next_n, int32_t topk,
@@ -627,6 +647,24 @@ idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, 
 idx_status indexer_attend_paged(const idx_attend* a, void* stream);
 
 /*
+ * Attention of trees of drafted tokens over the paged cache (speculative
+ * decoding): as indexer_attend_paged, except for what a row sees. A request's Q
+ * new tokens are the nodes of its tree, whose keys and values are in the cache,
+ * in the nodes' order, at L - Q .. L - 1. A row sees key s < L - Q (one before
+ * the tree) always, with a window when p - s < window or s < sinks, p being the
+ * token's own position; and node j (key L - Q + j) when bit j % 32 of word j / 32
+ * of the row's mask is set, whatever the window. So a mask may name any of the
+ * request's new tokens, later ones too; bits past them are not looked at, nodes
+ * past the mask's words are not seen, and a row without any visible key gives 0
+ * and -inf.
+ * masks int32 [num_tokens, mask_words], row stride mask_stride; positions int32
+ * [num_tokens], needed with a window only (clamped to [L - Q, L - 1]).
+ * indexer_plan_tree makes both.
+ */
+idx_status indexer_attend_tree(const idx_attend* a, const int32_t* masks, int64_t mask_stride,
+                               int32_t mask_words, const int32_t* positions, void* stream);
+
+/*
  * Attention of every token to the keys listed for it: indices[t] holds topk
  * positions of t's request in any order, entries < 0 are empty (what
  * indexer_decode_topk and indexer_prefill_topk write; every entry counts, so a
@@ -701,6 +739,110 @@ idx_status indexer_compact_pages(const idx_page_pool* pools, int32_t num_pools, 
                                  int32_t num_rows, const int32_t* seq_lens, int32_t* ref_counts,
                                  int32_t* remap, int32_t* num_live, void* workspace,
                                  size_t workspace_bytes, uint32_t* dev_error, void* stream);
+
+/*
+ * New and drafted tokens in the caches
+ * ------------------------------------
+ */
+
+/* Arguments of indexer_append_kv. Strides in elements, multiples of 8; the
+ * head_dim values contiguous; addresses of values 16-byte aligned. */
+typedef struct idx_append {
+  const void* q;               /* nullable: [num_tokens, num_heads, head_dim] */
+  const void* k;               /* [num_tokens, num_kv_heads, head_dim] */
+  const void* v;               /* the same */
+  const int64_t* slot_mapping; /* [num_tokens] */
+  const int32_t* positions;    /* [num_tokens] (with a rotation) */
+  const float* rotary;         /* nullable: [num_positions, rotary_dim] cosines, then sines */
+  void* q_out;                 /* as q (with q and a rotation); may be q itself */
+  void* k_cache;               /* pages as in idx_attend */
+  void* v_cache;
+  uint32_t* dev_error;         /* nullable */
+  int64_t q_stride_token, q_stride_head, k_stride_token, k_stride_head;
+  int64_t v_stride_token, v_stride_head, q_out_stride_token, q_out_stride_head;
+  int64_t k_cache_stride_page, k_cache_stride_token, k_cache_stride_head;
+  int64_t v_cache_stride_page, v_cache_stride_token, v_cache_stride_head;
+  int64_t num_pages, num_positions, rotary_stride;
+  int32_t num_tokens, num_heads, num_kv_heads;
+  int32_t head_dim;            /* 64 or 128 */
+  int32_t dtype;               /* of q, k, v and the caches: IDX_BF16 or IDX_FP16 */
+  int32_t rotary_dim;          /* a multiple of 16, <= head_dim */
+  int32_t interleaved;         /* 0: value i is paired with i + rotary_dim / 2; 1: 2i with 2i + 1 */
+} idx_append;
+
+/*
+ * Appends new tokens' keys and values to the paged cache, with the position
+ * rotation of queries and keys on the way. Token t, at position p =
+ * positions[t], goes to slot s = slot_mapping[t] (page s / 64, token s % 64):
+ *
+ *     K[s] = rot_p(k[t])     V[s] = v[t]     q_out[t] = rot_p(q[t])
+ *
+ * where rot_p turns pair i of the first rotary_dim values, (a, b), into
+ * (a c - b d, b c + a d) with c = rotary[p, i], d = rotary[p, rotary_dim / 2 + i],
+ * in fp32, rounded once; the other values stay as they are. rotary NULL: no
+ * rotation (q, positions and q_out are not looked at).
+ * A negative slot is padding: no key or value is written (the query is rotated
+ * all the same). A slot >= num_pages * 64 sets IDX_DEV_BAD_BLOCK and is treated
+ * as padding. A position outside the table is clamped, and sets IDX_DEV_BAD_LEN
+ * unless its token is padding. Two tokens with the same slot race.
+ */
+idx_status indexer_append_kv(const idx_append* a, void* stream);
+
+/*
+ * What a tree of drafted tokens asks of its attention. parents int32
+ * [num_tokens]: a node's parent, as an index among its request's new tokens and
+ * below the node's own, or -1 for a node that follows the last token before the
+ * tree. Anything else sets IDX_DEV_BAD_ROW and counts as -1. With Q new tokens and
+ * L keys, per token t (node i, the depth being the number of its ancestors):
+ *   masks[t]      (int32, mask_words words, row stride mask_words): bit j is set
+ *                 when j is i or an ancestor and, with a window, depth_i - depth_j <
+ *                 window or position_j < sinks (window 0: none)
+ *   positions[t]  L - Q + depth
+ *   paths[t]      (nullable, int32, path_width entries): the places L - Q + j in
+ *                 the cache of i and its ancestors, i first, then -1: appended to
+ *                 the indexer's selection among the keys before the tree, what
+ *                 indexer_attend_selected takes for a sparse layer
+ * A node past the masks' words or a path past its width sets IDX_DEV_OVERFLOW and
+ * is left out. Tokens in no request are left as they are.
+ */
+idx_status indexer_plan_tree(const int32_t* parents, const int32_t* seq_lens,
+                             const int32_t* query_start_loc, int32_t num_reqs, int32_t num_tokens,
+                             int32_t window, int32_t sinks, int32_t* masks, int32_t mask_words,
+                             int32_t* positions, int32_t* paths, int32_t path_width,
+                             uint32_t* dev_error, void* stream);
+
+/* Where the tokens of a cache's pages lie: `pieces` runs of piece_bytes at base +
+ * page * page_stride + token * token_stride + piece * piece_stride (bytes, all
+ * multiples of 4). K or V [pages, 64, kv heads, dim]: one piece of all heads where
+ * they are contiguous, else one per head. An fp8 index cache is two such pools
+ * (128 bytes a token from the page's beginning, 4 bytes from byte 8192), an MXFP4
+ * one is one (68 bytes). */
+typedef struct idx_token_pool {
+  void* base;
+  int64_t page_stride, token_stride, piece_stride;
+  int32_t pieces, piece_bytes;
+} idx_token_pool;
+
+/*
+ * Keeps the accepted path of every request's tree and drops its other nodes.
+ * accepted int32 [num_reqs, max_accepted], row stride accepted_stride: the n
+ * accepted nodes of a request, ascending, then -1 (a path is ascending, for a
+ * node's parent is below it). In every pool the token at L - Q + accepted[i]
+ * moves to L - Q + i, i < n; the request then has L - Q + n keys. An entry that
+ * is not above the one before it or not below Q sets IDX_DEV_BAD_ROW and ends the
+ * list. Rows of block_table and seq_lens are the requests. ref_counts (nullable,
+ * int32 [num_pages]): pages that the row no longer holds lose a reference (one
+ * without sets IDX_DEV_BAD_REF and stays at 0). A page outside the pools sets
+ * IDX_DEV_BAD_BLOCK, its moves or references are left out; lengths outside the
+ * table, or L < Q, set IDX_DEV_BAD_LEN and leave the request as it is. The pages
+ * of the new tokens belong to one row each.
+ */
+idx_status indexer_commit_tree(const idx_token_pool* pools, int32_t num_pools, int64_t num_pages,
+                               const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+                               int32_t num_reqs, int32_t* seq_lens, const int32_t* query_start_loc,
+                               const int32_t* accepted, int64_t accepted_stride,
+                               int32_t max_accepted, int32_t* ref_counts, uint32_t* dev_error,
+                               void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,9 +9,12 @@ from .binding import (  # noqa: F401
     IndexerError,
     attend_workspace,
     decode_workspace,
+    indexer_append_kv,
     indexer_attend_paged,
     indexer_attend_selected,
+    indexer_attend_tree,
     indexer_block_topk,
+    indexer_commit_tree,
     indexer_compact_pages,
     indexer_copy_pages,
     indexer_dcp_merge,
@@ -29,7 +32,9 @@ from .binding import (  # noqa: F401
     indexer_expand_decode_rows,
     indexer_expand_pools,
     indexer_insert_keys,
+    indexer_insert_keys_mxfp4,
     indexer_plan_prefill_chunks,
+    indexer_plan_tree,
     indexer_prefill_topk,
     indexer_prefill_topk_values,
     indexer_prefill_workspace_bytes,

@@ -25,6 +25,7 @@ STATUS_NAMES = {0: "IDX_OK", 1: "IDX_ERR_INVALID_ARG", 2: "IDX_ERR_UNSUPPORTED",
 DEV_BAD_BLOCK, DEV_BAD_LEN, DEV_TIMEOUT, DEV_OVERFLOW = 1, 2, 4, 8
 DEV_BAD_ROW, DEV_NO_PAGE, DEV_BAD_REF = 32, 64, 128
 NUM_HEADS, HEAD_DIM, PAGE_TOKENS, PAGE_BYTES, MAX_TOPK = 64, 128, 64, 8448, 2048
+MXFP4_PAGE_BYTES, MXFP4_TOKEN_BYTES = 4352, 68
 DCP_MAX_CANDIDATES = 16384
 
 
@@ -52,6 +53,35 @@ assert _ATTEND_BYTES.size == C.sizeof(Attend)
 class PagePool(C.Structure):
     """idx_page_pool of indexer.h."""
     _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("page_bytes", C.c_int64)]
+
+
+class Append(C.Structure):
+    """idx_append of indexer.h."""
+    _fields_ = ([(n, C.c_void_p) for n in ("q", "k", "v", "slot_mapping", "positions", "rotary", "q_out",
+                                           "k_cache", "v_cache", "dev_error")]
+                + [(n, C.c_int64) for n in ("q_stride_token", "q_stride_head", "k_stride_token",
+                                            "k_stride_head", "v_stride_token", "v_stride_head",
+                                            "q_out_stride_token", "q_out_stride_head",
+                                            "k_cache_stride_page", "k_cache_stride_token",
+                                            "k_cache_stride_head", "v_cache_stride_page",
+                                            "v_cache_stride_token", "v_cache_stride_head",
+                                            "num_pages", "num_positions", "rotary_stride")]
+                + [(n, C.c_int32) for n in ("num_tokens", "num_heads", "num_kv_heads", "head_dim",
+                                            "dtype", "rotary_dim", "interleaved")])
+
+
+_APPEND_BYTES = struct.Struct("=10Q17q7i4x")
+assert _APPEND_BYTES.size == C.sizeof(Append)
+
+
+class TokenPool(C.Structure):
+    """idx_token_pool of indexer.h."""
+    _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("piece_stride", C.c_int64), ("pieces", C.c_int32), ("piece_bytes", C.c_int32)]
+
+
+_TOKEN_POOL_BYTES = struct.Struct("=Q3q2i")
+assert _TOKEN_POOL_BYTES.size == C.sizeof(TokenPool)
 
 
 # exported symbols and their ctypes signatures (kept in step with indexer.h)
@@ -112,6 +142,13 @@ SIGNATURES.update({
     "indexer_compact_workspace_bytes": (C.c_int, [_I64, C.POINTER(_SZ)]),
     "indexer_compact_pages": (C.c_int, [C.POINTER(PagePool), _I32, _I64, _P, _I64, _I32, _I32, _P,
                                         _P, _P, _P, _P, _SZ, _P, _P]),
+    "indexer_attend_tree": (C.c_int, [_P, _P, _I64, _I32, _P, _P]),
+    "indexer_append_kv": (C.c_int, [_P, _P]),
+    "indexer_insert_keys_mxfp4": (C.c_int, [_P, _I64, _P, _I64, _I32, _P, _I64, _P, _P, _P]),
+    "indexer_plan_tree": (C.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, _I32, _P,
+                                    _P]),
+    "indexer_commit_tree": (C.c_int, [_P, _I32, _I64, _P, _I64, _I32, _I32, _P, _P, _P, _I64, _I32,
+                                      _P, _P, _P]),
 })
 
 _lock = threading.Lock()
@@ -671,7 +708,8 @@ def attend_workspace(num_tokens: int, num_reqs: int, num_heads: int, num_kv_head
 
 
 def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices, scale, out,
-            lse, workspace, dev_error, stream, max_query_len=0, window=0, sinks=0):
+            lse, workspace, dev_error, stream, max_query_len=0, window=0, sinks=0, masks=None,
+            positions=None):
     for what, t, dims in (("q", q, 3), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4)):
         if not isinstance(t, torch.Tensor) or t.dim() != dims:
             _refuse(name, f"{what} must have {dims} dimensions")
@@ -718,9 +756,22 @@ def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, i
     for what, n in (("max_query_len", max_query_len), ("window", window), ("sinks", sinks)):
         if not 0 <= n <= 0x7fffffff:
             _refuse(name, f"{what} {n}")
+    tree = ()
+    if masks is not None:
+        _need_i32(name, "masks", masks, tokens, None)
+        words = masks.shape[1]
+        if words < 1:
+            _refuse(name, "masks has no columns")
+        if positions is not None:
+            _need_vector(name, "positions", positions, _I32T, tokens)
+        elif window:
+            _refuse(name, "a window needs positions")
+        tree = (masks.data_ptr(), masks.stride(0) if tokens > 1 else words, words, _at(positions))
+        if tokens > 1 and tree[1] < words:
+            _refuse(name, "masks' rows overlap")
     _need_error(name, dev_error)
     index = _need_device(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices,
-                         out, lse, workspace, dev_error)
+                         out, lse, workspace, dev_error, masks, positions)
     with _On(index, stream) as s:
         if out is None:
             out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
@@ -736,7 +787,7 @@ def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, i
                 0 if dev_error is None else dev_error.data_ptr(),
                 qt, qh, kp, kt, kh, vp, vt, vh, pages, bt_stride, idx_stride, bt_width, reqs, tokens,
                 heads, kv_heads, dim, _ATTEND_TYPES[dtype], max_query_len, window, sinks, topk,
-                dim ** -0.5 if scale is None else scale), s)
+                dim ** -0.5 if scale is None else scale), *tree, s)
 
         st = _WORKSPACE
         if workspace is None:
@@ -780,6 +831,23 @@ def indexer_attend_selected(q, k_cache, v_cache, block_table, indices, query_sta
         _refuse("indexer_attend_selected", "indices is missing")
     return _attend("indexer_attend_selected", q, k_cache, v_cache, block_table, query_start_loc, None,
                    indices, scale, out, lse, workspace, dev_error, stream)
+
+
+def indexer_attend_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks,
+                        max_query_len: int = 0, positions=None, scale=None, window: int = 0,
+                        sinks: int = 0, out=None, lse=None, workspace=None, dev_error=None,
+                        stream=None):
+    """Attention of trees of drafted tokens over the paged cache: a request's new
+    tokens see every key before them (with a window: those that the token's
+    position, int32 [tokens], leaves) and the new tokens that their rows of masks
+    (int32 [tokens, words], bit j: the request's new token j) name. masks and
+    positions are what indexer_plan_tree makes. Other arguments and the result as
+    indexer_attend_paged; max_query_len (nodes of the largest tree) is a hint."""
+    if masks is None:
+        _refuse("indexer_attend_tree", "masks is missing")
+    return _attend("indexer_attend_tree", q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
+                   None, scale, out, lse, workspace, dev_error, stream, max_query_len, window, sinks,
+                   masks, positions)
 
 
 def _pools(name, pools, num_pages):
@@ -922,3 +990,259 @@ def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, 
             _at(seq_lens), _at(ref_counts), _at(remap), _at(num_live), _at(workspace), workspace.numel() * workspace.element_size(),
             _at(dev_error), s))
     return remap, num_live
+
+
+# ---------------------------------------------------------------------------
+# new and drafted tokens in the caches
+# ---------------------------------------------------------------------------
+
+
+def _need_vector(name, what, t, dtype, n):
+    """A contiguous tensor [n] of that type (n None: any size)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        _refuse(name, f"{what} must be a tensor of {dtype}")
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        _refuse(name, f"{what} has shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _refuse(name, f"{what} must be contiguous")
+
+
+def _outer_strides(name, what, t, written=False):
+    """Strides of all dimensions but the last, which must be contiguous (0 for a dimension of one
+    entry, whose stride is never used)."""
+    *strides, last = t.stride()
+    *shape, dim = t.shape
+    if last != 1 and dim > 1:
+        _refuse(name, f"{what} must be contiguous in its last dimension")
+    for i, n in enumerate(shape):
+        if n == 1:
+            strides[i] = 0
+        elif written and strides[i] == 0 and n:
+            _refuse(name, f"{what}'s entries overlap")
+    return strides
+
+
+def indexer_append_kv(k, v, k_cache, v_cache, slot_mapping, q=None, positions=None, rotary=None,
+                      interleaved: bool = False, q_out=None, dev_error=None, stream=None):
+    """Writes new tokens' keys and values k, v [tokens, kv heads, dim] (bf16 or
+    fp16, dim 64 or 128) to their slots (slot_mapping int64 [tokens]: page * 64 +
+    token, negative: padding) of k_cache, v_cache [pages, 64, kv heads, dim], in
+    place. With rotary (float32 [positions, rotary_dim]: cosines, then sines; rotary_dim
+    a multiple of 16) the first rotary_dim values of the keys, and of the
+    queries q [tokens, heads, dim] if given, are rotated to their positions (int32
+    [tokens]) on the way: value i with i + rotary_dim / 2, or neighbours when
+    interleaved. Any strides that keep dim contiguous. Returns the rotated queries
+    (q_out; q itself may be given), None without q."""
+    name = "indexer_append_kv"
+    for what, t, dims in (("k", k, 3), ("v", v, 3), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            _refuse(name, f"{what} must have {dims} dimensions")
+    tokens, kv_heads, dim = k.shape
+    dtype = k.dtype
+    if dtype not in _ATTEND_TYPES:
+        _refuse(name, f"k is {dtype}, not bfloat16 or float16", _UNSUPPORTED)
+    if v.dtype is not dtype or k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        _refuse(name, "k, v, k_cache and v_cache differ in type")
+    if dim != 64 and dim != 128:
+        _refuse(name, f"head_dim {dim}, not 64 or 128", _UNSUPPORTED)
+    pages, page = k_cache.shape[:2]
+    if v.shape != k.shape or k_cache.shape[2:] != k.shape[1:] or v_cache.shape != k_cache.shape:
+        _refuse(name, "k and v must be [tokens, kv heads, dim], the caches [pages, 64, kv heads, dim]")
+    if page != PAGE_TOKENS:
+        _refuse(name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
+    _need_vector(name, "slot_mapping", slot_mapping, torch.int64, tokens)
+    heads = rotary_dim = num_positions = rotary_stride = 0
+    qs = os = (0, 0)
+    if rotary is None:
+        if q is not None or positions is not None or q_out is not None:
+            _refuse(name, "q, positions and q_out belong to a rotation")
+    else:
+        if not isinstance(rotary, torch.Tensor) or rotary.dtype is not _F32T or rotary.dim() != 2:
+            _refuse(name, "rotary must be a float32 tensor [positions, rotary_dim]")
+        num_positions, rotary_dim = rotary.shape
+        if rotary_dim < 16 or rotary_dim % 16 or rotary_dim > dim:
+            _refuse(name, f"rotary_dim {rotary_dim}, not a multiple of 16 up to {dim}", _UNSUPPORTED)
+        rotary_stride = _outer_strides(name, "rotary", rotary)[0] or rotary_dim
+        if positions is None:
+            _refuse(name, "positions is missing")
+        _need_vector(name, "positions", positions, _I32T, tokens)
+        if q is not None:
+            if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] != tokens \
+                    or q.shape[2] != dim or q.shape[1] < 1 or q.dtype is not dtype:
+                _refuse(name, f"q must be {dtype} [tokens, heads, {dim}]")
+            heads = q.shape[1]
+            qs = _outer_strides(name, "q", q)
+            if q_out is not None:
+                if not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape or q_out.dtype is not dtype:
+                    _refuse(name, "q_out must be a tensor like q")
+                os = _outer_strides(name, "q_out", q_out, True)
+        elif q_out is not None:
+            _refuse(name, "q_out without q")
+    ks, vs = _outer_strides(name, "k", k), _outer_strides(name, "v", v)
+    kc = _outer_strides(name, "k_cache", k_cache, True)
+    vc = _outer_strides(name, "v_cache", v_cache, True)
+    _need_error(name, dev_error)
+    index = _need_device(name, k, v, k_cache, v_cache, slot_mapping, q, positions, rotary, q_out, dev_error)
+    with _On(index, stream) as s:
+        if heads and q_out is None:
+            q_out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
+            os = (heads * dim, dim)
+        _ok(name, load().indexer_append_kv(_APPEND_BYTES.pack(
+            _at(q) or 0, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), _at(positions) or 0,
+            _at(rotary) or 0, _at(q_out) or 0, k_cache.data_ptr(), v_cache.data_ptr(), _at(dev_error) or 0,
+            *qs, *ks, *vs, *os, *kc, *vc, pages, num_positions, rotary_stride, tokens, heads, kv_heads,
+            dim, _ATTEND_TYPES[dtype], rotary_dim, 1 if interleaved else 0), s))
+    return q_out
+
+
+def indexer_insert_keys_mxfp4(k, slot_mapping, index_cache, values=None, dev_error=None, stream=None):
+    """Quantises k (bf16 [T, 128], rows of any stride) to MXFP4 entries and writes them into the
+    paged index cache (uint8 [pages, 4352]) at slot_mapping (int64 [T]); in place. values (bf16
+    [T, 128], contiguous) gets what the entries stand for."""
+    name = "indexer_insert_keys_mxfp4"
+    if not isinstance(k, torch.Tensor) or k.dim() != 2 or k.dtype is not torch.bfloat16:
+        _refuse(name, "k must be a bfloat16 tensor [tokens, 128]")
+    tokens, dim = k.shape
+    if dim != HEAD_DIM:
+        _refuse(name, f"keys of {dim} values, not {HEAD_DIM}", _UNSUPPORTED)
+    stride = _outer_strides(name, "k", k)[0] or dim
+    _need_vector(name, "slot_mapping", slot_mapping, torch.int64, tokens)
+    if not isinstance(index_cache, torch.Tensor) or index_cache.dtype is not torch.uint8 \
+            or index_cache.dim() != 2 or index_cache.shape[1] != MXFP4_PAGE_BYTES \
+            or not index_cache.is_contiguous():
+        _refuse(name, f"index_cache must be a contiguous uint8 tensor [pages, {MXFP4_PAGE_BYTES}]")
+    if values is not None and not (isinstance(values, torch.Tensor) and values.shape == k.shape
+                                   and values.dtype is torch.bfloat16 and values.is_contiguous()):
+        _refuse(name, "values must be a contiguous bfloat16 tensor of k's shape")
+    _need_error(name, dev_error)
+    index = _need_device(name, k, slot_mapping, index_cache, values, dev_error)
+    with _On(index, stream) as s:
+        _ok(name, load().indexer_insert_keys_mxfp4(
+            k.data_ptr(), stride, slot_mapping.data_ptr(), tokens, dim, index_cache.data_ptr(),
+            index_cache.shape[0], _at(values), _at(dev_error), s))
+    return index_cache
+
+
+def indexer_plan_tree(parents, seq_lens, query_start_loc, max_query_len: int, window: int = 0,
+                      sinks: int = 0, max_path: int = 0, masks=None, positions=None, paths=None,
+                      dev_error=None, stream=None):
+    """What trees of drafted tokens ask of attention, from their nodes' parents (int32 [tokens],
+    indices among the request's new tokens, -1 for a root). Returns (masks int32 [tokens, words]:
+    every node and its ancestors, with a window those that it leaves; positions int32 [tokens]; paths
+    int32 [tokens, max_path]: the places of a node and its ancestors in the cache, -1 after, None
+    with max_path 0). max_query_len: nodes of the largest tree (words = ceil(max_query_len / 32))."""
+    name = "indexer_plan_tree"
+    _need_vector(name, "parents", parents, _I32T, None)
+    tokens = parents.shape[0]
+    _need_vector(name, "query_start_loc", query_start_loc, _I32T, None)
+    reqs = query_start_loc.shape[0] - 1
+    if reqs < 0:
+        _refuse(name, "query_start_loc is empty")
+    _need_vector(name, "seq_lens", seq_lens, _I32T, reqs)
+    for what, n, least in (("max_query_len", max_query_len, 1), ("window", window, 0),
+                           ("sinks", sinks, 0), ("max_path", max_path, 0)):
+        if not least <= n <= 0x7fffffff:
+            _refuse(name, f"{what} {n}")
+    words = (max_query_len + 31) // 32
+    outputs = (("masks", masks, (tokens, words)), ("paths", paths, (tokens, max_path)))
+    for what, t, shape in outputs:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is _I32T
+                                  and tuple(t.shape) == shape and t.is_contiguous()):
+            _refuse(name, f"{what} must be a contiguous int32 tensor {list(shape)}")
+    if positions is not None:
+        _need_vector(name, "positions", positions, _I32T, tokens)
+    _need_error(name, dev_error)
+    index = _need_device(name, parents, seq_lens, query_start_loc, masks, positions, paths, dev_error)
+    with _On(index, stream) as s:
+        new = functools.partial(torch.empty, dtype=_I32T, device=parents.device)
+        if masks is None:
+            masks = new((tokens, words))
+        if positions is None:
+            positions = new((tokens,))
+        if paths is None and max_path:
+            paths = new((tokens, max_path))
+        _ok(name, load().indexer_plan_tree(
+            parents.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), reqs, tokens, window,
+            sinks, masks.data_ptr(), words, positions.data_ptr(), _at(paths) if max_path else None, max_path,
+            _at(dev_error), s))
+    return masks, positions, paths
+
+
+def _token_pools(name, pools):
+    """(idx_token_pool entries as bytes, their number, pages): tensors [pages, 64, ...], or uint8
+    index caches [pages, 8448] and [pages, 4352]."""
+    out, pages = [], None
+    for t in pools:
+        if not isinstance(t, torch.Tensor) or t.dim() < 2 or t.shape[0] < 1:
+            _refuse(name, "a pool must be a tensor [pages, 64, ...] or a uint8 index cache")
+        shape, at = t.shape, t.data_ptr()
+        if pages is not None and shape[0] != pages:
+            _refuse(name, "the pools differ in pages")
+        pages = shape[0]
+        if t.dtype is torch.uint8 and len(shape) == 2 and shape[1] in (PAGE_BYTES, MXFP4_PAGE_BYTES):
+            if t.stride(1) != 1 or (pages > 1 and t.stride(0) < shape[1]) or t.stride(0) % 4 or at % 4:
+                _refuse(name, "an index cache's pages must be contiguous and of whole words")
+            if shape[1] == PAGE_BYTES:
+                values = PAGE_TOKENS * HEAD_DIM
+                out.append((at, t.stride(0), HEAD_DIM, 0, 1, HEAD_DIM))
+                out.append((at + values, t.stride(0), 4, 0, 1, 4))
+            else:
+                out.append((at, t.stride(0), MXFP4_TOKEN_BYTES, 0, 1, MXFP4_TOKEN_BYTES))
+            continue
+        if shape[1] != PAGE_TOKENS:
+            _refuse(name, f"pages of {shape[1]} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
+        size, strides = t.element_size(), t.stride()
+        if any(n > 1 and st == 0 for n, st in zip(shape, strides)):
+            _refuse(name, "a pool's tokens overlap")
+        # a token's values from the last dimension up to where they stop being contiguous
+        run, dim = size, len(shape) - 1
+        while dim >= 2 and (shape[dim] == 1 or strides[dim] * size == run):
+            run *= shape[dim]
+            dim -= 1
+        pieces = piece_stride = 1
+        if dim >= 2:
+            pieces, piece_stride = shape[dim], strides[dim] * size
+            if any(n > 1 for n in shape[2:dim]):
+                _refuse(name, "a pool's token must be one run of values or evenly spaced ones")
+        page_stride, token_stride = strides[0] * size, strides[1] * size
+        if pages == 1:
+            page_stride = token_stride
+        if dim < 2:
+            piece_stride = run
+        if run == 0 or run % 4 or at % 4 or token_stride % 4 or page_stride % 4 or piece_stride % 4:
+            _refuse(name, "a pool's tokens must be of whole 4-byte words")
+        out.append((at, page_stride, token_stride, piece_stride, pieces, run))
+    return b"".join(_TOKEN_POOL_BYTES.pack(*e) for e in out), len(out), pages
+
+
+def indexer_commit_tree(pools, block_table, seq_lens, query_start_loc, accepted, ref_counts=None,
+                        dev_error=None, stream=None):
+    """Keeps every request's accepted nodes (accepted int32 [requests, n]: ascending, then -1) of its
+    tree of new tokens and drops the others: in every pool (tensors [pages, 64, ...] of keys or
+    values, uint8 index caches [pages, 8448] or [pages, 4352]) their tokens move to the tree's first
+    places, seq_lens becomes L - Q + accepted nodes, and the pages that a row no longer holds lose a
+    reference in ref_counts (int32 [pages]), all in place. Rows of block_table are the requests."""
+    name = "indexer_commit_tree"
+    entries, num_pools, pages = _token_pools(name, pools)
+    _need_vector(name, "query_start_loc", query_start_loc, _I32T, None)
+    reqs = query_start_loc.shape[0] - 1
+    if reqs < 0:
+        _refuse(name, "query_start_loc is empty")
+    width, bt_stride = _need_table(name, block_table, reqs)
+    _need_vector(name, "seq_lens", seq_lens, _I32T, reqs)
+    _need_i32(name, "accepted", accepted, reqs, None)
+    most = accepted.shape[1]
+    stride = accepted.stride(0) if reqs > 1 else most
+    if stride < most:
+        _refuse(name, "accepted's rows overlap")
+    if ref_counts is not None:
+        _need_vector(name, "ref_counts", ref_counts, _I32T, pages)
+        pages = ref_counts.shape[0]
+    if pages is None:
+        _refuse(name, "neither pools nor ref_counts")
+    _need_error(name, dev_error)
+    index = _need_device(name, block_table, seq_lens, query_start_loc, accepted, ref_counts, dev_error, *pools)
+    with _On(index, stream) as s:
+        _ok(name, load().indexer_commit_tree(
+            entries, num_pools, pages, block_table.data_ptr(), bt_stride, width, reqs, seq_lens.data_ptr(),
+            query_start_loc.data_ptr(), accepted.data_ptr(), stride, most, _at(ref_counts), _at(dev_error), s))

@@ -1,0 +1,326 @@
+// New tokens into the caches: keys and values with the position rotation on
+// the way, and index keys into an MXFP4 cache.
+#include <algorithm>
+
+#include "attend.cuh"
+
+namespace saib {
+
+namespace {
+
+constexpr int kThreads = 128;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// ---------------------------------------------------------------------------
+// keys and values
+// ---------------------------------------------------------------------------
+
+struct AppendParams {
+  idx_append a;
+  int32_t splits;  // blocks that share a token
+};
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (std::is_same<T, __half>::value) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  } else {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+}
+
+// Two 16-byte chunks of a head, x and y, turned by eight angles: pairs (x[i], y[i]), or
+// (interleaved) neighbours, x holding the first four pairs. Products and differences in fp32; one
+// rounding to T at the end.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void turn(uint4* x, uint4* y, const float (&c)[8], const float (&s)[8]) {
+  uint32_t* const a = reinterpret_cast<uint32_t*>(x);
+  uint32_t* const b = reinterpret_cast<uint32_t*>(y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kInterleaved) {
+      const float2 u = unpack2<T>(a[i]), v = unpack2<T>(b[i]);
+      a[i] = pack2<T>(u.x * c[i] - u.y * s[i], u.y * c[i] + u.x * s[i]);
+      b[i] = pack2<T>(v.x * c[4 + i] - v.y * s[4 + i], v.y * c[4 + i] + v.x * s[4 + i]);
+    } else {
+      const float2 u = unpack2<T>(a[i]), v = unpack2<T>(b[i]);
+      const int e = 2 * i;
+      a[i] = pack2<T>(u.x * c[e] - v.x * s[e], u.y * c[e + 1] - v.y * s[e + 1]);
+      b[i] = pack2<T>(v.x * c[e] + u.x * s[e], v.y * c[e + 1] + u.y * s[e + 1]);
+    }
+  }
+}
+
+// A token's heads (its queries', keys', values') go to the lanes' groups of D / 16, a lane holding
+// two 16-byte chunks of a head: the two halves of eight pairs, whose angles it reads once for all
+// its heads.
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kUnits = D / 16, kGroups = kThreads / kUnits, kAtOnce = 2;
+  const idx_append& a = p.a;
+  pdl_wait();
+  pdl_trigger();
+  const int token = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+  const int unit = threadIdx.x % kUnits;
+  const int step = kGroups * p.splits;
+  const int queries = a.rotary && a.q ? a.num_heads : 0;
+  const int heads = queries + 2 * a.num_kv_heads;
+  const bool turned = a.rotary && unit < a.rotary_dim / 16;
+  // the lane's chunks of a rotated head, and of one that is not
+  const int half = a.rotary_dim / 16;
+  const int c0 = turned && !kInterleaved ? unit : 2 * unit;
+  const int c1 = turned && !kInterleaved ? unit + half : 2 * unit + 1;
+  const int64_t t = token;
+  int64_t slot = a.slot_mapping[t];
+  float c[8], s[8];
+  const bool bad = slot >= a.num_pages * kPageTokens;
+  if (bad && threadIdx.x == 0 && split == 0) set_error(a.dev_error, IDX_DEV_BAD_BLOCK);
+  if (bad) slot = -1;
+  if (a.rotary) {
+    int64_t pos = a.positions[t];
+    if (pos < 0 || pos >= a.num_positions) {
+      if (slot >= 0 && threadIdx.x == 0 && split == 0) set_error(a.dev_error, IDX_DEV_BAD_LEN);
+      pos = pos < 0 ? 0 : a.num_positions - 1;
+    }
+    if (turned) {
+      const float4* row = reinterpret_cast<const float4*>(a.rotary + pos * a.rotary_stride) + 2 * unit;
+      const float4* sin = row + a.rotary_dim / 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<float4*>(c + 4 * i) = __ldg(row + i);
+        *reinterpret_cast<float4*>(s + 4 * i) = __ldg(sin + i);
+      }
+    }
+  }
+  const int64_t page = slot < 0 ? 0 : slot / kPageTokens, at = slot < 0 ? 0 : slot % kPageTokens;
+  for (int h0 = split * kGroups + threadIdx.x / kUnits; h0 < heads; h0 += kAtOnce * step) {
+    uint4 x[kAtOnce], y[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int h = h0 + i * step;
+      if (h >= heads) break;
+      const T* from;
+      if (h < queries)
+        from = static_cast<const T*>(a.q) + t * a.q_stride_token + h * a.q_stride_head;
+      else if (h < queries + a.num_kv_heads)
+        from = static_cast<const T*>(a.k) + t * a.k_stride_token + (h - queries) * a.k_stride_head;
+      else
+        from = static_cast<const T*>(a.v) + t * a.v_stride_token +
+               (h - queries - a.num_kv_heads) * a.v_stride_head;
+      const bool value = h >= queries + a.num_kv_heads;
+      x[i] = *(reinterpret_cast<const uint4*>(from) + (value ? 2 * unit : c0));
+      y[i] = *(reinterpret_cast<const uint4*>(from) + (value ? 2 * unit + 1 : c1));
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int h = h0 + i * step;
+      if (h >= heads) break;
+      const bool value = h >= queries + a.num_kv_heads;
+      T* to;
+      if (h < queries) {
+        to = static_cast<T*>(a.q_out) + t * a.q_out_stride_token + h * a.q_out_stride_head;
+      } else {
+        if (slot < 0) break;
+        to = value ? static_cast<T*>(a.v_cache) + page * a.v_cache_stride_page +
+                         at * a.v_cache_stride_token +
+                         (h - queries - a.num_kv_heads) * a.v_cache_stride_head
+                   : static_cast<T*>(a.k_cache) + page * a.k_cache_stride_page +
+                         at * a.k_cache_stride_token + (h - queries) * a.k_cache_stride_head;
+      }
+      if (turned && !value) turn<T, kInterleaved>(&x[i], &y[i], c, s);
+      *(reinterpret_cast<uint4*>(to) + (value ? 2 * unit : c0)) = x[i];
+      *(reinterpret_cast<uint4*>(to) + (value ? 2 * unit + 1 : c1)) = y[i];
+    }
+  }
+}
+
+template <typename T, int D>
+idx_status launch_append(const AppendParams& p, cudaStream_t s) {
+  const auto kernel = p.a.interleaved ? append_kernel<T, D, true> : append_kernel<T, D, false>;
+  return cuda_status(launch_pdl(kernel, static_cast<unsigned>(p.a.num_tokens) * p.splits, kThreads, 0, s, p));
+}
+
+// ---------------------------------------------------------------------------
+// index keys, MXFP4
+// ---------------------------------------------------------------------------
+
+// Eight values to e2m1 codes (value 2i in the low half of byte i), round to nearest even,
+// saturating.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// The value of an e2m1 code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+  const uint32_t m = code & 7;
+  // (two bits of exponent, one of mantissa; code 1 is the subnormal 0.5)
+  const uint32_t bits = m < 2 ? m * 0x3f000000u : ((m >> 1) + 126) << 23 | (m & 1) << 22;
+  return __uint_as_float(bits | (code & 8) << 28);
+}
+
+// Sixteen lanes a token, eight values each; four lanes hold a block of 32 and
+// its largest magnitude. The scale is a power of two, so the products are exact
+// and the codes those of the definition. Bound by the reads and writes.
+__global__ void __launch_bounds__(kThreads)
+    insert_mxfp4_kernel(const __nv_bfloat16* __restrict__ k, int64_t k_stride,
+                        const int64_t* __restrict__ slots, int64_t n, uint8_t* __restrict__ cache,
+                        int64_t num_pages, __nv_bfloat16* __restrict__ values, uint32_t* err) {
+  constexpr int kLanes = 16, kAtOnce = 2, kTokens = kThreads / kLanes;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % kLanes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTokens;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kTokens; base < n; base += kAtOnce * step) {
+    const int64_t t0 = base + threadIdx.x / kLanes;
+    uint4 raw[kAtOnce];
+    int64_t slot[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t t = t0 + u * step;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      slot[u] = -1;
+      if (t < n) {
+        raw[u] = *(reinterpret_cast<const uint4*>(k + t * k_stride) + lane);
+        slot[u] = slots[t];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t t = t0 + u * step;
+      const uint32_t(&w)[4] = reinterpret_cast<const uint32_t(&)[4]>(raw[u]);
+      float x[8];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (x[i] != x[i]) x[i] = 0.f;
+        top = fmaxf(top, fabsf(x[i]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // floor(log2 top) + 127 is the exponent field (0 for subnormals, whose E is 0 too)
+      const int32_t e = max(static_cast<int32_t>(__float_as_uint(top) >> 23) - 2, 0);
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= down;
+      uint32_t code = e2m1x8(x);
+      if (top == 0.f) code = 0;  // (no signs of zeros)
+      const uint32_t e0 = __shfl_sync(0xffffffffu, e, 0, kLanes), e1 = __shfl_sync(0xffffffffu, e, 4, kLanes);
+      const uint32_t e2 = __shfl_sync(0xffffffffu, e, 8, kLanes), e3 = __shfl_sync(0xffffffffu, e, 12, kLanes);
+      if (t >= n) continue;
+      const bool bad = slot[u] >= num_pages * kPageTokens;
+      if (bad && lane == 0) set_error(err, IDX_DEV_BAD_BLOCK);
+      const bool written = slot[u] >= 0 && !bad;
+      if (written) {
+        // (entries are 68 bytes, so only 4-byte aligned)
+        uint32_t* const entry = reinterpret_cast<uint32_t*>(cache + slot[u] * kMxTokenBytes);
+        entry[lane] = code;
+        if (lane == 0) entry[kLanes] = e0 | e1 << 8 | e2 << 16 | e3 << 24;
+      }
+      if (values) {
+        // 2^(e - 127), which is subnormal for e = 0
+        const float up = __uint_as_float(e ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = pack2<__nv_bfloat16>(e2m1_value(code >> (8 * i) & 15) * up,
+                                      e2m1_value(code >> (8 * i + 4) & 15) * up);
+        *(reinterpret_cast<uint4*>(values + t * kDim) + lane) =
+            written ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+}
+
+bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
+
+}  // namespace
+}  // namespace saib
+
+using namespace saib;
+
+extern "C" {
+
+idx_status indexer_append_kv(const idx_append* a, void* stream) {
+  if (!a) return IDX_ERR_INVALID_ARG;
+  if (a->dtype != IDX_BF16 && a->dtype != IDX_FP16) return IDX_ERR_UNSUPPORTED;
+  if (a->head_dim != 64 && a->head_dim != 128) return IDX_ERR_UNSUPPORTED;
+  const bool rotate = a->rotary != nullptr, queries = rotate && a->q;
+  if (a->num_tokens < 0 || a->num_kv_heads < 1 || a->num_heads < (queries ? 1 : 0) ||
+      a->num_pages < 1 || a->num_pages > INT32_MAX)
+    return IDX_ERR_INVALID_ARG;
+  // (heads of a token as 32-bit numbers, blocks of a launch)
+  if (a->num_heads > 1 << 20 || a->num_kv_heads > 1 << 20 || a->num_tokens > 1 << 28)
+    return IDX_ERR_UNSUPPORTED;
+  if (rotate) {
+    if (a->rotary_dim < 16 || a->rotary_dim % 16 || a->rotary_dim > a->head_dim)
+      return IDX_ERR_UNSUPPORTED;
+    if (a->interleaved != 0 && a->interleaved != 1) return IDX_ERR_INVALID_ARG;
+    if (a->num_positions < 1 || a->rotary_stride < a->rotary_dim || a->rotary_stride % 4 ||
+        !aligned(a->rotary, 16))
+      return IDX_ERR_INVALID_ARG;
+  }
+  if (a->num_tokens == 0) return IDX_OK;
+  if (!a->k || !a->v || !a->slot_mapping || !a->k_cache || !a->v_cache || !aligned(a->k, 16) ||
+      !aligned(a->v, 16) || !aligned(a->slot_mapping, 8) || !aligned(a->k_cache, 16) ||
+      !aligned(a->v_cache, 16))
+    return IDX_ERR_INVALID_ARG;
+  if (rotate && (!a->positions || !aligned(a->positions, 4))) return IDX_ERR_INVALID_ARG;
+  if (queries && (!a->q_out || !aligned(a->q, 16) || !aligned(a->q_out, 16) ||
+                  !stride_ok(a->q_stride_token) || !stride_ok(a->q_stride_head) ||
+                  !stride_ok(a->q_out_stride_token) || !stride_ok(a->q_out_stride_head)))
+    return IDX_ERR_INVALID_ARG;
+  for (const int64_t s :
+       {a->k_stride_token, a->k_stride_head, a->v_stride_token, a->v_stride_head,
+        a->k_cache_stride_page, a->k_cache_stride_token, a->k_cache_stride_head,
+        a->v_cache_stride_page, a->v_cache_stride_token, a->v_cache_stride_head})
+    if (!stride_ok(s)) return IDX_ERR_INVALID_ARG;
+  AppendParams p{*a, 1};
+  if (!rotate) p.a.rotary_dim = p.a.interleaved = 0;
+  const int heads = (queries ? a->num_heads : 0) + 2 * a->num_kv_heads;
+  const int groups = kThreads / (a->head_dim / 16);
+  const int rounds = (heads + groups - 1) / groups;  // of a block alone
+  // few tokens: a block a round
+  const int64_t room = int64_t{8} * device_sm_count() / a->num_tokens;
+  p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(rounds, room)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->dtype == IDX_FP16)
+    return a->head_dim == 64 ? launch_append<__half, 64>(p, s) : launch_append<__half, 128>(p, s);
+  return a->head_dim == 64 ? launch_append<__nv_bfloat16, 64>(p, s)
+                           : launch_append<__nv_bfloat16, 128>(p, s);
+}
+
+idx_status indexer_insert_keys_mxfp4(const void* k, int64_t k_stride, const int64_t* slot_mapping,
+                                     int64_t num_tokens, int32_t head_dim, uint8_t* index_cache,
+                                     int64_t num_pages, void* values, uint32_t* dev_error,
+                                     void* stream) {
+  if (num_tokens < 0 || num_pages < 0) return IDX_ERR_INVALID_ARG;
+  if (head_dim != kDim) return IDX_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return IDX_OK;
+  if (!k || !slot_mapping || !index_cache || !aligned(k, 16) || !aligned(slot_mapping, 8) ||
+      !aligned(index_cache, 16) || !aligned(values, 16) || k_stride < kDim || k_stride % 8)
+    return IDX_ERR_INVALID_ARG;
+  const int64_t blocks = (num_tokens + kThreads / 16 - 1) / (kThreads / 16);
+  const int64_t most = int64_t{16} * device_sm_count();
+  return cuda_status(launch_pdl(insert_mxfp4_kernel, static_cast<unsigned>(std::min(blocks, most)),
+                                kThreads, 0, static_cast<cudaStream_t>(stream),
+                                static_cast<const __nv_bfloat16*>(k), k_stride, slot_mapping,
+                                num_tokens, index_cache, num_pages,
+                                static_cast<__nv_bfloat16*>(values), dev_error));
+}
+
+}  // extern "C"

@@ -85,6 +85,7 @@ __device__ int4 cut_at(const AttendParams& p, int c) {
 
 // One CTA: entries of the requests, their costs and the CTAs' cuts. Bound by
 // the latency of a few dependent loads and scans.
+template <bool kTree>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendParams p) {
   __shared__ int64_t sums[32];
   pdl_wait();
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
     int64_t cost = 0;
     if (e < entries) {
       const int b = entry_request(p.req_entry, p.num_reqs, e);
-      cost = unit_tiles(p, request_shape(p, b, false), e - p.req_entry[b]).count + p.unit_overhead;
+      cost = unit_tiles<kTree>(p, request_shape(p, b, false), e - p.req_entry[b]).count + p.unit_overhead;
     }
     const int64_t incl = carry + block_scan<kPlanThreads>(cost, sums, &total);
     if (e < entries) p.entry_cost[e + 1] = incl;
@@ -187,12 +188,12 @@ __device__ __forceinline__ bool sees(const AttendParams& p, int32_t pos, int32_t
 // accumulators o. k_at, v_at: the lane's fragment addresses within a 16-key
 // block for step & 3; q_of(f, mt, kk): query fragments; valid: bit per key (a
 // list's); all: every row sees every key; s0: the first key's position; rpos: the
-// positions of the lane's rows.
-template <typename T, int D, int MT, bool kSel, typename QOf>
+// positions of the lane's rows (kTree: what they see).
+template <typename T, int D, int MT, bool kSel, bool kTree, typename QOf, typename Pos>
 __device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8_t* smem, uint32_t kt,
                                               const uint32_t (&k_at)[4], const uint32_t (&v_at)[4],
                                               const QOf& q_of, uint32_t valid, bool all, int32_t s0,
-                                              const int32_t (&rpos)[MT][2],
+                                              const Pos (&rpos)[MT][2],
                                               float (&o)[MT][D / 8][4], float (&m)[MT][2],
                                               float (&l)[MT][2]) {
   using C = RowsCfg<D, MT>;
@@ -227,6 +228,20 @@ __device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8
       }
     }
   }
+  uint32_t see[MT][2];  // kTree: bit per key
+  if constexpr (kTree) {
+    if (!all) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) see[mt][h] = rpos[mt][h].sees(p, s0);
+    }
+  }
+  const auto seen = [&](int mt, int h, int key) -> bool {
+    if constexpr (kSel) return (valid >> key) & 1;
+    else if constexpr (kTree) return (see[mt][h] >> key) & 1;
+    else return sees(p, rpos[mt][h], s0 + key);
+  };
   uint32_t pa[MT][kSub / 16][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -249,8 +264,7 @@ __device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int key = n * 8 + 2 * (lane & 3) + e;
-            if (!(kSel ? (valid >> key) & 1 : sees(p, rpos[mt][h], s0 + key)))
-              x[n][e] = -INFINITY;
+            if (!seen(mt, h, key)) x[n][e] = -INFINITY;
           }
       }
       float mx = fmaxf(x[0][0], x[0][1]);
@@ -335,7 +349,7 @@ __device__ __forceinline__ void score_subtile(const AttendParams& p, const uint8
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                if (sees(p, rpos[mt][h], s0 + key)) o[mt][n][2 * h + e] += x;
+                if (seen(mt, h, key)) o[mt][n][2 * h + e] += x;
           }
         }
   }
@@ -386,7 +400,9 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
 // units of every request and kv head) belongs to a cluster whose blocks take equal
 // ranges of its tiles and join their results in each other's shared memory, so
 // that one launch does all.
-template <typename T, int D, int MT, bool kSel, bool kCluster>
+//
+// kTree: the rows see what TreeRow says, instead of the keys up to their position.
+template <typename T, int D, int MT, bool kSel, bool kCluster, bool kTree>
 __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const AttendParams p) {
   using C = RowsCfg<D, MT>;
   constexpr int kChunks = D / 8;         // 16-byte chunks of a row
@@ -428,16 +444,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
     first_tile = a.y;
     last_tile = b.y;
   }
-  PieceWalk<false> walk;
+  PieceWalk<false, kTree> walk;
   if constexpr (!kSel && !kCluster) {
     if (p.self_plan) {
       __shared__ int64_t sums[32];
       __shared__ int4 cuts[2];
       __shared__ ReqShape first;
-      self_plan<kWarps * 32>(p, cta, reinterpret_cast<int64_t*>(smem), sums, cuts, &first);
-      walk = PieceWalk<false>(p, cuts[0], cuts[1], first);
+      self_plan<kWarps * 32, kTree>(p, cta, reinterpret_cast<int64_t*>(smem), sums, cuts, &first);
+      walk = PieceWalk<false, kTree>(p, cuts[0], cuts[1], first);
     } else {
-      walk = PieceWalk<false>(p, p.bound[cta], p.bound[cta + 1]);
+      walk = PieceWalk<false, kTree>(p, p.bound[cta], p.bound[cta + 1]);
     }
   }
 
@@ -473,7 +489,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       u.rows = min(p.rows, shape.nq * p.group - u.row0);
       u.q0 = shape.q0;
       u.ahead = shape.keys - shape.nq;
-      u.tiles = unit_tiles(p, shape, entry);
+      u.tiles = unit_tiles<kTree>(p, shape, entry);
     } else {
       if (!walk.next(p, &u)) break;
     }
@@ -485,16 +501,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
 
     if (!kSel || u.req >= 0) {
       const int32_t p_lo = u.tiles.p_lo, p_hi = u.tiles.p_hi;
-      int32_t rpos[MT][2];  // positions of this thread's rows
+      // positions of this thread's rows, or what they see
+      typename std::conditional<kTree, TreeRow, int32_t>::type rpos[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = mt * 16 + h * 8 + (lane >> 2);
           int64_t token;
-          int head;
-          row_place(p, u, r, &token, &head, &rpos[mt][h]);
-          if (r >= u.rows) rpos[mt][h] = INT32_MIN;
+          int head, pos;
+          row_place(p, u, r, &token, &head, &pos);
+          if constexpr (kTree) rpos[mt][h] = TreeRow(p, u, token, r < u.rows);
+          else rpos[mt][h] = r < u.rows ? pos : INT32_MIN;
         }
 
       float o[MT][D / 8][4];
@@ -671,10 +689,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
           all = valid == (0xffffffffu >> (32 - kSub));
         } else {
           any = s0 <= p_hi && (s0 + kSub - 1 > w_lo || s0 < p.sinks);
-          all = s0 + kSub - 1 <= p_lo && (s0 > w_hi || s0 + kSub <= p.sinks);
+          all = s0 + kSub - 1 <= p_lo - kTree && (s0 > w_hi || s0 + kSub <= p.sinks);
         }
         if (any) {
-          score_subtile<T, D, MT, kSel>(p, smem, ring + stage * C::kStageBytes, k_at, v_at, q_of,
+          score_subtile<T, D, MT, kSel, kTree>(p, smem, ring + stage * C::kStageBytes, k_at, v_at, q_of,
                                         valid, all, s0, rpos, o, m, l);
         }
         __syncwarp();
@@ -946,7 +964,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_lists_kernel(const Atte
       issue();  // into the sub-tile that the last round read
       const uint32_t valid = s_valid[warp][stage];
       if (valid)
-        score_subtile<T, D, 1, true>(p, smem, ring + stage * C::kStageBytes, k_at, v_at, q_of, valid,
+        score_subtile<T, D, 1, true, false>(p, smem, ring + stage * C::kStageBytes, k_at, v_at, q_of, valid,
                                      valid == (0xffffffffu >> (32 - kSub)), 0, rpos, o, m, l);
       __syncwarp();
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -1118,20 +1136,20 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attend_combine_kernel(cons
   }
 }
 
-template <typename T, int D, int MT, bool kSel>
+template <typename T, int D, int MT, bool kSel, bool kTree>
 idx_status launch_rows_as(const AttendParams& p, cudaStream_t s) {
   using C = RowsCfg<D, MT>;
-  const auto kernel = attend_rows_kernel<T, D, MT, kSel, false>;
+  const auto kernel = attend_rows_kernel<T, D, MT, kSel, false, kTree>;
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_pdl(kernel, p.grid, kWarps * 32, C::kSmem, s, p));
 }
 
-template <typename T, int D, bool kSel>
+template <typename T, int D, bool kSel, bool kTree>
 idx_status launch_cluster_as(const AttendParams& p, cudaStream_t s) {
   using C = RowsCfg<D, 1>;
-  const auto kernel = attend_rows_kernel<T, D, 1, kSel, true>;
+  const auto kernel = attend_rows_kernel<T, D, 1, kSel, true, kTree>;
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
   if (e != cudaSuccess) return cuda_status(e);
@@ -1162,10 +1180,15 @@ idx_status launch_lists_as(const AttendParams& p, cudaStream_t s) {
 
 template <typename T, int D>
 idx_status launch_rows_d(const AttendParams& p, int mt, cudaStream_t s) {
+  if (p.masks)
+    return p.cluster ? launch_cluster_as<T, D, false, true>(p, s)
+                     : launch_rows_as<T, D, 1, false, true>(p, s);
   if (p.cluster)
-    return p.indices ? launch_cluster_as<T, D, true>(p, s) : launch_cluster_as<T, D, false>(p, s);
-  if (!p.indices) return launch_rows_as<T, D, 1, false>(p, s);
-  return mt == 1 ? launch_rows_as<T, D, 1, true>(p, s) : launch_rows_as<T, D, 2, true>(p, s);
+    return p.indices ? launch_cluster_as<T, D, true, false>(p, s)
+                     : launch_cluster_as<T, D, false, false>(p, s);
+  if (!p.indices) return launch_rows_as<T, D, 1, false, false>(p, s);
+  return mt == 1 ? launch_rows_as<T, D, 1, true, false>(p, s)
+                 : launch_rows_as<T, D, 2, true, false>(p, s);
 }
 
 template <typename T, int D>
@@ -1189,7 +1212,8 @@ idx_status launch_combine_as(const AttendParams& p, cudaStream_t s) {
 }  // namespace
 
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s) {
-  return cuda_status(launch_pdl(attend_plan_kernel, 1, kPlanThreads, 0, s, p));
+  return cuda_status(launch_pdl(p.masks ? attend_plan_kernel<true> : attend_plan_kernel<false>, 1,
+                                kPlanThreads, 0, s, p));
 }
 
 idx_status launch_attend_rows(const AttendParams& p, int head_dim, bool half, int mt,

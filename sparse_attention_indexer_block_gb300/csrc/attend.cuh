@@ -62,6 +62,12 @@ struct AttendParams {
   int32_t unit_overhead;           // tiles of streaming that a unit's start and end cost
   uint32_t* dev_error;
   uint64_t wait_ns;
+  // a tree's: the new tokens that each of them sees (bit j of a row's words: new token j of its
+  // request), and their positions (nullptr without a window)
+  const int32_t* masks;            // [num_tokens, mask_words]
+  int64_t mask_stride;
+  int32_t mask_words;
+  const int32_t* positions;        // [num_tokens]
 };
 
 // A unit is one kv head's block of `rows` query rows of one request (rows are
@@ -73,7 +79,9 @@ struct UnitTiles {
   int32_t first;  // tiles of the sinks
   int32_t skip;   // tiles between them and the window's
   int32_t count;  // all tiles of the unit
-  int32_t p_lo, p_hi;  // positions of the unit's first and last token
+  // positions of the unit's first and last token; of a tree the lowest that a new token can have,
+  // and the last key
+  int32_t p_lo, p_hi;
 
   __device__ __forceinline__ int32_t tile(int32_t i) const { return i < first ? i : i + skip; }
 };
@@ -102,13 +110,15 @@ __device__ __forceinline__ int32_t request_entries(const AttendParams& p, const 
 }
 
 // (All in 32 bits: num_tokens * num_heads and the table's tokens fit with room for a tile.)
+// kTree: any row of a request may see any of its new tokens, so its units have the same tiles.
+template <bool kTree>
 __device__ __forceinline__ UnitTiles unit_tiles(const AttendParams& p, const ReqShape& r, int32_t u) {
   UnitTiles t;
   const int32_t row0 = u * p.rows;
   const int32_t row1 = min(row0 + p.rows, r.nq * p.group);
   const int32_t ahead = r.keys - r.nq;
-  t.p_lo = ahead + row0 / p.group;
-  t.p_hi = ahead + (row1 - 1) / p.group;
+  t.p_lo = kTree ? ahead : ahead + row0 / p.group;
+  t.p_hi = kTree ? r.keys - 1 : ahead + (row1 - 1) / p.group;
   if (t.p_hi < 0) {
     t.first = t.skip = t.count = 0;
     return t;
@@ -145,11 +155,47 @@ __device__ __forceinline__ void row_place(const AttendParams& p, const Piece& u,
   *pos = u.ahead + i;
 }
 
+// The n lowest bits of a word, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t low_bits(int32_t n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// What a row of a tree sees: the keys before the new tokens (with a window, those that it leaves),
+// and the new tokens that its mask names.
+struct TreeRow {
+  const int32_t* mask;  // nullptr: a row that does not exist, which sees nothing
+  int32_t ahead, keys;  // the request's keys without and with its new tokens
+  int32_t pos;
+
+  TreeRow() = default;
+  __device__ __forceinline__ TreeRow(const AttendParams& p, const Piece& u, int64_t token, bool there)
+      : mask(nullptr), ahead(u.ahead), keys(u.tiles.p_hi + 1), pos(0) {
+    if (!there) return;
+    mask = p.masks + token * p.mask_stride;
+    if (p.positions) pos = max(min(max(p.positions[token], ahead), keys - 1), 0);
+  }
+
+  // Bit i: key s0 + i.
+  __device__ __forceinline__ uint32_t sees(const AttendParams& p, int32_t s0) const {
+    if (!mask) return 0;
+    uint32_t see = low_bits(ahead - s0);
+    if (p.positions) see &= ~low_bits(pos - p.window + 1 - s0) | low_bits(p.sinks - s0);
+    const int32_t c = s0 - ahead;  // new token of bit 0
+    if (c > -32) {
+      const int32_t w = c >> 5;
+      const uint32_t lo = w >= 0 && w < p.mask_words ? mask[w] : 0;
+      const uint32_t hi = w + 1 < p.mask_words ? mask[w + 1] : 0;
+      see |= __funnelshift_r(lo, hi, c & 31) & low_bits(keys - s0);
+    }
+    return see;
+  }
+};
+
 // The pieces of a CTA's range in the paged form, in order; with kFirstLast, a
 // first piece that begins inside its unit comes last. (The CTAs of one request
 // and kv head then all begin at its first keys and read them at the same time:
 // from HBM once, from L2 otherwise.)
-template <bool kFirstLast>
+template <bool kFirstLast, bool kTree>
 struct PieceWalk {
   int4 cur, end;
   ReqShape shape;   // of request cur.w
@@ -196,7 +242,7 @@ struct PieceWalk {
       u->rows = min(p.rows, shape.nq * p.group - u->row0);
       u->q0 = shape.q0;
       u->ahead = shape.keys - shape.nq;
-      u->tiles = unit_tiles(p, shape, cur.x);
+      u->tiles = unit_tiles<kTree>(p, shape, cur.x);
       u->t0 = cur.z;
       u->t1 = last ? min(end.z, u->tiles.count) : u->tiles.count;
       done = last;
@@ -361,6 +407,7 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
 // The same from the costs of whole requests (cost[b]: exclusive prefix of
 // their units' costs for one kv head), which a CTA works out for itself
 // when there are few requests.
+template <bool kTree>
 __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost, int64_t units,
                                       int c) {
   const int64_t all = cost[p.num_reqs] * p.num_kv_heads, n = cutters(p, all, units);
@@ -377,7 +424,7 @@ __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost
   const ReqShape r = request_shape(p, lo, false);
   int32_t u = 0, tiles;
   for (;; ++u) {
-    tiles = unit_tiles(p, r, u).count;
+    tiles = unit_tiles<kTree>(p, r, u).count;
     if (off < tiles + p.unit_overhead) break;
     off -= tiles + p.unit_overhead;
   }
@@ -407,7 +454,7 @@ constexpr int kMostCluster = 8;
 
 // The cuts at both ends of a CTA's range and its first request's shape, by its
 // kThreads threads; `cost` has room for num_reqs + 1. p.bound gets them too, for the join.
-template <int kThreads>
+template <int kThreads, bool kTree>
 __device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t* sums, int4* cuts,
                           ReqShape* first) {
   constexpr int kEntryShift = 40;  // one scan for both sums: costs below, entries above
@@ -418,7 +465,7 @@ __device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t
     if (b < p.num_reqs) {
       const ReqShape r = request_shape(p, b, cta == 0);
       const int32_t e = request_entries(p, r);
-      for (int32_t i = 0; i < e; ++i) n += unit_tiles(p, r, i).count + p.unit_overhead;
+      for (int32_t i = 0; i < e; ++i) n += unit_tiles<kTree>(p, r, i).count + p.unit_overhead;
       n += static_cast<int64_t>(e) << kEntryShift;
     }
     const int64_t incl = carry + block_scan<kThreads>(n, sums, &total);
@@ -429,7 +476,7 @@ __device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t
   if (threadIdx.x == 0) cost[0] = 0;
   __syncthreads();
   if (threadIdx.x < 2) {
-    const int4 at = cut_at_request(p, cost, units, cta + threadIdx.x);
+    const int4 at = cut_at_request<kTree>(p, cost, units, cta + threadIdx.x);
     cuts[threadIdx.x] = at;
     if (threadIdx.x == 0 && at.w < p.num_reqs) *first = request_shape(p, at.w, false);
     if (threadIdx.x == 0 || cta == p.grid - 1) p.bound[cta + threadIdx.x] = at;

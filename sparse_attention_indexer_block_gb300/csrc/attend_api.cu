@@ -196,39 +196,40 @@ idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& 
   return IDX_OK;
 }
 
-}  // namespace
-}  // namespace saib
+// A tree's masks and positions.
+struct Tree {
+  const int32_t* masks;
+  int64_t stride;
+  int32_t words;
+  const int32_t* positions;
+};
 
-using namespace saib;
-
-extern "C" {
-
-idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, int32_t num_heads,
-                                          int32_t num_kv_heads, int32_t head_dim, size_t* bytes) {
-  if (!bytes || num_tokens < 0 || num_reqs < 0 || num_heads < 1 || num_kv_heads < 1 ||
-      num_heads % num_kv_heads != 0)
-    return IDX_ERR_INVALID_ARG;
-  if ((head_dim != 64 && head_dim != 128) ||
-      static_cast<int64_t>(num_tokens) * num_heads > kMostRows)
-    return IDX_ERR_UNSUPPORTED;
-  *bytes = most_workspace(num_tokens, num_reqs, num_heads, head_dim);
-  return IDX_OK;
-}
-
-idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
+// Attention of the new tokens over the paged cache: causal, or of a tree.
+idx_status attend_new_tokens(const idx_attend* a, const Tree* tree, void* stream) {
   idx_status st = check_attend(a);
   if (st != IDX_OK) return st;
   if (a->window < 0 || a->sinks < 0 || a->max_query_len < 0) return IDX_ERR_INVALID_ARG;
+  if (tree && (tree->words < 1 || tree->stride < tree->words)) return IDX_ERR_INVALID_ARG;
   if (a->num_tokens == 0 || a->num_reqs == 0) return IDX_OK;
   if (!a->seq_lens || !aligned(a->seq_lens, 4)) return IDX_ERR_INVALID_ARG;
   AttendParams p = attend_params(a);
   p.seq_lens = a->seq_lens;
+  if (tree) {
+    if (!tree->masks || !aligned(tree->masks, 4) || !aligned(tree->positions, 4) ||
+        (a->window > 0 && !tree->positions))
+      return IDX_ERR_INVALID_ARG;
+    p.masks = tree->masks;
+    p.mask_stride = tree->stride;
+    p.mask_words = tree->words;
+    p.positions = a->window > 0 ? tree->positions : nullptr;
+  }
   if (a->window > 0) {
     p.window = std::min(a->window, kMostKeys);
     p.sinks = a->sinks;
   }
-  const int64_t longest =
+  int64_t longest =
       a->max_query_len > 0 ? std::min(a->max_query_len, a->num_tokens) : a->num_tokens;
+  if (tree) longest = std::min(longest, 32 * int64_t{tree->words});  // (no mask names more)
   // The row-block kernel holds 16 rows at once and reads K and V again for the next 16; from
   // 17 rows on the tensor-memory kernel is faster (24 requests of 8000 keys, 8 kv heads of 128:
   // 15 rows 132 against 140 us, 20 rows 173 against 142).
@@ -263,6 +264,35 @@ idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
           : launch_attend_rows(p, a->head_dim, half, v.mt, s);
   if (st != IDX_OK) return st;
   return launch_attend_combine(p, a->head_dim, half, s);
+}
+
+}  // namespace
+}  // namespace saib
+
+using namespace saib;
+
+extern "C" {
+
+idx_status indexer_attend_workspace_bytes(int32_t num_tokens, int32_t num_reqs, int32_t num_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, size_t* bytes) {
+  if (!bytes || num_tokens < 0 || num_reqs < 0 || num_heads < 1 || num_kv_heads < 1 ||
+      num_heads % num_kv_heads != 0)
+    return IDX_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) ||
+      static_cast<int64_t>(num_tokens) * num_heads > kMostRows)
+    return IDX_ERR_UNSUPPORTED;
+  *bytes = most_workspace(num_tokens, num_reqs, num_heads, head_dim);
+  return IDX_OK;
+}
+
+idx_status indexer_attend_paged(const idx_attend* a, void* stream) {
+  return attend_new_tokens(a, nullptr, stream);
+}
+
+idx_status indexer_attend_tree(const idx_attend* a, const int32_t* masks, int64_t mask_stride,
+                               int32_t mask_words, const int32_t* positions, void* stream) {
+  const Tree tree{masks, mask_stride, mask_words, positions};
+  return attend_new_tokens(a, &tree, stream);
 }
 
 idx_status indexer_attend_selected(const idx_attend* a, void* stream) {

@@ -174,28 +174,28 @@ __device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
 }
 
 // Whether some row of the unit does not see some key of the tile.
+template <bool kTree>
 __device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles& t, int32_t tile) {
   const int32_t s0 = tile * kTileTc;
-  return !(s0 + kTileTc - 1 <= t.p_lo && (s0 > t.p_hi - p.window || s0 + kTileTc <= p.sinks));
-}
-
-// The n lowest bits of a word, n clamped to [0, 32].
-__device__ __forceinline__ uint32_t low_bits(int32_t n) {
-  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+  return !(s0 + kTileTc - 1 <= t.p_lo - kTree && (s0 > t.p_hi - p.window || s0 + kTileTc <= p.sinks));
 }
 
 // The infinities and NaNs that were left out of the edge tiles' products, for
 // a row that sees them: added to the row where it was written.
-template <typename T, int D>
-__device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u, int32_t pos,
+template <typename T, int D, bool kTree, typename Pos>
+__device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u, const Pos pos,
                                            T* out, float* part) {
   const int32_t* bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
   for (int j = u.t0; j < u.t1; ++j) {
     const int32_t tile = u.tiles.tile(j);
-    if (!edge_tile(p, u.tiles, tile)) continue;
+    if (!edge_tile<kTree>(p, u.tiles, tile)) continue;
     for (int i = 0; i < kTileTc; ++i) {
       const int32_t key = tile * kTileTc + i;
-      if (key > pos || (key >= p.sinks && pos - key >= p.window)) continue;
+      if constexpr (kTree) {
+        if (!(pos.sees(p, key) & 1)) continue;
+      } else {
+        if (key > pos || (key >= p.sinks && pos - key >= p.window)) continue;
+      }
       const int32_t page = bt[key / kPageTokens];
       if (page < 0 || page >= p.num_pages) continue;
       const T* v = static_cast<const T*>(p.v) + page * p.v_stride_page +
@@ -229,8 +229,9 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u,
 // either, and two slots do not hide all of it.
 //
 // kSelfPlan: the blocks work out their ranges themselves. (A kernel of its own: with the code in
-// one, the others take 5 % longer.)
-template <typename T, int D, bool kSelfPlan>
+// one, the others take 5 % longer.) kTree: the rows see what TreeRow says, instead of the keys up
+// to their position.
+template <typename T, int D, bool kSelfPlan, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ ReqShape first;
     // (the costs lie where the queries will: written by these threads too, not by TMA; the cuts
     // are in p.bound as well)
-    self_plan<kThreads>(p, blockIdx.x, reinterpret_cast<int64_t*>(smem), sums, cuts, &first);
+    self_plan<kThreads, kTree>(p, blockIdx.x, reinterpret_cast<int64_t*>(smem), sums, cuts, &first);
     if (threadIdx.x == 0) bars.cut_end = cuts[1];
   }
   Piece u;
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t v_tiles = 0;
         int filled = 0;  // places of the ring of pieces
         bool ok = true;
-        PieceWalk<true> walk(p, p.bound[blockIdx.x],
+        PieceWalk<true, kTree> walk(p, p.bound[blockIdx.x],
                              kSelfPlan ? bars.cut_end : p.bound[blockIdx.x + 1]);
         while (ok) {
           if (!walk.next(p, &u)) u.req = -1;
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int stage = va.stage;
           if (!(ok = wait_warp(&bars.v_full[stage], va.phase))) break;
           va.step();
-          if (!edge_tile(p, u.tiles, tile)) {
+          if (!edge_tile<kTree>(p, u.tiles, tile)) {
             if (lane == 0) mbar_arrive(&bars.v_ok[stage]);
             continue;
           }
@@ -648,6 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int head, pos;
       row_place(p, u, r, &token, &head, &pos);
       if (r >= u.rows) pos = INT32_MIN;
+      TreeRow tree;
+      if constexpr (kTree) tree = TreeRow(p, u, token, r < u.rows);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         const int32_t tile = u.tiles.tile(u.t0 + j);
@@ -663,15 +666,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.s_read[slot]);
         }
-        if (edge_tile(p, u.tiles, tile)) {
+        if (edge_tile<kTree>(p, u.tiles, tile)) {
           // bit i of a word: key s0 + i is seen (i <= hi and (i > lo or i < first))
           const int32_t s0 = tile * kTileTc;
           const int32_t hi = max(pos, -1) - s0, lo = max(pos, -1) - p.window - s0;
           const int32_t first = p.sinks - s0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t see = low_bits(hi + 1 - 32 * c) &
-                                 (~low_bits(lo + 1 - 32 * c) | low_bits(first - 32 * c));
+            uint32_t see;
+            if constexpr (kTree)
+              see = tree.sees(p, s0 + 32 * c);
+            else
+              see = low_bits(hi + 1 - 32 * c) &
+                    (~low_bits(lo + 1 - 32 * c) | low_bits(first - 32 * c));
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!(see >> i & 1)) s[c][i] = -INFINITY;
@@ -805,9 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (odd) {
         __threadfence_block();  // (the row was written by four lanes)
         __syncwarp();
-        if (r < u.rows)
-          add_nonfinite<T, D>(p, u, pos, whole ? static_cast<T*>(p.out) + at * D : nullptr,
-                              p.part_o + part * D);
+        if (r < u.rows) {
+          T* const out = whole ? static_cast<T*>(p.out) + at * D : nullptr;
+          if constexpr (kTree) add_nonfinite<T, D, true>(p, u, tree, out, p.part_o + part * D);
+          else add_nonfinite<T, D, false>(p, u, pos, out, p.part_o + part * D);
+        }
         __syncwarp();
       }
       tc_fence_before();
@@ -853,11 +862,11 @@ bool encode_map(CUtensorMap* map, const void* base, bool half, int head_dim, int
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, bool kSelfPlan>
+template <typename T, int D, bool kSelfPlan, bool kTree>
 idx_status launch_tc_as(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         cudaStream_t s) {
   using C = TcCfg<D>;
-  const auto kernel = attend_tc_kernel<T, D, kSelfPlan>;
+  const auto kernel = attend_tc_kernel<T, D, kSelfPlan, kTree>;
   // (the register split hands out what the launch holds, no more)
   static std::atomic<bool> configured[kMaxDevices];
   const cudaError_t e = allow_smem<C::kSmem, kRegsLaunch>(kernel, configured);
@@ -868,8 +877,11 @@ idx_status launch_tc_as(const AttendParams& p, const CUtensorMap& kmap, const CU
 template <typename T, int D>
 idx_status launch_tc_d(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                        cudaStream_t s) {
-  return p.self_plan ? launch_tc_as<T, D, true>(p, kmap, vmap, s)
-                     : launch_tc_as<T, D, false>(p, kmap, vmap, s);
+  if (p.masks)
+    return p.self_plan ? launch_tc_as<T, D, true, true>(p, kmap, vmap, s)
+                       : launch_tc_as<T, D, false, true>(p, kmap, vmap, s);
+  return p.self_plan ? launch_tc_as<T, D, true, false>(p, kmap, vmap, s)
+                     : launch_tc_as<T, D, false, false>(p, kmap, vmap, s);
 }
 
 bool map_stride_ok(int64_t stride, int64_t entries) {
