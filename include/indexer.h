@@ -745,8 +745,9 @@ idx_status indexer_compact_pages(const idx_page_pool* pools, int32_t num_pools, 
  * ------------------------------------
  */
 
-/* Arguments of indexer_append_kv. Strides in elements, multiples of 8; the
- * head_dim values contiguous; addresses of values 16-byte aligned. */
+/* Arguments of indexer_append_kv. Strides in elements, multiples of 8 (those of a
+ * dimension of one entry are not looked at; q_out and the caches have entries
+ * apart); the head_dim values contiguous; addresses of values 16-byte aligned. */
 typedef struct idx_append {
   const void* q;               /* nullable: [num_tokens, num_heads, head_dim] */
   const void* k;               /* [num_tokens, num_kv_heads, head_dim] */

@@ -1001,25 +1001,11 @@ def _need_vector(name, what, t, dtype, n):
     """A contiguous tensor [n] of that type (n None: any size)."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         _refuse(name, f"{what} must be a tensor of {dtype}")
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        _refuse(name, f"{what} has shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 1 or (n is not None and shape[0] != n):
+        _refuse(name, f"{what} has shape {tuple(shape)}")
     if not t.is_contiguous():
         _refuse(name, f"{what} must be contiguous")
-
-
-def _outer_strides(name, what, t, written=False):
-    """Strides of all dimensions but the last, which must be contiguous (0 for a dimension of one
-    entry, whose stride is never used)."""
-    *strides, last = t.stride()
-    *shape, dim = t.shape
-    if last != 1 and dim > 1:
-        _refuse(name, f"{what} must be contiguous in its last dimension")
-    for i, n in enumerate(shape):
-        if n == 1:
-            strides[i] = 0
-        elif written and strides[i] == 0 and n:
-            _refuse(name, f"{what}'s entries overlap")
-    return strides
 
 
 def indexer_append_kv(k, v, k_cache, v_cache, slot_mapping, q=None, positions=None, rotary=None,
@@ -1031,28 +1017,35 @@ def indexer_append_kv(k, v, k_cache, v_cache, slot_mapping, q=None, positions=No
     a multiple of 16) the first rotary_dim values of the keys, and of the
     queries q [tokens, heads, dim] if given, are rotated to their positions (int32
     [tokens]) on the way: value i with i + rotary_dim / 2, or neighbours when
-    interleaved. Any strides that keep dim contiguous. Returns the rotated queries
-    (q_out; q itself may be given), None without q."""
+    interleaved. Any strides that keep dim contiguous and are multiples of 8. Returns
+    the rotated queries (q_out; q itself may be given), None without q."""
     name = "indexer_append_kv"
-    for what, t, dims in (("k", k, 3), ("v", v, 3), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4)):
-        if not isinstance(t, torch.Tensor) or t.dim() != dims:
-            _refuse(name, f"{what} must have {dims} dimensions")
-    tokens, kv_heads, dim = k.shape
-    dtype = k.dtype
+    for t in (k, v, k_cache, v_cache):
+        if not isinstance(t, torch.Tensor):
+            _refuse(name, "k, v, k_cache and v_cache must be tensors")
+    shape, cache, dtype = k.shape, k_cache.shape, k.dtype
+    if len(shape) != 3 or len(cache) != 4:
+        _refuse(name, "k and v must have 3 dimensions, k_cache and v_cache 4")
     if dtype not in _ATTEND_TYPES:
         _refuse(name, f"k is {dtype}, not bfloat16 or float16", _UNSUPPORTED)
-    if v.dtype is not dtype or k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+    if not dtype is v.dtype is k_cache.dtype is v_cache.dtype:
         _refuse(name, "k, v, k_cache and v_cache differ in type")
+    tokens, kv_heads, dim = shape
+    pages, page, cache_heads, cache_dim = cache
     if dim != 64 and dim != 128:
         _refuse(name, f"head_dim {dim}, not 64 or 128", _UNSUPPORTED)
-    pages, page = k_cache.shape[:2]
-    if v.shape != k.shape or k_cache.shape[2:] != k.shape[1:] or v_cache.shape != k_cache.shape:
+    if v.shape != shape or cache_heads != kv_heads or cache_dim != dim or v_cache.shape != cache:
         _refuse(name, "k and v must be [tokens, kv heads, dim], the caches [pages, 64, kv heads, dim]")
     if page != PAGE_TOKENS:
         _refuse(name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
+    k0, k1, kd = k.stride()
+    v0, v1, vd = v.stride()
+    kp, kt, kh, kcd = k_cache.stride()
+    vp, vt, vh, vcd = v_cache.stride()
+    if not kd == vd == kcd == vcd == 1:
+        _refuse(name, "k, v, k_cache and v_cache must be contiguous in their last dimension")
     _need_vector(name, "slot_mapping", slot_mapping, torch.int64, tokens)
-    heads = rotary_dim = num_positions = rotary_stride = 0
-    qs = os = (0, 0)
+    heads = rotary_dim = num_positions = rotary_stride = q0 = q1 = o0 = o1 = pos_at = rot_at = q_at = 0
     if rotary is None:
         if q is not None or positions is not None or q_out is not None:
             _refuse(name, "q, positions and q_out belong to a rotation")
@@ -1062,64 +1055,79 @@ def indexer_append_kv(k, v, k_cache, v_cache, slot_mapping, q=None, positions=No
         num_positions, rotary_dim = rotary.shape
         if rotary_dim < 16 or rotary_dim % 16 or rotary_dim > dim:
             _refuse(name, f"rotary_dim {rotary_dim}, not a multiple of 16 up to {dim}", _UNSUPPORTED)
-        rotary_stride = _outer_strides(name, "rotary", rotary)[0] or rotary_dim
-        if positions is None:
-            _refuse(name, "positions is missing")
+        rotary_stride, last = rotary.stride()
+        if last != 1:
+            _refuse(name, "rotary must be contiguous in its last dimension")
+        if num_positions == 1:
+            rotary_stride = rotary_dim
         _need_vector(name, "positions", positions, _I32T, tokens)
+        pos_at, rot_at = positions.data_ptr(), rotary.data_ptr()
         if q is not None:
-            if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] != tokens \
-                    or q.shape[2] != dim or q.shape[1] < 1 or q.dtype is not dtype:
-                _refuse(name, f"q must be {dtype} [tokens, heads, {dim}]")
-            heads = q.shape[1]
-            qs = _outer_strides(name, "q", q)
+            if not isinstance(q, torch.Tensor) or q.dtype is not dtype:
+                _refuse(name, f"q must be a tensor of {dtype}")
+            q_shape = q.shape
+            if len(q_shape) != 3 or q_shape[0] != tokens or q_shape[2] != dim or q_shape[1] < 1:
+                _refuse(name, f"q must be [{tokens}, heads, {dim}]")
+            heads, q_at = q_shape[1], q.data_ptr()
+            q0, q1, last = q.stride()
+            if last != 1:
+                _refuse(name, "q must be contiguous in its last dimension")
             if q_out is not None:
-                if not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape or q_out.dtype is not dtype:
+                if not isinstance(q_out, torch.Tensor) or q_out.shape != q_shape or q_out.dtype is not dtype:
                     _refuse(name, "q_out must be a tensor like q")
-                os = _outer_strides(name, "q_out", q_out, True)
+                o0, o1, last = q_out.stride()
+                if last != 1:
+                    _refuse(name, "q_out must be contiguous in its last dimension")
         elif q_out is not None:
             _refuse(name, "q_out without q")
-    ks, vs = _outer_strides(name, "k", k), _outer_strides(name, "v", v)
-    kc = _outer_strides(name, "k_cache", k_cache, True)
-    vc = _outer_strides(name, "v_cache", v_cache, True)
     _need_error(name, dev_error)
-    index = _need_device(name, k, v, k_cache, v_cache, slot_mapping, q, positions, rotary, q_out, dev_error)
+    index = _need_device(name, k, v, k_cache, v_cache, slot_mapping, positions, rotary, q, q_out, dev_error)
     with _On(index, stream) as s:
         if heads and q_out is None:
-            q_out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
-            os = (heads * dim, dim)
-        _ok(name, load().indexer_append_kv(_APPEND_BYTES.pack(
-            _at(q) or 0, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), _at(positions) or 0,
-            _at(rotary) or 0, _at(q_out) or 0, k_cache.data_ptr(), v_cache.data_ptr(), _at(dev_error) or 0,
-            *qs, *ks, *vs, *os, *kc, *vc, pages, num_positions, rotary_stride, tokens, heads, kv_heads,
-            dim, _ATTEND_TYPES[dtype], rotary_dim, 1 if interleaved else 0), s))
+            q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+            o0, o1 = heads * dim, dim
+        st = (_lib or load()).indexer_append_kv(_APPEND_BYTES.pack(
+            q_at, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), pos_at, rot_at,
+            q_out.data_ptr() if heads else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+            0 if dev_error is None else dev_error.data_ptr(), q0, q1, k0, k1, v0, v1, o0, o1, kp, kt, kh,
+            vp, vt, vh, pages, num_positions, rotary_stride, tokens, heads, kv_heads, dim,
+            _ATTEND_TYPES[dtype], rotary_dim, 1 if interleaved else 0), s)
+        if st:
+            _check(name, st)
     return q_out
 
 
 def indexer_insert_keys_mxfp4(k, slot_mapping, index_cache, values=None, dev_error=None, stream=None):
-    """Quantises k (bf16 [T, 128], rows of any stride) to MXFP4 entries and writes them into the
-    paged index cache (uint8 [pages, 4352]) at slot_mapping (int64 [T]); in place. values (bf16
-    [T, 128], contiguous) gets what the entries stand for."""
+    """Quantises k (bf16 [T, 128], rows of any stride that is a multiple of 8) to MXFP4 entries and
+    writes them into the paged index cache (uint8 [pages, 4352]) at slot_mapping (int64 [T]); in
+    place. values (bf16 [T, 128], contiguous) gets what the entries stand for."""
     name = "indexer_insert_keys_mxfp4"
     if not isinstance(k, torch.Tensor) or k.dim() != 2 or k.dtype is not torch.bfloat16:
         _refuse(name, "k must be a bfloat16 tensor [tokens, 128]")
-    tokens, dim = k.shape
+    shape = k.shape
+    tokens, dim = shape
     if dim != HEAD_DIM:
         _refuse(name, f"keys of {dim} values, not {HEAD_DIM}", _UNSUPPORTED)
-    stride = _outer_strides(name, "k", k)[0] or dim
+    stride, last = k.stride()
+    if last != 1:
+        _refuse(name, "k must be contiguous in its last dimension")
     _need_vector(name, "slot_mapping", slot_mapping, torch.int64, tokens)
     if not isinstance(index_cache, torch.Tensor) or index_cache.dtype is not torch.uint8 \
             or index_cache.dim() != 2 or index_cache.shape[1] != MXFP4_PAGE_BYTES \
             or not index_cache.is_contiguous():
         _refuse(name, f"index_cache must be a contiguous uint8 tensor [pages, {MXFP4_PAGE_BYTES}]")
-    if values is not None and not (isinstance(values, torch.Tensor) and values.shape == k.shape
+    if values is not None and not (isinstance(values, torch.Tensor) and values.shape == shape
                                    and values.dtype is torch.bfloat16 and values.is_contiguous()):
         _refuse(name, "values must be a contiguous bfloat16 tensor of k's shape")
     _need_error(name, dev_error)
     index = _need_device(name, k, slot_mapping, index_cache, values, dev_error)
     with _On(index, stream) as s:
-        _ok(name, load().indexer_insert_keys_mxfp4(
-            k.data_ptr(), stride, slot_mapping.data_ptr(), tokens, dim, index_cache.data_ptr(),
-            index_cache.shape[0], _at(values), _at(dev_error), s))
+        st = (_lib or load()).indexer_insert_keys_mxfp4(
+            k.data_ptr(), stride if tokens > 1 else dim, slot_mapping.data_ptr(), tokens, dim,
+            index_cache.data_ptr(), index_cache.shape[0], None if values is None else values.data_ptr(),
+            None if dev_error is None else dev_error.data_ptr(), s)
+        if st:
+            _check(name, st)
     return index_cache
 
 
@@ -1168,51 +1176,67 @@ def indexer_plan_tree(parents, seq_lens, query_start_loc, max_query_len: int, wi
     return masks, positions, paths
 
 
+@functools.lru_cache(maxsize=256)
+def _token_layout(shape, strides, dtype):
+    """idx_token_pool entries of a tensor of that layout, as (offset, page stride, token stride, piece
+    stride, pieces, piece bytes); a text where it has none."""
+    if len(shape) < 2 or shape[0] < 1:
+        return "a pool must be a tensor [pages, 64, ...] or a uint8 index cache"
+    pages = shape[0]
+    if dtype is torch.uint8 and len(shape) == 2 and shape[1] in (PAGE_BYTES, MXFP4_PAGE_BYTES):
+        stride = strides[0] if pages > 1 else shape[1]
+        if strides[1] != 1 or stride < shape[1] or stride % 4:
+            return "an index cache's pages must be contiguous and of whole words"
+        if shape[1] == PAGE_BYTES:
+            return ((0, stride, HEAD_DIM, 0, 1, HEAD_DIM), (PAGE_TOKENS * HEAD_DIM, stride, 4, 0, 1, 4))
+        return ((0, stride, MXFP4_TOKEN_BYTES, 0, 1, MXFP4_TOKEN_BYTES),)
+    if shape[1] != PAGE_TOKENS:
+        return f"pages of {shape[1]} tokens, not {PAGE_TOKENS}"
+    if any(n > 1 and st == 0 for n, st in zip(shape, strides)):
+        return "a pool's tokens overlap"
+    size = dtype.itemsize
+    # a token's values from the last dimension up to where they stop being contiguous
+    run, dim = size, len(shape) - 1
+    while dim >= 2 and (shape[dim] == 1 or strides[dim] * size == run):
+        run *= shape[dim]
+        dim -= 1
+    pieces, piece_stride = 1, run
+    if dim >= 2:
+        pieces, piece_stride = shape[dim], strides[dim] * size
+        if any(n > 1 for n in shape[2:dim]):
+            return "a pool's token must be one run of values or evenly spaced ones"
+    token_stride = strides[1] * size
+    page_stride = strides[0] * size if pages > 1 else token_stride
+    if run == 0 or run % 4 or token_stride % 4 or page_stride % 4 or piece_stride % 4:
+        return "a pool's tokens must be of whole 4-byte words"
+    return ((0, page_stride, token_stride, piece_stride, pieces, run),)
+
+
 def _token_pools(name, pools):
     """(idx_token_pool entries as bytes, their number, pages): tensors [pages, 64, ...], or uint8
     index caches [pages, 8448] and [pages, 4352]."""
-    out, pages = [], None
+    out, n, pages = [], 0, None
     for t in pools:
-        if not isinstance(t, torch.Tensor) or t.dim() < 2 or t.shape[0] < 1:
+        if not isinstance(t, torch.Tensor):
             _refuse(name, "a pool must be a tensor [pages, 64, ...] or a uint8 index cache")
-        shape, at = t.shape, t.data_ptr()
-        if pages is not None and shape[0] != pages:
+        shape = t.shape
+        layout = _token_layout(shape, t.stride(), t.dtype)
+        if isinstance(layout, str):
+            _refuse(name, layout, _UNSUPPORTED if layout.startswith("pages of") else _INVALID)
+        if pages is None:
+            pages = shape[0]
+        elif shape[0] != pages:
             _refuse(name, "the pools differ in pages")
-        pages = shape[0]
-        if t.dtype is torch.uint8 and len(shape) == 2 and shape[1] in (PAGE_BYTES, MXFP4_PAGE_BYTES):
-            if t.stride(1) != 1 or (pages > 1 and t.stride(0) < shape[1]) or t.stride(0) % 4 or at % 4:
-                _refuse(name, "an index cache's pages must be contiguous and of whole words")
-            if shape[1] == PAGE_BYTES:
-                values = PAGE_TOKENS * HEAD_DIM
-                out.append((at, t.stride(0), HEAD_DIM, 0, 1, HEAD_DIM))
-                out.append((at + values, t.stride(0), 4, 0, 1, 4))
-            else:
-                out.append((at, t.stride(0), MXFP4_TOKEN_BYTES, 0, 1, MXFP4_TOKEN_BYTES))
-            continue
-        if shape[1] != PAGE_TOKENS:
-            _refuse(name, f"pages of {shape[1]} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
-        size, strides = t.element_size(), t.stride()
-        if any(n > 1 and st == 0 for n, st in zip(shape, strides)):
-            _refuse(name, "a pool's tokens overlap")
-        # a token's values from the last dimension up to where they stop being contiguous
-        run, dim = size, len(shape) - 1
-        while dim >= 2 and (shape[dim] == 1 or strides[dim] * size == run):
-            run *= shape[dim]
-            dim -= 1
-        pieces = piece_stride = 1
-        if dim >= 2:
-            pieces, piece_stride = shape[dim], strides[dim] * size
-            if any(n > 1 for n in shape[2:dim]):
-                _refuse(name, "a pool's token must be one run of values or evenly spaced ones")
-        page_stride, token_stride = strides[0] * size, strides[1] * size
-        if pages == 1:
-            page_stride = token_stride
-        if dim < 2:
-            piece_stride = run
-        if run == 0 or run % 4 or at % 4 or token_stride % 4 or page_stride % 4 or piece_stride % 4:
-            _refuse(name, "a pool's tokens must be of whole 4-byte words")
-        out.append((at, page_stride, token_stride, piece_stride, pieces, run))
-    return b"".join(_TOKEN_POOL_BYTES.pack(*e) for e in out), len(out), pages
+        at = t.data_ptr()
+        for offset, *entry in layout:
+            out += (at + offset, *entry)
+            n += 1
+    return _token_pool_struct(n).pack(*out), n, pages
+
+
+@functools.lru_cache(maxsize=64)
+def _token_pool_struct(n):
+    return struct.Struct("=" + "Q3q2i" * n)
 
 
 def indexer_commit_tree(pools, block_table, seq_lens, query_start_loc, accepted, ref_counts=None,

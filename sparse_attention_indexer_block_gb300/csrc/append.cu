@@ -54,7 +54,7 @@ __device__ __forceinline__ void turn(uint4* x, uint4* y, const float (&c)[8], co
 
 // A token's heads (its queries', keys', values') go to the lanes' groups of D / 16, a lane holding
 // two 16-byte chunks of a head: the two halves of eight pairs, whose angles it reads once for all
-// its heads.
+// its heads. The first heads are asked for before the token's slot and position are there.
 template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kUnits = D / 16, kGroups = kThreads / kUnits, kAtOnce = 2;
@@ -65,26 +65,40 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int unit = threadIdx.x % kUnits;
   const int step = kGroups * p.splits;
   const int queries = a.rotary && a.q ? a.num_heads : 0;
-  const int heads = queries + 2 * a.num_kv_heads;
+  const int keys = queries + a.num_kv_heads, heads = keys + a.num_kv_heads;
   const bool turned = a.rotary && unit < a.rotary_dim / 16;
-  // the lane's chunks of a rotated head, and of one that is not
-  const int half = a.rotary_dim / 16;
+  // the lane's chunks of a rotated head (of others: 2 unit and the next)
   const int c0 = turned && !kInterleaved ? unit : 2 * unit;
-  const int c1 = turned && !kInterleaved ? unit + half : 2 * unit + 1;
+  const int c1 = turned && !kInterleaved ? unit + a.rotary_dim / 16 : 2 * unit + 1;
   const int64_t t = token;
-  int64_t slot = a.slot_mapping[t];
-  float c[8], s[8];
-  const bool bad = slot >= a.num_pages * kPageTokens;
-  if (bad && threadIdx.x == 0 && split == 0) set_error(a.dev_error, IDX_DEV_BAD_BLOCK);
-  if (bad) slot = -1;
-  if (a.rotary) {
-    int64_t pos = a.positions[t];
-    if (pos < 0 || pos >= a.num_positions) {
-      if (slot >= 0 && threadIdx.x == 0 && split == 0) set_error(a.dev_error, IDX_DEV_BAD_LEN);
-      pos = pos < 0 ? 0 : a.num_positions - 1;
+  const T* const q = static_cast<const T*>(a.q) + t * a.q_stride_token;
+  const T* const k = static_cast<const T*>(a.k) + t * a.k_stride_token;
+  const T* const v = static_cast<const T*>(a.v) + t * a.v_stride_token;
+  uint4 x[kAtOnce], y[kAtOnce];
+  const auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int h = h0 + i * step;
+      if (h >= heads) break;
+      const T* const from = h < queries ? q + h * a.q_stride_head
+                            : h < keys  ? k + (h - queries) * a.k_stride_head
+                                        : v + (h - keys) * a.v_stride_head;
+      x[i] = *(reinterpret_cast<const uint4*>(from) + (h < keys ? c0 : 2 * unit));
+      y[i] = *(reinterpret_cast<const uint4*>(from) + (h < keys ? c1 : 2 * unit + 1));
     }
+  };
+  int h0 = split * kGroups + threadIdx.x / kUnits;
+  load(h0);
+  int64_t slot = a.slot_mapping[t];
+  int64_t pos = a.rotary ? a.positions[t] : 0;
+  const bool first = threadIdx.x == 0 && split == 0;
+  float c[8], s[8];
+  if (a.rotary) {
+    const int64_t in = min(max(pos, int64_t{0}), a.num_positions - 1);
+    if (first && in != pos && slot >= 0 && slot < a.num_pages * kPageTokens)
+      set_error(a.dev_error, IDX_DEV_BAD_LEN);
     if (turned) {
-      const float4* row = reinterpret_cast<const float4*>(a.rotary + pos * a.rotary_stride) + 2 * unit;
+      const float4* row = reinterpret_cast<const float4*>(a.rotary + in * a.rotary_stride) + 2 * unit;
       const float4* sin = row + a.rotary_dim / 8;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -93,45 +107,29 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       }
     }
   }
+  if (slot >= a.num_pages * kPageTokens) {
+    if (first) set_error(a.dev_error, IDX_DEV_BAD_BLOCK);
+    slot = -1;
+  }
   const int64_t page = slot < 0 ? 0 : slot / kPageTokens, at = slot < 0 ? 0 : slot % kPageTokens;
-  for (int h0 = split * kGroups + threadIdx.x / kUnits; h0 < heads; h0 += kAtOnce * step) {
-    uint4 x[kAtOnce], y[kAtOnce];
+  T* const q_out = static_cast<T*>(a.q_out) + t * a.q_out_stride_token;
+  T* const k_out = static_cast<T*>(a.k_cache) + page * a.k_cache_stride_page + at * a.k_cache_stride_token;
+  T* const v_out = static_cast<T*>(a.v_cache) + page * a.v_cache_stride_page + at * a.v_cache_stride_token;
+  for (;;) {
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const int h = h0 + i * step;
-      if (h >= heads) break;
-      const T* from;
-      if (h < queries)
-        from = static_cast<const T*>(a.q) + t * a.q_stride_token + h * a.q_stride_head;
-      else if (h < queries + a.num_kv_heads)
-        from = static_cast<const T*>(a.k) + t * a.k_stride_token + (h - queries) * a.k_stride_head;
-      else
-        from = static_cast<const T*>(a.v) + t * a.v_stride_token +
-               (h - queries - a.num_kv_heads) * a.v_stride_head;
-      const bool value = h >= queries + a.num_kv_heads;
-      x[i] = *(reinterpret_cast<const uint4*>(from) + (value ? 2 * unit : c0));
-      y[i] = *(reinterpret_cast<const uint4*>(from) + (value ? 2 * unit + 1 : c1));
+      if (h >= heads || (h >= queries && slot < 0)) break;
+      T* const to = h < queries ? q_out + h * a.q_out_stride_head
+                    : h < keys  ? k_out + (h - queries) * a.k_cache_stride_head
+                                : v_out + (h - keys) * a.v_cache_stride_head;
+      if (turned && h < keys) turn<T, kInterleaved>(&x[i], &y[i], c, s);
+      *(reinterpret_cast<uint4*>(to) + (h < keys ? c0 : 2 * unit)) = x[i];
+      *(reinterpret_cast<uint4*>(to) + (h < keys ? c1 : 2 * unit + 1)) = y[i];
     }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int h = h0 + i * step;
-      if (h >= heads) break;
-      const bool value = h >= queries + a.num_kv_heads;
-      T* to;
-      if (h < queries) {
-        to = static_cast<T*>(a.q_out) + t * a.q_out_stride_token + h * a.q_out_stride_head;
-      } else {
-        if (slot < 0) break;
-        to = value ? static_cast<T*>(a.v_cache) + page * a.v_cache_stride_page +
-                         at * a.v_cache_stride_token +
-                         (h - queries - a.num_kv_heads) * a.v_cache_stride_head
-                   : static_cast<T*>(a.k_cache) + page * a.k_cache_stride_page +
-                         at * a.k_cache_stride_token + (h - queries) * a.k_cache_stride_head;
-      }
-      if (turned && !value) turn<T, kInterleaved>(&x[i], &y[i], c, s);
-      *(reinterpret_cast<uint4*>(to) + (value ? 2 * unit : c0)) = x[i];
-      *(reinterpret_cast<uint4*>(to) + (value ? 2 * unit + 1 : c1)) = y[i];
-    }
+    h0 += kAtOnce * step;
+    if (h0 >= heads) break;
+    load(h0);
   }
 }
 
@@ -168,6 +166,8 @@ __device__ __forceinline__ float e2m1_value(uint32_t code) {
   return __uint_as_float(bits | (code & 8) << 28);
 }
 
+constexpr int kInsertAtOnce = 2;  // tokens in flight per 16 lanes
+
 // Sixteen lanes a token, eight values each; four lanes hold a block of 32 and
 // its largest magnitude. The scale is a power of two, so the products are exact
 // and the codes those of the definition. Bound by the reads and writes.
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads)
     insert_mxfp4_kernel(const __nv_bfloat16* __restrict__ k, int64_t k_stride,
                         const int64_t* __restrict__ slots, int64_t n, uint8_t* __restrict__ cache,
                         int64_t num_pages, __nv_bfloat16* __restrict__ values, uint32_t* err) {
-  constexpr int kLanes = 16, kAtOnce = 2, kTokens = kThreads / kLanes;
+  constexpr int kLanes = 16, kAtOnce = kInsertAtOnce, kTokens = kThreads / kLanes;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % kLanes;
@@ -246,7 +246,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
+// A stride of a dimension of n entries (of one entry it is never used); `written`: entries apart.
+bool stride_ok(int64_t s, int64_t n, bool written) {
+  return n <= 1 || (s >= (written ? 1 : 0) && s % 8 == 0);
+}
 
 }  // namespace
 }  // namespace saib
@@ -280,15 +283,22 @@ idx_status indexer_append_kv(const idx_append* a, void* stream) {
       !aligned(a->v_cache, 16))
     return IDX_ERR_INVALID_ARG;
   if (rotate && (!a->positions || !aligned(a->positions, 4))) return IDX_ERR_INVALID_ARG;
+  const int64_t n = a->num_tokens, kv = a->num_kv_heads;
   if (queries && (!a->q_out || !aligned(a->q, 16) || !aligned(a->q_out, 16) ||
-                  !stride_ok(a->q_stride_token) || !stride_ok(a->q_stride_head) ||
-                  !stride_ok(a->q_out_stride_token) || !stride_ok(a->q_out_stride_head)))
+                  !stride_ok(a->q_stride_token, n, false) ||
+                  !stride_ok(a->q_stride_head, a->num_heads, false) ||
+                  !stride_ok(a->q_out_stride_token, n, true) ||
+                  !stride_ok(a->q_out_stride_head, a->num_heads, true)))
     return IDX_ERR_INVALID_ARG;
-  for (const int64_t s :
-       {a->k_stride_token, a->k_stride_head, a->v_stride_token, a->v_stride_head,
-        a->k_cache_stride_page, a->k_cache_stride_token, a->k_cache_stride_head,
-        a->v_cache_stride_page, a->v_cache_stride_token, a->v_cache_stride_head})
-    if (!stride_ok(s)) return IDX_ERR_INVALID_ARG;
+  if (!stride_ok(a->k_stride_token, n, false) || !stride_ok(a->k_stride_head, kv, false) ||
+      !stride_ok(a->v_stride_token, n, false) || !stride_ok(a->v_stride_head, kv, false) ||
+      !stride_ok(a->k_cache_stride_page, a->num_pages, true) ||
+      !stride_ok(a->k_cache_stride_token, kPageTokens, true) ||
+      !stride_ok(a->k_cache_stride_head, kv, true) ||
+      !stride_ok(a->v_cache_stride_page, a->num_pages, true) ||
+      !stride_ok(a->v_cache_stride_token, kPageTokens, true) ||
+      !stride_ok(a->v_cache_stride_head, kv, true))
+    return IDX_ERR_INVALID_ARG;
   AppendParams p{*a, 1};
   if (!rotate) p.a.rotary_dim = p.a.interleaved = 0;
   const int heads = (queries ? a->num_heads : 0) + 2 * a->num_kv_heads;
@@ -314,9 +324,12 @@ idx_status indexer_insert_keys_mxfp4(const void* k, int64_t k_stride, const int6
   if (!k || !slot_mapping || !index_cache || !aligned(k, 16) || !aligned(slot_mapping, 8) ||
       !aligned(index_cache, 16) || !aligned(values, 16) || k_stride < kDim || k_stride % 8)
     return IDX_ERR_INVALID_ARG;
+  // few tokens: one a group of lanes; many: kInsertAtOnce, and no second round
   const int64_t blocks = (num_tokens + kThreads / 16 - 1) / (kThreads / 16);
-  const int64_t most = int64_t{16} * device_sm_count();
-  return cuda_status(launch_pdl(insert_mxfp4_kernel, static_cast<unsigned>(std::min(blocks, most)),
+  const int64_t grid = std::max(std::min(blocks, int64_t{4} * device_sm_count()),
+                                (blocks + kInsertAtOnce - 1) / kInsertAtOnce);
+  return cuda_status(launch_pdl(insert_mxfp4_kernel,
+                                static_cast<unsigned>(std::min<int64_t>(grid, INT32_MAX)),
                                 kThreads, 0, static_cast<cudaStream_t>(stream),
                                 static_cast<const __nv_bfloat16*>(k), k_stride, slot_mapping,
                                 num_tokens, index_cache, num_pages,

@@ -425,7 +425,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
   int64_t unit = 0, unit_end = 0;
   int32_t first_tile = 0, last_tile = 0, req_token = -1, req = -1;
   const int rank = kCluster ? cluster_rank() : 0;
-  const int64_t mine = kCluster ? cta / p.cluster : 0;  // this cluster's unit, or request and kv head
+  const int clusters = kTree ? p.cluster_entries : 1;  // of a request's kv head
+  // this cluster's unit, or request and kv head
+  const int64_t mine = kCluster ? cta / (p.cluster * clusters) : 0;
   ReqShape shape{};
   if constexpr (kCluster) {
     if (kSel) {
@@ -433,7 +435,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       unit_end = mine + 1;
     } else {
       req = static_cast<int32_t>(mine / p.num_kv_heads);
-      shape = request_shape(p, req, cta == req * p.num_kv_heads * p.cluster);
+      shape = request_shape(p, req, cta == req * p.num_kv_heads * p.cluster * clusters);
+      unit = kTree ? cta / p.cluster % clusters : 0;
       unit_end = request_entries(p, shape);
     }
   } else if constexpr (kSel) {
@@ -482,7 +485,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
       first_tile = 0;
     } else if constexpr (kCluster) {
       if (unit >= unit_end) break;
-      const int32_t entry = static_cast<int32_t>(unit++);
+      const int32_t entry = static_cast<int32_t>(unit);
+      unit += clusters;
       u.req = req;
       u.head = static_cast<int32_t>(mine % p.num_kv_heads);
       u.row0 = entry * p.rows;

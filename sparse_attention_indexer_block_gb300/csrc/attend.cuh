@@ -56,6 +56,7 @@ struct AttendParams {
   int32_t self_plan;               // the CTAs work `bound` out for themselves
   int32_t min_cost;                // least work of a CTA, in tiles
   int32_t cluster;                 // row-block kernel: blocks that share a unit; 0: a plan cuts
+  int32_t cluster_entries;         // trees: clusters of a request's kv head
   int32_t grid;                    // CTAs of the row-block launch
   int32_t rows;                    // query rows of a unit
   int32_t tile_log2;               // keys of a tile

@@ -91,6 +91,15 @@ int cluster_blocks(int64_t units, int64_t tiles, int64_t slack, int64_t most, co
   return units * c <= v.grid && one <= most && one <= tiles * units / v.grid + slack ? c : 0;
 }
 
+// The same for a tree of several blocks of rows, each a cluster's: against the chunk kernel's plan,
+// units and join.
+constexpr int64_t kClusterEntries = 4;
+int tree_cluster_blocks(int64_t units, int64_t tiles, const Variant& v) {
+  int c = kMostCluster;
+  while (c > 1 && (units * c > v.grid || c >= 2 * tiles)) c /= 2;
+  return units * c <= v.grid && (tiles + c - 1) / c <= 8 ? c : 0;
+}
+
 constexpr int64_t kLittleTiles = 12;  // a block's
 
 Variant tc_variant() { return Variant{0, kRowsTc, 7, device_sm_count(), 3, 4}; }
@@ -230,28 +239,39 @@ idx_status attend_new_tokens(const idx_attend* a, const Tree* tree, void* stream
   int64_t longest =
       a->max_query_len > 0 ? std::min(a->max_query_len, a->num_tokens) : a->num_tokens;
   if (tree) longest = std::min(longest, 32 * int64_t{tree->words});  // (no mask names more)
+  // (a window's tiles: those of the sinks, and the window and the new tokens, cut at both ends)
+  const auto tiles_of = [&](const Variant& v) {
+    set_variant(&p, v);
+    const int64_t tile = int64_t{1} << v.tile_log2;
+    return std::min((a->bt_width * int64_t{kPageTokens} + tile - 1) / tile,
+                    p.sinks_tiles + (p.window + longest + tile - 1) / tile + 1);
+  };
+  const bool half = a->dtype == IDX_FP16;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Calls of little work: clusters, without a plan or a join.
+  const Variant few = rows_variant(1, a->head_dim, false);
+  const int64_t entries = (longest * p.group + few.rows - 1) / few.rows;
+  if (entries <= (tree ? kClusterEntries : 1)) {
+    const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads * entries;
+    p.cluster = entries == 1 ? cluster_blocks(units, tiles_of(few), 10, 16, few)
+                             : tree_cluster_blocks(units, tiles_of(few), few);
+    if (p.cluster) {
+      p.grid = static_cast<int32_t>(units * p.cluster);
+      p.cluster_entries = static_cast<int32_t>(entries);
+      if ((st = place_workspace(&p, a, few)) != IDX_OK) return st;
+      return launch_attend_rows(p, a->head_dim, half, few.mt, s);
+    }
+  }
+  if (!a->workspace) return IDX_ERR_WORKSPACE;
   // The row-block kernel holds 16 rows at once and reads K and V again for the next 16; from
   // 17 rows on the tensor-memory kernel is faster (24 requests of 8000 keys, 8 kv heads of 128:
   // 15 rows 132 against 140 us, 20 rows 173 against 142).
-  const bool half = a->dtype == IDX_FP16;
   CUtensorMap kmap, vmap;
   const bool tc =
       longest * p.group > 16 && attend_tc_maps(p, a->head_dim, half, &kmap, &vmap);
-  const Variant v = tc ? tc_variant() : rows_variant(1, a->head_dim, false);
-  set_variant(&p, v);
-  // (a window's tiles: those of the sinks, and the window and the new tokens, cut at both ends)
-  const int64_t tile = int64_t{1} << v.tile_log2;
-  const int64_t tiles =
-      std::min((a->bt_width * int64_t{kPageTokens} + tile - 1) / tile,
-               p.sinks_tiles + (p.window + longest + tile - 1) / tile + 1);
-  if (!tc && longest * p.group <= v.rows) {
-    const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads;
-    p.cluster = cluster_blocks(units, tiles, 10, 16, v);
-    if (p.cluster) p.grid = static_cast<int32_t>(units * p.cluster);
-  }
+  const Variant v = tc ? tc_variant() : few;
+  const int64_t tiles = tiles_of(v);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.cluster) return launch_attend_rows(p, a->head_dim, half, v.mt, s);
   // The chunk kernel's blocks plan for themselves when there is little work: a launch less is 4 us
   // less of the host's time, which is what such calls take (100 tokens of a first prompt: 33 us a
   // call, then 29; on the device 256 tokens 20.9, then 15.7). The cuts of the planning kernel are

@@ -651,12 +651,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (r >= u.rows) pos = INT32_MIN;
       TreeRow tree;
       if constexpr (kTree) tree = TreeRow(p, u, token, r < u.rows);
+      // Trees seldom fill a unit. A warp without rows only takes part in the hand-overs; what the
+      // second product reads for its rows goes to rows that nobody reads.
+      const bool idle = kTree && r - lane >= u.rows;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         const int32_t tile = u.tiles.tile(u.t0 + j);
         if (!(ok = wait_warp(&bars.s_full[slot], s_phase))) break;
         s_phase ^= 1;
         tc_fence_after();
+        if (idle) {
+          if (C::kAhead && lane == 0) mbar_arrive(&bars.s_read[slot]);
+          if (C::kAhead && j > 0) {
+            if (!(ok = wait_warp(&bars.o_full[slot], o_phase))) break;
+            o_phase ^= 1;
+          }
+          if (lane == 0) {
+            if (!C::kAhead) mbar_arrive(&bars.p_half[slot]);
+            mbar_arrive(&bars.p_full[slot]);
+          }
+          __syncwarp();
+          continue;
+        }
         float s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
@@ -762,6 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         o_phase ^= 1;
         tc_fence_after();
       }
+      if (idle) continue;
       const bool odd =
           n > 0 && *reinterpret_cast<volatile uint32_t*>(&bars.odd[this_unit % kOddUnits]) ==
                        this_unit + 1;

@@ -100,15 +100,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_tree_kernel(const PlanParam
 // the accepted path
 // ---------------------------------------------------------------------------
 
-constexpr int kMoveThreads = 128;
-constexpr int kMoveLoads = 4;         // loads in flight per thread
+constexpr int kMoveThreads = 256;
+constexpr int kMoves = 64;            // of a round
+constexpr int kMoveLoads = 8;         // loads in flight per thread
 constexpr int kPoolsPerLaunch = 48;   // pools in one launch's parameters
+constexpr int kMostBlocks = 8;        // of a request
 
 struct MovePools {
   uint8_t* base[kPoolsPerLaunch];
   int64_t page_stride[kPoolsPerLaunch], token_stride[kPoolsPerLaunch], piece_stride[kPoolsPerLaunch];
-  int32_t pieces[kPoolsPerLaunch], piece_bytes[kPoolsPerLaunch];
-  uint8_t wide[kPoolsPerLaunch];  // 16 bytes at once (else 4)
+  int32_t columns[kPoolsPerLaunch];      // of a piece
+  int32_t column0[kPoolsPerLaunch + 1];  // exclusive prefix of the pools' columns
+  uint8_t wide[kPoolsPerLaunch];         // a column has 16 bytes (else 4)
+  int32_t num;
 };
 
 struct CommitParams {
@@ -121,126 +125,109 @@ struct CommitParams {
   int64_t accepted_stride;
   int32_t max_accepted;
   int32_t num_pages;
+  int32_t blocks;      // of a request: a cluster
+  int32_t last;        // the call's last launch: lengths and references follow
   int32_t* ref_counts;
   uint32_t* err;
 };
 
-struct TreeShape {
-  int32_t keys, nq;  // keys, the tree's nodes among them
-  bool ok;
-};
-
-__device__ __forceinline__ TreeShape tree_shape(const CommitParams& p, int32_t b) {
-  const int32_t keys = p.seq_lens[b];
-  const int64_t nq = static_cast<int64_t>(p.query_start_loc[b + 1]) - p.query_start_loc[b];
-  const bool ok = nq >= 0 && keys >= nq && keys <= static_cast<int64_t>(p.bt_width) * kPageTokens;
-  return TreeShape{keys, static_cast<int32_t>(ok ? nq : 0), ok};
-}
-
-// Whether entry i of a list continues it.
-__device__ __forceinline__ bool continues(const int32_t* list, int32_t i, int32_t nq) {
-  const int32_t a = list[i];
-  return a >= 0 && a < nq && (i == 0 || a > list[i - 1]);
-}
-
-// Moves the bytes of a thread's columns for n moves from place from[i] to to[i] (byte offsets in
-// the pool, -1: none). A list is ascending and entry i is at least i, so a later move never reads
-// what an earlier one has written, and no thread reads another's columns.
+// Moves a column's bytes for n moves (from[i] and to[i]: page and token; a page of -1: none). A list
+// is ascending and entry i is at least i, so a later move never reads what an earlier one has
+// written; no other thread touches the column.
 template <typename V>
-__device__ __forceinline__ void move_columns(uint8_t* base, int64_t piece_stride, int32_t pieces,
-                                             int32_t piece_bytes, const int64_t* from,
-                                             const int64_t* to, int32_t n) {
-  const int32_t per = piece_bytes / static_cast<int32_t>(sizeof(V));
-  for (int32_t col = threadIdx.x; col < per * pieces; col += kMoveThreads) {
-    const int32_t piece = col / per;
-    uint8_t* const at = base + piece * piece_stride + (col - piece * per) * sizeof(V);
-    for (int32_t i0 = 0; i0 < n; i0 += kMoveLoads) {
-      V x[kMoveLoads];
+__device__ __forceinline__ void move_column(uint8_t* at, int64_t page_stride, int64_t token_stride,
+                                            const int2* from, const int2* to, int32_t n) {
+  for (int32_t i0 = 0; i0 < n; i0 += kMoveLoads) {
+    V x[kMoveLoads];
 #pragma unroll
-      for (int e = 0; e < kMoveLoads; ++e)
-        if (i0 + e < n && from[i0 + e] >= 0) x[e] = *reinterpret_cast<const V*>(at + from[i0 + e]);
+    for (int e = 0; e < kMoveLoads; ++e)
+      if (i0 + e < n && from[i0 + e].x >= 0)
+        x[e] = *reinterpret_cast<const V*>(at + from[i0 + e].x * page_stride +
+                                           from[i0 + e].y * token_stride);
 #pragma unroll
-      for (int e = 0; e < kMoveLoads; ++e)
-        if (i0 + e < n && from[i0 + e] >= 0) *reinterpret_cast<V*>(at + to[i0 + e]) = x[e];
-    }
+    for (int e = 0; e < kMoveLoads; ++e)
+      if (i0 + e < n && from[i0 + e].x >= 0)
+        *reinterpret_cast<V*>(at + to[i0 + e].x * page_stride + to[i0 + e].y * token_stride) = x[e];
   }
 }
 
-// Block (request, pool): the accepted tokens to the tree's first places.
+// A cluster per request: its blocks share the columns (16 or 4 bytes of a token) of all pools; the
+// first one writes the length, once all have read it, and drops the references of the pages that the
+// row no longer holds. Bound by the latency of a chain of loads (lengths, list, table, data).
 __global__ void __launch_bounds__(kMoveThreads)
-    move_tokens_kernel(const __grid_constant__ CommitParams p, const __grid_constant__ MovePools pools) {
-  __shared__ int64_t from[kMoveThreads], to[kMoveThreads];
+    commit_tree_kernel(const __grid_constant__ CommitParams p, const __grid_constant__ MovePools pools) {
+  __shared__ int2 from[kMoves], to[kMoves];
   __shared__ int32_t end;
   pdl_wait();
   pdl_trigger();
-  const int32_t b = blockIdx.x, pool = blockIdx.y;
-  const TreeShape r = tree_shape(p, b);
-  if (!r.ok) return;
-  const int32_t ahead = r.keys - r.nq;
+  const int32_t b = blockIdx.x / p.blocks, rank = blockIdx.x % p.blocks;
+  const bool first = rank == 0 && threadIdx.x == 0;
+  const int32_t keys = p.seq_lens[b];
+  const int64_t new_tokens = static_cast<int64_t>(p.query_start_loc[b + 1]) - p.query_start_loc[b];
+  if (p.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const bool ok = new_tokens >= 0 && keys >= new_tokens &&
+                  keys <= static_cast<int64_t>(p.bt_width) * kPageTokens;
+  const int32_t nq = ok ? static_cast<int32_t>(new_tokens) : 0, ahead = keys - nq;
   const int32_t* const list = p.accepted + b * p.accepted_stride;
   const int32_t* const bt = p.block_table + b * p.bt_stride;
-  const int32_t most = min(p.max_accepted, r.nq);
-  for (int32_t i0 = 0; i0 < most; i0 += kMoveThreads) {
-    if (threadIdx.x == 0) end = kMoveThreads;
+  const int32_t most = min(p.max_accepted, nq);
+  int32_t kept = 0;
+  for (int32_t i0 = 0; i0 < most; i0 += kMoves) {
+    if (threadIdx.x == 0) end = kMoves;
     __syncthreads();
-    const int32_t i = i0 + threadIdx.x;
-    const bool in = i < most && continues(list, i, r.nq);
-    if (!in) atomicMin(&end, static_cast<int32_t>(threadIdx.x));
-    int64_t a = -1, c = -1;
-    if (in && list[i] != i) {
-      const int32_t s = ahead + list[i], d = ahead + i;
-      const int32_t sp = bt[s / kPageTokens], dp = bt[d / kPageTokens];
-      if (sp >= 0 && sp < p.num_pages && dp >= 0 && dp < p.num_pages) {
-        a = sp * pools.page_stride[pool] + (s % kPageTokens) * pools.token_stride[pool];
-        c = dp * pools.page_stride[pool] + (d % kPageTokens) * pools.token_stride[pool];
+    if (threadIdx.x < kMoves) {
+      const int32_t i = i0 + threadIdx.x;
+      const int32_t a = i < most ? list[i] : -1;
+      const int32_t before = i > 0 && i < most ? list[i - 1] : -1;
+      int2 src = make_int2(-1, 0), dst = make_int2(0, 0);
+      if (a > before && a < nq) {
+        if (a != i) {
+          src = make_int2(bt[(ahead + a) / kPageTokens], (ahead + a) % kPageTokens);
+          dst = make_int2(bt[(ahead + i) / kPageTokens], (ahead + i) % kPageTokens);
+          if (src.x < 0 || src.x >= p.num_pages || dst.x < 0 || dst.x >= p.num_pages) {
+            set_error(p.err, IDX_DEV_BAD_BLOCK);
+            src.x = -1;
+          }
+        }
       } else {
-        set_error(p.err, IDX_DEV_BAD_BLOCK);
+        atomicMin(&end, static_cast<int32_t>(threadIdx.x));
       }
+      from[threadIdx.x] = src;
+      to[threadIdx.x] = dst;
     }
-    from[threadIdx.x] = a;
-    to[threadIdx.x] = c;
     __syncthreads();
     const int32_t n = end;
-    if (pools.wide[pool])
-      move_columns<uint4>(pools.base[pool], pools.piece_stride[pool], pools.pieces[pool],
-                          pools.piece_bytes[pool], from, to, n);
-    else
-      move_columns<uint32_t>(pools.base[pool], pools.piece_stride[pool], pools.pieces[pool],
-                             pools.piece_bytes[pool], from, to, n);
-    if (n < kMoveThreads) return;
+    kept = i0 + n;
+    for (int32_t col = rank * kMoveThreads + threadIdx.x; col < pools.column0[pools.num];
+         col += p.blocks * kMoveThreads) {
+      int lo = 0, hi = pools.num - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pools.column0[mid] <= col) lo = mid; else hi = mid - 1;
+      }
+      const int32_t at = col - pools.column0[lo], piece = at / pools.columns[lo];
+      uint8_t* const base = pools.base[lo] + piece * pools.piece_stride[lo] +
+                            (at - piece * pools.columns[lo]) * (pools.wide[lo] ? 16 : 4);
+      if (pools.wide[lo])
+        move_column<uint4>(base, pools.page_stride[lo], pools.token_stride[lo], from, to, n);
+      else
+        move_column<uint32_t>(base, pools.page_stride[lo], pools.token_stride[lo], from, to, n);
+    }
+    if (n < kMoves) break;
     __syncthreads();
   }
-}
-
-// A warp per request: its new length, and the references of the pages that it no longer holds.
-__global__ void __launch_bounds__(kMoveThreads) commit_lens_kernel(const CommitParams p, int32_t num_reqs) {
-  pdl_wait();
-  pdl_trigger();
-  const int32_t b = (blockIdx.x * kMoveThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (b >= num_reqs) return;
-  const TreeShape r = tree_shape(p, b);
-  if (!r.ok) {
-    if (lane == 0) set_error(p.err, IDX_DEV_BAD_LEN);
+  if (p.blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank != 0 || !p.last) return;
+  if (!ok) {
+    if (first) set_error(p.err, IDX_DEV_BAD_LEN);
     return;
   }
-  const int32_t* const list = p.accepted + b * p.accepted_stride;
-  int32_t n = 0;
-  for (int32_t i0 = 0; i0 < p.max_accepted; i0 += 32) {
-    const int32_t i = i0 + lane;
-    const bool in = i < p.max_accepted && continues(list, i, r.nq);
-    const uint32_t all = __ballot_sync(0xffffffffu, in);
-    if (all != 0xffffffffu) {
-      n = i0 + __ffs(~all) - 1;
-      break;
-    }
-    n = i0 + 32;
-  }
-  if (lane == 0 && n < p.max_accepted && list[n] >= 0) set_error(p.err, IDX_DEV_BAD_ROW);
-  const int32_t left = r.keys - r.nq + n;
+  if (first && kept < p.max_accepted && list[kept] >= 0) set_error(p.err, IDX_DEV_BAD_ROW);
+  const int32_t left = ahead + kept;
   const auto pages = [](int32_t k) { return (k + kPageTokens - 1) / kPageTokens; };
   if (p.ref_counts) {
-    for (int32_t c = pages(left) + lane; c < pages(r.keys); c += 32) {
-      const int32_t page = p.block_table[b * p.bt_stride + c];
+    for (int32_t c = pages(left) + threadIdx.x; c < pages(keys); c += kMoveThreads) {
+      const int32_t page = bt[c];
       if (page < 0 || page >= p.num_pages) {
         set_error(p.err, IDX_DEV_BAD_BLOCK);
       } else if (atomicSub(p.ref_counts + page, 1) <= 0) {
@@ -249,8 +236,7 @@ __global__ void __launch_bounds__(kMoveThreads) commit_lens_kernel(const CommitP
       }
     }
   }
-  __syncwarp();
-  if (lane == 0) p.seq_lens[b] = left;
+  if (first) p.seq_lens[b] = left;
 }
 
 }  // namespace
@@ -297,7 +283,7 @@ idx_status indexer_commit_tree(const idx_token_pool* pools, int32_t num_pools, i
                                int32_t max_accepted, int32_t* ref_counts, uint32_t* dev_error,
                                void* stream) {
   if (num_pools < 0 || (num_pools && !pools) || num_pages < 1 || num_pages > INT32_MAX / 2 ||
-      num_reqs < 0 || bt_width < 1 || bt_width > INT32_MAX / kPageTokens || bt_stride < bt_width ||
+      num_reqs < 0 || num_reqs > INT32_MAX / kMostBlocks || bt_width < 1 || bt_width > INT32_MAX / kPageTokens || bt_stride < bt_width ||
       max_accepted < 0 || accepted_stride < max_accepted)
     return IDX_ERR_INVALID_ARG;
   for (int32_t i = 0; i < num_pools; ++i) {
@@ -313,38 +299,45 @@ idx_status indexer_commit_tree(const idx_token_pool* pools, int32_t num_pools, i
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) ||
       !aligned(accepted, 4) || !aligned(ref_counts, 4))
     return IDX_ERR_INVALID_ARG;
-  const CommitParams p{block_table, bt_stride,       bt_width,     seq_lens,
-                       query_start_loc, accepted,    accepted_stride, max_accepted,
-                       static_cast<int32_t>(num_pages), ref_counts, dev_error};
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  for (int32_t first = 0; max_accepted && first < num_pools; first += kPoolsPerLaunch) {
+  CommitParams p{block_table,  bt_stride,    bt_width, seq_lens, query_start_loc, accepted, accepted_stride,
+                 max_accepted, static_cast<int32_t>(num_pages), 1, 0, ref_counts, dev_error};
+  int32_t first = 0;
+  do {
     MovePools q{};
-    const int32_t n = std::min(num_pools - first, kPoolsPerLaunch);
-    for (int32_t i = 0; i < n; ++i) {
+    q.num = std::min(num_pools - first, kPoolsPerLaunch);
+    int64_t columns = 0;
+    for (int32_t i = 0; i < q.num; ++i) {
       const idx_token_pool& t = pools[first + i];
       q.base[i] = static_cast<uint8_t*>(t.base);
       q.page_stride[i] = t.page_stride;
       q.token_stride[i] = t.token_stride;
       q.piece_stride[i] = t.piece_stride;
-      q.pieces[i] = t.pieces;
-      q.piece_bytes[i] = t.piece_bytes;
-      q.wide[i] = aligned(t.base, 16) &&
-                  (t.page_stride | t.token_stride | (t.pieces > 1 ? t.piece_stride : 0) | t.piece_bytes) % 16 == 0;
+      q.wide[i] = aligned(t.base, 16) && (t.page_stride | t.token_stride | t.piece_bytes |
+                                          (t.pieces > 1 ? t.piece_stride : 0)) % 16 == 0;
+      q.columns[i] = t.piece_bytes / (q.wide[i] ? 16 : 4);
+      columns += static_cast<int64_t>(q.columns[i]) * t.pieces;
+      if (columns > INT32_MAX) return IDX_ERR_UNSUPPORTED;
+      q.column0[i + 1] = static_cast<int32_t>(columns);
     }
+    first += q.num;
+    p.last = first >= num_pools;
+    p.blocks = 1;
+    while (p.blocks < kMostBlocks && int64_t{p.blocks} * kMoveThreads < columns) p.blocks *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_reqs, n);
+    cfg.gridDim = dim3(static_cast<unsigned>(num_reqs) * p.blocks);
     cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(p.blocks), 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const idx_status st = cuda_status(cudaLaunchKernelEx(&cfg, move_tokens_kernel, p, q));
+    cfg.numAttrs = 2;
+    const idx_status st = cuda_status(cudaLaunchKernelEx(&cfg, commit_tree_kernel, p, q));
     if (st != IDX_OK) return st;
-  }
-  const unsigned grid = static_cast<unsigned>((num_reqs + kMoveThreads / 32 - 1) / (kMoveThreads / 32));
-  return cuda_status(launch_pdl(commit_lens_kernel, grid, kMoveThreads, 0, s, p, num_reqs));
+  } while (first < num_pools);
+  return IDX_OK;
 }
 
 }  // extern "C"
