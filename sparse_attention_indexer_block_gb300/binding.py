@@ -710,17 +710,20 @@ def attend_workspace(num_tokens: int, num_reqs: int, num_heads: int, num_kv_head
 def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices, scale, out,
             lse, workspace, dev_error, stream, max_query_len=0, window=0, sinks=0, masks=None,
             positions=None):
-    for what, t, dims in (("q", q, 3), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4)):
-        if not isinstance(t, torch.Tensor) or t.dim() != dims:
-            _refuse(name, f"{what} must have {dims} dimensions")
-    tokens, heads, dim = q.shape
-    pages, page, kv_heads, kv_dim = k_cache.shape
+    if not (isinstance(q, torch.Tensor) and isinstance(k_cache, torch.Tensor)
+            and isinstance(v_cache, torch.Tensor)):
+        _refuse(name, "q, k_cache and v_cache must be tensors")
+    q_shape, cache = q.shape, k_cache.shape
+    if len(q_shape) != 3 or len(cache) != 4:
+        _refuse(name, "q must have 3 dimensions, k_cache and v_cache 4")
+    tokens, heads, dim = q_shape
+    pages, page, kv_heads, kv_dim = cache
     dtype = q.dtype
     if dtype not in _ATTEND_TYPES:
         _refuse(name, f"q is {dtype}, not bfloat16 or float16", _UNSUPPORTED)
     if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         _refuse(name, "q, k_cache and v_cache differ in type")
-    if v_cache.shape != k_cache.shape or kv_dim != dim:
+    if v_cache.shape != cache or kv_dim != dim:
         _refuse(name, "k_cache and v_cache must be [pages, 64, kv heads, head_dim of q]")
     if page != PAGE_TOKENS:
         _refuse(name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
@@ -753,9 +756,8 @@ def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, i
     if lse is not None and not (isinstance(lse, torch.Tensor) and tuple(lse.shape) == (tokens, heads)
                                 and lse.dtype is _F32T and lse.is_contiguous()):
         _refuse(name, "lse must be a contiguous float32 tensor [tokens, heads]")
-    for what, n in (("max_query_len", max_query_len), ("window", window), ("sinks", sinks)):
-        if not 0 <= n <= 0x7fffffff:
-            _refuse(name, f"{what} {n}")
+    if not (0 <= max_query_len <= 0x7fffffff and 0 <= window <= 0x7fffffff and 0 <= sinks <= 0x7fffffff):
+        _refuse(name, f"max_query_len {max_query_len}, window {window}, sinks {sinks}")
     tree = ()
     if masks is not None:
         _need_i32(name, "masks", masks, tokens, None)
@@ -774,10 +776,10 @@ def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, i
                          out, lse, workspace, dev_error, masks, positions)
     with _On(index, stream) as s:
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
+            out = torch.empty(q_shape, dtype=dtype, device=q.device)
         if lse is None:
             lse = torch.empty((tokens, heads), dtype=_F32T, device=q.device)
-        call = getattr(load(), name)
+        call = getattr(_lib or load(), name)
 
         def run(at, size):
             return call(_ATTEND_BYTES.pack(
@@ -1147,32 +1149,34 @@ def indexer_plan_tree(parents, seq_lens, query_start_loc, max_query_len: int, wi
     if reqs < 0:
         _refuse(name, "query_start_loc is empty")
     _need_vector(name, "seq_lens", seq_lens, _I32T, reqs)
-    for what, n, least in (("max_query_len", max_query_len, 1), ("window", window, 0),
-                           ("sinks", sinks, 0), ("max_path", max_path, 0)):
-        if not least <= n <= 0x7fffffff:
-            _refuse(name, f"{what} {n}")
+    if not (1 <= max_query_len <= 0x7fffffff and 0 <= window <= 0x7fffffff and 0 <= sinks <= 0x7fffffff
+            and 0 <= max_path <= 0x7fffffff):
+        _refuse(name, f"max_query_len {max_query_len}, window {window}, sinks {sinks}, max_path {max_path}")
     words = (max_query_len + 31) // 32
-    outputs = (("masks", masks, (tokens, words)), ("paths", paths, (tokens, max_path)))
-    for what, t, shape in outputs:
-        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is _I32T
-                                  and tuple(t.shape) == shape and t.is_contiguous()):
-            _refuse(name, f"{what} must be a contiguous int32 tensor {list(shape)}")
+    if masks is not None:
+        _need_i32(name, "masks", masks, tokens, words)
+    if paths is not None:
+        _need_i32(name, "paths", paths, tokens, max_path)
+    if not ((masks is None or masks.is_contiguous()) and (paths is None or paths.is_contiguous())):
+        _refuse(name, "masks and paths must be contiguous")
     if positions is not None:
         _need_vector(name, "positions", positions, _I32T, tokens)
     _need_error(name, dev_error)
     index = _need_device(name, parents, seq_lens, query_start_loc, masks, positions, paths, dev_error)
     with _On(index, stream) as s:
-        new = functools.partial(torch.empty, dtype=_I32T, device=parents.device)
+        device = parents.device
         if masks is None:
-            masks = new((tokens, words))
+            masks = torch.empty((tokens, words), dtype=_I32T, device=device)
         if positions is None:
-            positions = new((tokens,))
+            positions = torch.empty(tokens, dtype=_I32T, device=device)
         if paths is None and max_path:
-            paths = new((tokens, max_path))
-        _ok(name, load().indexer_plan_tree(
+            paths = torch.empty((tokens, max_path), dtype=_I32T, device=device)
+        st = (_lib or load()).indexer_plan_tree(
             parents.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), reqs, tokens, window,
-            sinks, masks.data_ptr(), words, positions.data_ptr(), _at(paths) if max_path else None, max_path,
-            _at(dev_error), s))
+            sinks, masks.data_ptr(), words, positions.data_ptr(), paths.data_ptr() if max_path else None,
+            max_path, None if dev_error is None else dev_error.data_ptr(), s)
+        if st:
+            _check(name, st)
     return masks, positions, paths
 
 
@@ -1267,6 +1271,8 @@ def indexer_commit_tree(pools, block_table, seq_lens, query_start_loc, accepted,
     _need_error(name, dev_error)
     index = _need_device(name, block_table, seq_lens, query_start_loc, accepted, ref_counts, dev_error, *pools)
     with _On(index, stream) as s:
-        _ok(name, load().indexer_commit_tree(
+        st = (_lib or load()).indexer_commit_tree(
             entries, num_pools, pages, block_table.data_ptr(), bt_stride, width, reqs, seq_lens.data_ptr(),
-            query_start_loc.data_ptr(), accepted.data_ptr(), stride, most, _at(ref_counts), _at(dev_error), s))
+            query_start_loc.data_ptr(), accepted.data_ptr(), stride, most, _at(ref_counts), _at(dev_error), s)
+        if st:
+            _check(name, st)

@@ -158,24 +158,25 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
   return r;
 }
 
-// The value of an e2m1 code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-  const uint32_t m = code & 7;
-  // (two bits of exponent, one of mantissa; code 1 is the subnormal 0.5)
-  const uint32_t bits = m < 2 ? m * 0x3f000000u : ((m >> 1) + 126) << 23 | (m & 1) << 22;
-  return __uint_as_float(bits | (code & 8) << 28);
+// The larger magnitude of each half of two bf16 pairs; NaN where either is one.
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 constexpr int kInsertAtOnce = 2;  // tokens in flight per 16 lanes
 
-// Sixteen lanes a token, eight values each; four lanes hold a block of 32 and
-// its largest magnitude. The scale is a power of two, so the products are exact
-// and the codes those of the definition. Bound by the reads and writes.
+// Sixteen lanes a token, eight values each; four lanes hold a block of 32 and its
+// largest magnitude. The scale is a power of two, so the products are exact and the
+// codes those of the definition. Magnitudes, products by the scale and the values that
+// a code stands for are worked out on bf16 pairs (a value from two byte tables): with
+// each value by itself the instructions, not the reads and writes, bound it.
 __global__ void __launch_bounds__(kThreads)
     insert_mxfp4_kernel(const __nv_bfloat16* __restrict__ k, int64_t k_stride,
                         const int64_t* __restrict__ slots, int64_t n, uint8_t* __restrict__ cache,
                         int64_t num_pages, __nv_bfloat16* __restrict__ values, uint32_t* err) {
   constexpr int kLanes = 16, kAtOnce = kInsertAtOnce, kTokens = kThreads / kLanes;
+  constexpr uint32_t kAbs = 0x7fff7fffu;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % kLanes;
@@ -197,50 +198,64 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int64_t t = t0 + u * step;
-      const uint32_t(&w)[4] = reinterpret_cast<const uint32_t(&)[4]>(raw[u]);
+      uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      // bits of the block's largest magnitude
+      const auto largest = [&]() -> uint32_t {
+        uint32_t m = larger2(larger2(w[0] & kAbs, w[1] & kAbs), larger2(w[2] & kAbs, w[3] & kAbs));
+        m = larger2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = larger2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        return max(m & 0xffffu, m >> 16);
+      };
+      uint32_t top = largest();
+      if (__any_sync(0xffffffffu, top > 0x7f80u)) {  // a NaN counts as 0
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((w[i] & 0x7fffu) > 0x7f80u) w[i] &= 0xffff0000u;
+          if ((w[i] & 0x7fff0000u) > 0x7f800000u) w[i] &= 0xffffu;
+        }
+        top = largest();
+      }
+      // floor(log2 top) + 127 is the exponent field (0 for subnormals, whose E is 0 too)
+      const uint32_t e = max(static_cast<int32_t>(top >> 7) - 2, 0);
+      const uint32_t down = (254 - e) * 0x00800080u;  // 2^(127 - e), twice
       float x[8];
-      float top = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&down));
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(&y);
+        x[2 * i] = __uint_as_float(v << 16);
+        x[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (x[i] != x[i]) x[i] = 0.f;
-        top = fmaxf(top, fabsf(x[i]));
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // floor(log2 top) + 127 is the exponent field (0 for subnormals, whose E is 0 too)
-      const int32_t e = max(static_cast<int32_t>(__float_as_uint(top) >> 23) - 2, 0);
-      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= down;
       uint32_t code = e2m1x8(x);
-      if (top == 0.f) code = 0;  // (no signs of zeros)
-      const uint32_t e0 = __shfl_sync(0xffffffffu, e, 0, kLanes), e1 = __shfl_sync(0xffffffffu, e, 4, kLanes);
-      const uint32_t e2 = __shfl_sync(0xffffffffu, e, 8, kLanes), e3 = __shfl_sync(0xffffffffu, e, 12, kLanes);
+      if (top == 0) code = 0;  // (no signs of zeros)
       if (t >= n) continue;
       const bool bad = slot[u] >= num_pages * kPageTokens;
       if (bad && lane == 0) set_error(err, IDX_DEV_BAD_BLOCK);
       const bool written = slot[u] >= 0 && !bad;
       if (written) {
         // (entries are 68 bytes, so only 4-byte aligned)
-        uint32_t* const entry = reinterpret_cast<uint32_t*>(cache + slot[u] * kMxTokenBytes);
-        entry[lane] = code;
-        if (lane == 0) entry[kLanes] = e0 | e1 << 8 | e2 << 16 | e3 << 24;
+        uint8_t* const entry = cache + slot[u] * kMxTokenBytes;
+        reinterpret_cast<uint32_t*>(entry)[lane] = code;
+        if ((lane & 3) == 0) entry[kDim / 2 + (lane >> 2)] = static_cast<uint8_t>(e);
       }
       if (values) {
+        // codes 0 to 7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6: bytes of their bf16 forms
+        const uint32_t m = written ? code & 0x77777777u : 0, sign = written ? code & 0x88888888u : 0;
+        const uint32_t lo[2] = {__byte_perm(0xc0800000u, 0xc0804000u, m), __byte_perm(0xc0800000u, 0xc0804000u, m >> 16)};
+        const uint32_t hi[2] = {__byte_perm(0x3f3f3f00u, 0x40404040u, m), __byte_perm(0x3f3f3f00u, 0x40404040u, m >> 16)};
         // 2^(e - 127), which is subnormal for e = 0
-        const float up = __uint_as_float(e ? static_cast<uint32_t>(e) << 23 : 0x00400000u);
+        const uint32_t up = e ? e * 0x00800080u : 0x00400040u;
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = pack2<__nv_bfloat16>(e2m1_value(code >> (8 * i) & 15) * up,
-                                      e2m1_value(code >> (8 * i + 4) & 15) * up);
-        *(reinterpret_cast<uint4*>(values + t * kDim) + lane) =
-            written ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v = __byte_perm(lo[i >> 1], hi[i >> 1], i & 1 ? 0x7362 : 0x5140);
+          v |= (sign << (28 - 8 * i) & 0x80000000u) >> 16 | (sign << (24 - 8 * i) & 0x80000000u);
+          const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&up));
+          o[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        *(reinterpret_cast<uint4*>(values + t * kDim) + lane) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
