@@ -513,6 +513,8 @@ bool attend_tc_maps(const AttendParams& p, int head_dim, bool half, CUtensorMap*
                     CUtensorMap* vmap);
 idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, cudaStream_t s);
+// The join of the chunk kernel's pieces of trees (launch_attend_combine: of all others).
+idx_status launch_attend_join(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 idx_status launch_attend_lists(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 idx_status launch_attend_combine(const AttendParams& p, int head_dim, bool half, cudaStream_t s);
 

@@ -283,7 +283,8 @@ idx_status attend_new_tokens(const idx_attend* a, const Tree* tree, void* stream
   st = tc ? launch_attend_tc(p, a->head_dim, half, kmap, vmap, s)
           : launch_attend_rows(p, a->head_dim, half, v.mt, s);
   if (st != IDX_OK) return st;
-  return launch_attend_combine(p, a->head_dim, half, s);
+  return tc && tree ? launch_attend_join(p, a->head_dim, half, s)
+                    : launch_attend_combine(p, a->head_dim, half, s);
 }
 
 }  // namespace

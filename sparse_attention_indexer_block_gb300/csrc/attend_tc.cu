@@ -173,6 +173,14 @@ __device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
   swap(w[1], w[3], 2);
 }
 
+// Where 16 bytes of a piece's accumulator lie (float4s from the beginning of part_o), chunk c of row
+// r. A tree's pieces hold the rows' equal chunks side by side, since a thread of the chunk kernel and
+// of the join has a row: 32 rows a store (row after row: 8 us more for a piece of 192 rows of 128).
+template <int D, bool kTree>
+__device__ __forceinline__ int64_t part_chunk(const AttendParams& p, int64_t piece, int r, int c) {
+  return kTree ? (piece * (D / 4) + c) * p.rows + r : (piece * p.rows + r) * (D / 4) + c;
+}
+
 // Whether some row of the unit does not see some key of the tile.
 template <bool kTree>
 __device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles& t, int32_t tile) {
@@ -184,7 +192,7 @@ __device__ __forceinline__ bool edge_tile(const AttendParams& p, const UnitTiles
 // a row that sees them: added to the row where it was written.
 template <typename T, int D, bool kTree, typename Pos>
 __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u, const Pos pos,
-                                           T* out, float* part) {
+                                           T* out, int64_t piece, int r) {
   const int32_t* bt = p.block_table + static_cast<int64_t>(u.req) * p.bt_stride;
   for (int j = u.t0; j < u.t1; ++j) {
     const int32_t tile = u.tiles.tile(j);
@@ -204,7 +212,7 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Piece u,
         const float x = static_cast<float>(v[e]);
         if (isfinite(x)) continue;
         if (out) out[e] = static_cast<T>(static_cast<float>(out[e]) + x);
-        else part[e] += x;
+        else p.part_o[part_chunk<D, kTree>(p, piece, r, e / 4) * 4 + e % 4] += x;
       }
     }
   }
@@ -651,9 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (r >= u.rows) pos = INT32_MIN;
       TreeRow tree;
       if constexpr (kTree) tree = TreeRow(p, u, token, r < u.rows);
-      // Trees seldom fill a unit. A warp without rows only takes part in the hand-overs; what the
-      // second product reads for its rows goes to rows that nobody reads.
-      const bool idle = kTree && r - lane >= u.rows;
+      // Trees seldom fill a unit. A warp without rows only takes part in the hand-overs: its scores are
+      // zeros (of queries of zeros), which the second product reads as weights of 0. Less power, so a
+      // higher clock, is what it gives (32 requests of 16 to 32 nodes, 64/8 heads: 440 -> 422 us a
+      // call); at D = 64 the longer code costs 2 to 3 % of a tile.
+      const bool idle = kTree && !C::kAhead && r - lane >= u.rows;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         const int32_t tile = u.tiles.tile(u.t0 + j);
@@ -661,13 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_phase ^= 1;
         tc_fence_after();
         if (idle) {
-          if (C::kAhead && lane == 0) mbar_arrive(&bars.s_read[slot]);
-          if (C::kAhead && j > 0) {
-            if (!(ok = wait_warp(&bars.o_full[slot], o_phase))) break;
-            o_phase ^= 1;
-          }
           if (lane == 0) {
-            if (!C::kAhead) mbar_arrive(&bars.p_half[slot]);
+            mbar_arrive(&bars.p_half[slot]);
             mbar_arrive(&bars.p_full[slot]);
           }
           __syncwarp();
@@ -785,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = u.whole();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t at = token * p.num_heads + head;
-      const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (u.t0 == 0 ? 1 : 0)) * p.rows + r;
+      const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (u.t0 == 0 ? 1 : 0);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
@@ -815,15 +820,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (r - lane + from < u.rows) out[row * (D / 8) + c * 4 + (lane & 3)] = w[i];
           }
         } else if (r < u.rows) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            reinterpret_cast<float4*>(p.part_o)[part_chunk<D, kTree>(p, piece, r, c * 8 + i)] =
+                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
         __syncwarp();
       }
       if (r < u.rows) {
-        if (!whole) p.part_ml[part] = make_float2(m, l);
+        if (!whole) p.part_ml[piece * p.rows + r] = make_float2(m, l);
         else if (p.lse) p.lse[at] = row_lse<static_cast<int>(kTopWeightTc<T>)>(m, l);
       }
       if (odd) {
@@ -831,8 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (r < u.rows) {
           T* const out = whole ? static_cast<T*>(p.out) + at * D : nullptr;
-          if constexpr (kTree) add_nonfinite<T, D, true>(p, u, tree, out, p.part_o + part * D);
-          else add_nonfinite<T, D, false>(p, u, pos, out, p.part_o + part * D);
+          if constexpr (kTree) add_nonfinite<T, D, true>(p, u, tree, out, piece, r);
+          else add_nonfinite<T, D, false>(p, u, pos, out, piece, r);
         }
         __syncwarp();
       }
@@ -846,6 +851,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Join of a tree's units that several CTAs share. Block (c, y): 32 rows of the unit whose first piece
+// ends CTA c's range, a thread per row and 32 of its values; only cuts inside a unit leave work. The
+// pieces are joined in the order of the CTAs, so the result does not depend on timing. Bound by
+// latency: the cuts, then the request's lengths and two pieces side by side.
+template <typename T, int D>
+__global__ void __launch_bounds__(D) attend_join_kernel(const __grid_constant__ AttendParams p) {
+  const int c = blockIdx.x, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int r = blockIdx.y * 32 + lane;
+  constexpr int kTop = static_cast<int>(kTopWeightTc<T>);
+  pdl_wait();
+  pdl_trigger();
+  const int4 here = p.bound[c];
+  const auto same = [](const int4& a, const int4& b) {
+    return a.x == b.x && a.y == b.y && a.w == b.w;
+  };
+  const auto first = [](const int4& a) {
+    return make_int4(__shfl_sync(0xffffffffu, a.x, 0), __shfl_sync(0xffffffffu, a.y, 0),
+                     __shfl_sync(0xffffffffu, a.z, 0), __shfl_sync(0xffffffffu, a.w, 0));
+  };
+  struct Part {
+    float2 ml;
+    float4 v[8];
+  };
+  const auto load = [&](int64_t piece, Part* x) {
+    x->ml = p.part_ml[piece * p.rows + r];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x->v[i] = reinterpret_cast<const float4*>(p.part_o)[part_chunk<D, true>(p, piece, r, part * 8 + i)];
+  };
+  Part sum, x;
+  int4 next = make_int4(0, 0, 0, 0);
+  int64_t token = 0;
+  int head = 0, rows = 0;
+  for (int c0 = c + 1; c0 < p.grid || c0 == c + 1; c0 += 32) {
+    // the cuts at both ends of 32 CTAs' ranges
+    const int cc = c0 + lane;
+    const int4 none = make_int4(-1, -1, 0, -1);
+    const int4 a = cc <= p.grid ? p.bound[cc] : none, b = cc < p.grid ? p.bound[cc + 1] : none;
+    if (c0 == c + 1) {
+      next = first(a);
+      if (next.z == 0 || next.w >= p.num_reqs || (same(here, next) && here.z > 0)) return;
+      load(2 * static_cast<int64_t>(c) + 1, &sum);
+      const ReqShape shape = request_shape(p, next.w, false);
+      Piece u;
+      u.q0 = shape.q0;
+      u.head = next.y;
+      u.row0 = next.x * p.rows;
+      u.ahead = 0;
+      rows = min(p.rows, shape.nq * p.group - u.row0);
+      if (blockIdx.y * 32 >= rows) return;
+      int pos;
+      row_place(p, u, r, &token, &head, &pos);
+    }
+    const bool in = cc < p.grid && same(a, next) && a.z > 0;
+    const uint32_t all = __ballot_sync(0xffffffffu, in);
+    uint32_t full = __ballot_sync(0xffffffffu, in && !(same(b, next) && b.z == a.z));
+    while (full) {
+      load(2 * static_cast<int64_t>(c0 + __ffs(full) - 1), &x);
+      full &= full - 1;
+      const float top = fmaxf(sum.ml.x, x.ml.x), base = top == -INFINITY ? 0.f : top;
+      const float keep = exp2_approx(sum.ml.x - base), add = exp2_approx(x.ml.x - base);
+      sum.ml = make_float2(top, sum.ml.y * keep + x.ml.y * add);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sum.v[i] = make_float4(sum.v[i].x * keep + x.v[i].x * add, sum.v[i].y * keep + x.v[i].y * add,
+                               sum.v[i].z * keep + x.v[i].z * add, sum.v[i].w * keep + x.v[i].w * add);
+    }
+    if (all != 0xffffffffu) break;
+  }
+  const float inv = sum.ml.y == 0.f ? 0.f : 1.f / sum.ml.y;
+  const int64_t at = token * p.num_heads + head;
+  uint4 w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 f = sum.v[2 * i], g = sum.v[2 * i + 1];
+    w[i] = make_uint4(pack2<T>(f.x * inv, f.y * inv), pack2<T>(f.z * inv, f.w * inv),
+                      pack2<T>(g.x * inv, g.y * inv), pack2<T>(g.z * inv, g.w * inv));
+  }
+  transpose4(w, lane);
+  uint4* const out = reinterpret_cast<uint4*>(p.out);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int from = (lane & ~3) + i;
+    const int64_t row = __shfl_sync(0xffffffffu, at, from);
+    if (r - lane + from < rows) out[row * (D / 8) + part * 4 + (lane & 3)] = w[i];
+  }
+  if (part == 0 && r < rows && p.lse) p.lse[at] = row_lse<kTop>(sum.ml.x, sum.ml.y);
+}
+
+template <typename T, int D>
+idx_status launch_join_as(const AttendParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid, kRowsTc / 32);
+  cfg.blockDim = dim3(D);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p));
 }
 
 // Map of a cache: [64 tokens of a page][64 of the head_dim values] boxes of one
@@ -918,6 +1026,12 @@ bool attend_tc_maps(const AttendParams& p, int head_dim, bool half, CUtensorMap*
                     p.num_kv_heads, p.num_pages) &&
          encode_map(vmap, p.v, half, head_dim, p.v_stride_token, p.v_stride_head, p.v_stride_page,
                     p.num_kv_heads, p.num_pages);
+}
+
+idx_status launch_attend_join(const AttendParams& p, int head_dim, bool half, cudaStream_t s) {
+  if (half) return head_dim == 64 ? launch_join_as<__half, 64>(p, s) : launch_join_as<__half, 128>(p, s);
+  return head_dim == 64 ? launch_join_as<__nv_bfloat16, 64>(p, s)
+                        : launch_join_as<__nv_bfloat16, 128>(p, s);
 }
 
 idx_status launch_attend_tc(const AttendParams& p, int head_dim, bool half, const CUtensorMap& kmap,
