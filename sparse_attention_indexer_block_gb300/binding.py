@@ -5,13 +5,14 @@ pointers, sizes and the current CUDA stream to the function of the same name
 in ``libsaib.so`` and raises :class:`IndexerError` on a non-OK status. Torch is
 used for device memory (outputs and workspaces the caller did not pass) and
 streams. There is no fallback: without the built library every call raises.
+The calls that run once a layer and step (attention, appends, trees) are
+marshalled by a native module (``_marshal.so``, ``csrc/marshal.cpp``).
 """
 from __future__ import annotations
 
 import ctypes as C
 import functools
 import os
-import struct
 import threading
 
 import torch
@@ -45,11 +46,6 @@ class Attend(C.Structure):
                 + [("scale", C.c_float)])
 
 
-# the same as packed bytes (building the structure costs three times as much)
-_ATTEND_BYTES = struct.Struct("=12Q11q11if")
-assert _ATTEND_BYTES.size == C.sizeof(Attend)
-
-
 class PagePool(C.Structure):
     """idx_page_pool of indexer.h."""
     _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("page_bytes", C.c_int64)]
@@ -70,18 +66,10 @@ class Append(C.Structure):
                                             "dtype", "rotary_dim", "interleaved")])
 
 
-_APPEND_BYTES = struct.Struct("=10Q17q7i4x")
-assert _APPEND_BYTES.size == C.sizeof(Append)
-
-
 class TokenPool(C.Structure):
     """idx_token_pool of indexer.h."""
     _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
                 ("piece_stride", C.c_int64), ("pieces", C.c_int32), ("piece_bytes", C.c_int32)]
-
-
-_TOKEN_POOL_BYTES = struct.Struct("=Q3q2i")
-assert _TOKEN_POOL_BYTES.size == C.sizeof(TokenPool)
 
 
 # exported symbols and their ctypes signatures (kept in step with indexer.h)
@@ -152,7 +140,7 @@ SIGNATURES.update({
 })
 
 _lock = threading.Lock()
-_lib = None
+_lib = _marshal = None
 
 
 class IndexerError(RuntimeError):
@@ -176,8 +164,18 @@ def load(path: str = LIB_PATH):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
+        from . import _marshal as marshal
+        marshal.set_error_class(IndexerError)
+        global _marshal
+        _marshal = marshal
         _lib = lib
         return lib
+
+
+def _native():
+    if _marshal is None:
+        load()
+    return _marshal
 
 
 def _ptr(t):
@@ -603,9 +601,8 @@ def indexer_decode_topk_noalloc(q, weights, index_cache, block_table, row_seq_le
 # What they allocate (outputs, workspaces) belongs to the stream they run on.
 # ---------------------------------------------------------------------------
 
-_INVALID, _UNSUPPORTED, _WORKSPACE = 1, 2, 3
-_FEW_UNITS = 304  # (request or token, kv head) pairs: calls of more always use a workspace
-_I32T, _F32T = torch.int32, torch.float32
+_INVALID = 1
+_I32T = torch.int32
 
 
 def _refuse(name, what, status=_INVALID):
@@ -687,9 +684,6 @@ class _On:
             self.guard.__exit__(*exc)
 
 
-_ATTEND_TYPES = {torch.bfloat16: 0, torch.float16: 1}
-
-
 @functools.lru_cache(maxsize=256)
 def _attend_workspace_bytes(device, *sizes):
     n = C.c_size_t(0)
@@ -707,105 +701,6 @@ def attend_workspace(num_tokens: int, num_reqs: int, num_heads: int, num_kv_head
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _attend(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices, scale, out,
-            lse, workspace, dev_error, stream, max_query_len=0, window=0, sinks=0, masks=None,
-            positions=None):
-    if not (isinstance(q, torch.Tensor) and isinstance(k_cache, torch.Tensor)
-            and isinstance(v_cache, torch.Tensor)):
-        _refuse(name, "q, k_cache and v_cache must be tensors")
-    q_shape, cache = q.shape, k_cache.shape
-    if len(q_shape) != 3 or len(cache) != 4:
-        _refuse(name, "q must have 3 dimensions, k_cache and v_cache 4")
-    tokens, heads, dim = q_shape
-    pages, page, kv_heads, kv_dim = cache
-    dtype = q.dtype
-    if dtype not in _ATTEND_TYPES:
-        _refuse(name, f"q is {dtype}, not bfloat16 or float16", _UNSUPPORTED)
-    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
-        _refuse(name, "q, k_cache and v_cache differ in type")
-    if v_cache.shape != cache or kv_dim != dim:
-        _refuse(name, "k_cache and v_cache must be [pages, 64, kv heads, head_dim of q]")
-    if page != PAGE_TOKENS:
-        _refuse(name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
-    if dim != 64 and dim != 128:
-        _refuse(name, f"head_dim {dim}, not 64 or 128", _UNSUPPORTED)
-    if kv_heads < 1 or heads < 1 or heads % kv_heads:
-        _refuse(name, f"{heads} heads over {kv_heads} kv heads")
-    qt, qh, qd = q.stride()
-    kp, kt, kh, kd = k_cache.stride()
-    vp, vt, vh, vd = v_cache.stride()
-    if qd != 1 or kd != 1 or vd != 1:
-        _refuse(name, "q, k_cache and v_cache must be contiguous in their last dimension")
-    _need_i32(name, "query_start_loc", query_start_loc, None)
-    reqs = query_start_loc.shape[0] - 1
-    if reqs < 0:
-        _refuse(name, "query_start_loc is empty")
-    bt_width, bt_stride = _need_table(name, block_table, reqs)
-    topk = idx_stride = 0
-    if seq_lens is not None:
-        _need_i32(name, "seq_lens", seq_lens, reqs)
-    if indices is not None:
-        _need_i32(name, "indices", indices, tokens, None)
-        topk = indices.shape[1]
-        if topk < 1:
-            _refuse(name, "indices has no columns")
-        idx_stride = indices.stride(0) if tokens > 1 else topk
-    if out is not None and not (isinstance(out, torch.Tensor) and out.shape == q.shape
-                                and out.dtype is dtype and out.is_contiguous()):
-        _refuse(name, f"out must be a contiguous {dtype} tensor of q's shape")
-    if lse is not None and not (isinstance(lse, torch.Tensor) and tuple(lse.shape) == (tokens, heads)
-                                and lse.dtype is _F32T and lse.is_contiguous()):
-        _refuse(name, "lse must be a contiguous float32 tensor [tokens, heads]")
-    if not (0 <= max_query_len <= 0x7fffffff and 0 <= window <= 0x7fffffff and 0 <= sinks <= 0x7fffffff):
-        _refuse(name, f"max_query_len {max_query_len}, window {window}, sinks {sinks}")
-    tree = ()
-    if masks is not None:
-        _need_i32(name, "masks", masks, tokens, None)
-        words = masks.shape[1]
-        if words < 1:
-            _refuse(name, "masks has no columns")
-        if positions is not None:
-            _need_vector(name, "positions", positions, _I32T, tokens)
-        elif window:
-            _refuse(name, "a window needs positions")
-        tree = (masks.data_ptr(), masks.stride(0) if tokens > 1 else words, words, _at(positions))
-        if tokens > 1 and tree[1] < words:
-            _refuse(name, "masks' rows overlap")
-    _need_error(name, dev_error)
-    index = _need_device(name, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, indices,
-                         out, lse, workspace, dev_error, masks, positions)
-    with _On(index, stream) as s:
-        if out is None:
-            out = torch.empty(q_shape, dtype=dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty((tokens, heads), dtype=_F32T, device=q.device)
-        call = getattr(_lib or load(), name)
-
-        def run(at, size):
-            return call(_ATTEND_BYTES.pack(
-                q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                0 if seq_lens is None else seq_lens.data_ptr(), query_start_loc.data_ptr(),
-                0 if indices is None else indices.data_ptr(), out.data_ptr(), lse.data_ptr(), at, size,
-                0 if dev_error is None else dev_error.data_ptr(),
-                qt, qh, kp, kt, kh, vp, vt, vh, pages, bt_stride, idx_stride, bt_width, reqs, tokens,
-                heads, kv_heads, dim, _ATTEND_TYPES[dtype], max_query_len, window, sinks, topk,
-                dim ** -0.5 if scale is None else scale), *tree, s)
-
-        st = _WORKSPACE
-        if workspace is None:
-            # (small steps need no workspace: the call says so)
-            if (reqs if indices is None else tokens) * kv_heads <= _FEW_UNITS:
-                st = run(0, 0)
-            if st == _WORKSPACE:
-                workspace = torch.empty(_attend_workspace_bytes(index, tokens, reqs, heads, kv_heads, dim),
-                                        dtype=torch.uint8, device=q.device)
-        if workspace is not None:
-            st = run(workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        if st:
-            _check(name, st)
-    return out, lse
-
-
 def indexer_attend_paged(q, k_cache, v_cache, block_table, seq_lens, query_start_loc,
                          max_query_len: int = 0, scale=None, window: int = 0, sinks: int = 0,
                          out=None, lse=None, workspace=None, dev_error=None, stream=None):
@@ -819,8 +714,8 @@ def indexer_attend_paged(q, k_cache, v_cache, block_table, seq_lens, query_start
     hint that chooses the kernel, for small and windowed steps the faster one;
     0 and anything above the tokens count as all of them. scale defaults to
     dim ** -0.5. Returns (out like q, lse float32 [tokens, heads])."""
-    return _attend("indexer_attend_paged", q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
-                   None, scale, out, lse, workspace, dev_error, stream, max_query_len, window, sinks)
+    return _native().attend(0, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, None, scale, out, lse,
+                            workspace, dev_error, stream, max_query_len, window, sinks, None, None)
 
 
 def indexer_attend_selected(q, k_cache, v_cache, block_table, indices, query_start_loc, scale=None,
@@ -829,10 +724,8 @@ def indexer_attend_selected(q, k_cache, v_cache, block_table, indices, query_sta
     [tokens, topk], positions of the token's request, entries < 0 empty (the
     output of indexer_decode_topk / indexer_prefill_topk). Other arguments and
     the result as indexer_attend_paged."""
-    if indices is None:
-        _refuse("indexer_attend_selected", "indices is missing")
-    return _attend("indexer_attend_selected", q, k_cache, v_cache, block_table, query_start_loc, None,
-                   indices, scale, out, lse, workspace, dev_error, stream)
+    return _native().attend(1, q, k_cache, v_cache, block_table, query_start_loc, None, indices, scale, out, lse,
+                            workspace, dev_error, stream, 0, 0, 0, None, None)
 
 
 def indexer_attend_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks,
@@ -845,11 +738,8 @@ def indexer_attend_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_
     (int32 [tokens, words], bit j: the request's new token j) name. masks and
     positions are what indexer_plan_tree makes. Other arguments and the result as
     indexer_attend_paged; max_query_len (nodes of the largest tree) is a hint."""
-    if masks is None:
-        _refuse("indexer_attend_tree", "masks is missing")
-    return _attend("indexer_attend_tree", q, k_cache, v_cache, block_table, query_start_loc, seq_lens,
-                   None, scale, out, lse, workspace, dev_error, stream, max_query_len, window, sinks,
-                   masks, positions)
+    return _native().attend(2, q, k_cache, v_cache, block_table, query_start_loc, seq_lens, None, scale, out, lse,
+                            workspace, dev_error, stream, max_query_len, window, sinks, masks, positions)
 
 
 def _pools(name, pools, num_pages):
@@ -999,17 +889,6 @@ def indexer_compact_pages(pools, block_table, seq_lens, ref_counts, remap=None, 
 # ---------------------------------------------------------------------------
 
 
-def _need_vector(name, what, t, dtype, n):
-    """A contiguous tensor [n] of that type (n None: any size)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
-        _refuse(name, f"{what} must be a tensor of {dtype}")
-    shape = t.shape
-    if len(shape) != 1 or (n is not None and shape[0] != n):
-        _refuse(name, f"{what} has shape {tuple(shape)}")
-    if not t.is_contiguous():
-        _refuse(name, f"{what} must be contiguous")
-
-
 def indexer_append_kv(k, v, k_cache, v_cache, slot_mapping, q=None, positions=None, rotary=None,
                       interleaved: bool = False, q_out=None, dev_error=None, stream=None):
     """Writes new tokens' keys and values k, v [tokens, kv heads, dim] (bf16 or
@@ -1021,116 +900,15 @@ def indexer_append_kv(k, v, k_cache, v_cache, slot_mapping, q=None, positions=No
     [tokens]) on the way: value i with i + rotary_dim / 2, or neighbours when
     interleaved. Any strides that keep dim contiguous and are multiples of 8. Returns
     the rotated queries (q_out; q itself may be given), None without q."""
-    name = "indexer_append_kv"
-    for t in (k, v, k_cache, v_cache):
-        if not isinstance(t, torch.Tensor):
-            _refuse(name, "k, v, k_cache and v_cache must be tensors")
-    shape, cache, dtype = k.shape, k_cache.shape, k.dtype
-    if len(shape) != 3 or len(cache) != 4:
-        _refuse(name, "k and v must have 3 dimensions, k_cache and v_cache 4")
-    if dtype not in _ATTEND_TYPES:
-        _refuse(name, f"k is {dtype}, not bfloat16 or float16", _UNSUPPORTED)
-    if not dtype is v.dtype is k_cache.dtype is v_cache.dtype:
-        _refuse(name, "k, v, k_cache and v_cache differ in type")
-    tokens, kv_heads, dim = shape
-    pages, page, cache_heads, cache_dim = cache
-    if dim != 64 and dim != 128:
-        _refuse(name, f"head_dim {dim}, not 64 or 128", _UNSUPPORTED)
-    if v.shape != shape or cache_heads != kv_heads or cache_dim != dim or v_cache.shape != cache:
-        _refuse(name, "k and v must be [tokens, kv heads, dim], the caches [pages, 64, kv heads, dim]")
-    if page != PAGE_TOKENS:
-        _refuse(name, f"pages of {page} tokens, not {PAGE_TOKENS}", _UNSUPPORTED)
-    k0, k1, kd = k.stride()
-    v0, v1, vd = v.stride()
-    kp, kt, kh, kcd = k_cache.stride()
-    vp, vt, vh, vcd = v_cache.stride()
-    if not kd == vd == kcd == vcd == 1:
-        _refuse(name, "k, v, k_cache and v_cache must be contiguous in their last dimension")
-    _need_vector(name, "slot_mapping", slot_mapping, torch.int64, tokens)
-    heads = rotary_dim = num_positions = rotary_stride = q0 = q1 = o0 = o1 = pos_at = rot_at = q_at = 0
-    if rotary is None:
-        if q is not None or positions is not None or q_out is not None:
-            _refuse(name, "q, positions and q_out belong to a rotation")
-    else:
-        if not isinstance(rotary, torch.Tensor) or rotary.dtype is not _F32T or rotary.dim() != 2:
-            _refuse(name, "rotary must be a float32 tensor [positions, rotary_dim]")
-        num_positions, rotary_dim = rotary.shape
-        if rotary_dim < 16 or rotary_dim % 16 or rotary_dim > dim:
-            _refuse(name, f"rotary_dim {rotary_dim}, not a multiple of 16 up to {dim}", _UNSUPPORTED)
-        rotary_stride, last = rotary.stride()
-        if last != 1:
-            _refuse(name, "rotary must be contiguous in its last dimension")
-        if num_positions == 1:
-            rotary_stride = rotary_dim
-        _need_vector(name, "positions", positions, _I32T, tokens)
-        pos_at, rot_at = positions.data_ptr(), rotary.data_ptr()
-        if q is not None:
-            if not isinstance(q, torch.Tensor) or q.dtype is not dtype:
-                _refuse(name, f"q must be a tensor of {dtype}")
-            q_shape = q.shape
-            if len(q_shape) != 3 or q_shape[0] != tokens or q_shape[2] != dim or q_shape[1] < 1:
-                _refuse(name, f"q must be [{tokens}, heads, {dim}]")
-            heads, q_at = q_shape[1], q.data_ptr()
-            q0, q1, last = q.stride()
-            if last != 1:
-                _refuse(name, "q must be contiguous in its last dimension")
-            if q_out is not None:
-                if not isinstance(q_out, torch.Tensor) or q_out.shape != q_shape or q_out.dtype is not dtype:
-                    _refuse(name, "q_out must be a tensor like q")
-                o0, o1, last = q_out.stride()
-                if last != 1:
-                    _refuse(name, "q_out must be contiguous in its last dimension")
-        elif q_out is not None:
-            _refuse(name, "q_out without q")
-    _need_error(name, dev_error)
-    index = _need_device(name, k, v, k_cache, v_cache, slot_mapping, positions, rotary, q, q_out, dev_error)
-    with _On(index, stream) as s:
-        if heads and q_out is None:
-            q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
-            o0, o1 = heads * dim, dim
-        st = (_lib or load()).indexer_append_kv(_APPEND_BYTES.pack(
-            q_at, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), pos_at, rot_at,
-            q_out.data_ptr() if heads else 0, k_cache.data_ptr(), v_cache.data_ptr(),
-            0 if dev_error is None else dev_error.data_ptr(), q0, q1, k0, k1, v0, v1, o0, o1, kp, kt, kh,
-            vp, vt, vh, pages, num_positions, rotary_stride, tokens, heads, kv_heads, dim,
-            _ATTEND_TYPES[dtype], rotary_dim, 1 if interleaved else 0), s)
-        if st:
-            _check(name, st)
-    return q_out
+    return _native().append_kv(k, v, k_cache, v_cache, slot_mapping, q, positions, rotary, interleaved, q_out,
+                               dev_error, stream)
 
 
 def indexer_insert_keys_mxfp4(k, slot_mapping, index_cache, values=None, dev_error=None, stream=None):
     """Quantises k (bf16 [T, 128], rows of any stride that is a multiple of 8) to MXFP4 entries and
     writes them into the paged index cache (uint8 [pages, 4352]) at slot_mapping (int64 [T]); in
     place. values (bf16 [T, 128], contiguous) gets what the entries stand for."""
-    name = "indexer_insert_keys_mxfp4"
-    if not isinstance(k, torch.Tensor) or k.dim() != 2 or k.dtype is not torch.bfloat16:
-        _refuse(name, "k must be a bfloat16 tensor [tokens, 128]")
-    shape = k.shape
-    tokens, dim = shape
-    if dim != HEAD_DIM:
-        _refuse(name, f"keys of {dim} values, not {HEAD_DIM}", _UNSUPPORTED)
-    stride, last = k.stride()
-    if last != 1:
-        _refuse(name, "k must be contiguous in its last dimension")
-    _need_vector(name, "slot_mapping", slot_mapping, torch.int64, tokens)
-    if not isinstance(index_cache, torch.Tensor) or index_cache.dtype is not torch.uint8 \
-            or index_cache.dim() != 2 or index_cache.shape[1] != MXFP4_PAGE_BYTES \
-            or not index_cache.is_contiguous():
-        _refuse(name, f"index_cache must be a contiguous uint8 tensor [pages, {MXFP4_PAGE_BYTES}]")
-    if values is not None and not (isinstance(values, torch.Tensor) and values.shape == shape
-                                   and values.dtype is torch.bfloat16 and values.is_contiguous()):
-        _refuse(name, "values must be a contiguous bfloat16 tensor of k's shape")
-    _need_error(name, dev_error)
-    index = _need_device(name, k, slot_mapping, index_cache, values, dev_error)
-    with _On(index, stream) as s:
-        st = (_lib or load()).indexer_insert_keys_mxfp4(
-            k.data_ptr(), stride if tokens > 1 else dim, slot_mapping.data_ptr(), tokens, dim,
-            index_cache.data_ptr(), index_cache.shape[0], None if values is None else values.data_ptr(),
-            None if dev_error is None else dev_error.data_ptr(), s)
-        if st:
-            _check(name, st)
-    return index_cache
+    return _native().insert_keys_mxfp4(k, slot_mapping, index_cache, values, dev_error, stream)
 
 
 def indexer_plan_tree(parents, seq_lens, query_start_loc, max_query_len: int, window: int = 0,
@@ -1141,106 +919,8 @@ def indexer_plan_tree(parents, seq_lens, query_start_loc, max_query_len: int, wi
     every node and its ancestors, with a window those that it leaves; positions int32 [tokens]; paths
     int32 [tokens, max_path]: the places of a node and its ancestors in the cache, -1 after, None
     with max_path 0). max_query_len: nodes of the largest tree (words = ceil(max_query_len / 32))."""
-    name = "indexer_plan_tree"
-    _need_vector(name, "parents", parents, _I32T, None)
-    tokens = parents.shape[0]
-    _need_vector(name, "query_start_loc", query_start_loc, _I32T, None)
-    reqs = query_start_loc.shape[0] - 1
-    if reqs < 0:
-        _refuse(name, "query_start_loc is empty")
-    _need_vector(name, "seq_lens", seq_lens, _I32T, reqs)
-    if not (1 <= max_query_len <= 0x7fffffff and 0 <= window <= 0x7fffffff and 0 <= sinks <= 0x7fffffff
-            and 0 <= max_path <= 0x7fffffff):
-        _refuse(name, f"max_query_len {max_query_len}, window {window}, sinks {sinks}, max_path {max_path}")
-    words = (max_query_len + 31) // 32
-    if masks is not None:
-        _need_i32(name, "masks", masks, tokens, words)
-    if paths is not None:
-        _need_i32(name, "paths", paths, tokens, max_path)
-    if not ((masks is None or masks.is_contiguous()) and (paths is None or paths.is_contiguous())):
-        _refuse(name, "masks and paths must be contiguous")
-    if positions is not None:
-        _need_vector(name, "positions", positions, _I32T, tokens)
-    _need_error(name, dev_error)
-    index = _need_device(name, parents, seq_lens, query_start_loc, masks, positions, paths, dev_error)
-    with _On(index, stream) as s:
-        device = parents.device
-        if masks is None:
-            masks = torch.empty((tokens, words), dtype=_I32T, device=device)
-        if positions is None:
-            positions = torch.empty(tokens, dtype=_I32T, device=device)
-        if paths is None and max_path:
-            paths = torch.empty((tokens, max_path), dtype=_I32T, device=device)
-        st = (_lib or load()).indexer_plan_tree(
-            parents.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), reqs, tokens, window,
-            sinks, masks.data_ptr(), words, positions.data_ptr(), paths.data_ptr() if max_path else None,
-            max_path, None if dev_error is None else dev_error.data_ptr(), s)
-        if st:
-            _check(name, st)
-    return masks, positions, paths
-
-
-@functools.lru_cache(maxsize=256)
-def _token_layout(shape, strides, dtype):
-    """idx_token_pool entries of a tensor of that layout, as (offset, page stride, token stride, piece
-    stride, pieces, piece bytes); a text where it has none."""
-    if len(shape) < 2 or shape[0] < 1:
-        return "a pool must be a tensor [pages, 64, ...] or a uint8 index cache"
-    pages = shape[0]
-    if dtype is torch.uint8 and len(shape) == 2 and shape[1] in (PAGE_BYTES, MXFP4_PAGE_BYTES):
-        stride = strides[0] if pages > 1 else shape[1]
-        if strides[1] != 1 or stride < shape[1] or stride % 4:
-            return "an index cache's pages must be contiguous and of whole words"
-        if shape[1] == PAGE_BYTES:
-            return ((0, stride, HEAD_DIM, 0, 1, HEAD_DIM), (PAGE_TOKENS * HEAD_DIM, stride, 4, 0, 1, 4))
-        return ((0, stride, MXFP4_TOKEN_BYTES, 0, 1, MXFP4_TOKEN_BYTES),)
-    if shape[1] != PAGE_TOKENS:
-        return f"pages of {shape[1]} tokens, not {PAGE_TOKENS}"
-    if any(n > 1 and st == 0 for n, st in zip(shape, strides)):
-        return "a pool's tokens overlap"
-    size = dtype.itemsize
-    # a token's values from the last dimension up to where they stop being contiguous
-    run, dim = size, len(shape) - 1
-    while dim >= 2 and (shape[dim] == 1 or strides[dim] * size == run):
-        run *= shape[dim]
-        dim -= 1
-    pieces, piece_stride = 1, run
-    if dim >= 2:
-        pieces, piece_stride = shape[dim], strides[dim] * size
-        if any(n > 1 for n in shape[2:dim]):
-            return "a pool's token must be one run of values or evenly spaced ones"
-    token_stride = strides[1] * size
-    page_stride = strides[0] * size if pages > 1 else token_stride
-    if run == 0 or run % 4 or token_stride % 4 or page_stride % 4 or piece_stride % 4:
-        return "a pool's tokens must be of whole 4-byte words"
-    return ((0, page_stride, token_stride, piece_stride, pieces, run),)
-
-
-def _token_pools(name, pools):
-    """(idx_token_pool entries as bytes, their number, pages): tensors [pages, 64, ...], or uint8
-    index caches [pages, 8448] and [pages, 4352]."""
-    out, n, pages = [], 0, None
-    for t in pools:
-        if not isinstance(t, torch.Tensor):
-            _refuse(name, "a pool must be a tensor [pages, 64, ...] or a uint8 index cache")
-        shape = t.shape
-        layout = _token_layout(shape, t.stride(), t.dtype)
-        if isinstance(layout, str):
-            _refuse(name, layout, _UNSUPPORTED if layout.startswith("pages of") else _INVALID)
-        if pages is None:
-            pages = shape[0]
-        elif shape[0] != pages:
-            _refuse(name, "the pools differ in pages")
-        at = t.data_ptr()
-        for offset, *entry in layout:
-            out += (at + offset, *entry)
-            n += 1
-    return _token_pool_struct(n).pack(*out), n, pages
-
-
-@functools.lru_cache(maxsize=64)
-def _token_pool_struct(n):
-    return struct.Struct("=" + "Q3q2i" * n)
+    return _native().plan_tree(parents, seq_lens, query_start_loc, max_query_len, window, sinks, max_path, masks,
+                               positions, paths, dev_error, stream)
 
 
 def indexer_commit_tree(pools, block_table, seq_lens, query_start_loc, accepted, ref_counts=None,
@@ -1250,29 +930,4 @@ def indexer_commit_tree(pools, block_table, seq_lens, query_start_loc, accepted,
     values, uint8 index caches [pages, 8448] or [pages, 4352]) their tokens move to the tree's first
     places, seq_lens becomes L - Q + accepted nodes, and the pages that a row no longer holds lose a
     reference in ref_counts (int32 [pages]), all in place. Rows of block_table are the requests."""
-    name = "indexer_commit_tree"
-    entries, num_pools, pages = _token_pools(name, pools)
-    _need_vector(name, "query_start_loc", query_start_loc, _I32T, None)
-    reqs = query_start_loc.shape[0] - 1
-    if reqs < 0:
-        _refuse(name, "query_start_loc is empty")
-    width, bt_stride = _need_table(name, block_table, reqs)
-    _need_vector(name, "seq_lens", seq_lens, _I32T, reqs)
-    _need_i32(name, "accepted", accepted, reqs, None)
-    most = accepted.shape[1]
-    stride = accepted.stride(0) if reqs > 1 else most
-    if stride < most:
-        _refuse(name, "accepted's rows overlap")
-    if ref_counts is not None:
-        _need_vector(name, "ref_counts", ref_counts, _I32T, pages)
-        pages = ref_counts.shape[0]
-    if pages is None:
-        _refuse(name, "neither pools nor ref_counts")
-    _need_error(name, dev_error)
-    index = _need_device(name, block_table, seq_lens, query_start_loc, accepted, ref_counts, dev_error, *pools)
-    with _On(index, stream) as s:
-        st = (_lib or load()).indexer_commit_tree(
-            entries, num_pools, pages, block_table.data_ptr(), bt_stride, width, reqs, seq_lens.data_ptr(),
-            query_start_loc.data_ptr(), accepted.data_ptr(), stride, most, _at(ref_counts), _at(dev_error), s)
-        if st:
-            _check(name, st)
+    _native().commit_tree(pools, block_table, seq_lens, query_start_loc, accepted, ref_counts, dev_error, stream)

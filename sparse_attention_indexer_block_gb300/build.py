@@ -3,7 +3,8 @@
 Each translation unit under ``csrc/`` is compiled by nvcc in parallel and the
 objects are linked into one shared library next to this file. The CUDA runtime
 is linked statically; the driver's tensor-map encoder is looked up at run time,
-so the library needs no libcuda at link time.
+so the library needs no libcuda at link time. Beside it, g++ builds the module
+that hands torch tensors to the library's small calls (_marshal.so).
 """
 from __future__ import annotations
 
@@ -11,10 +12,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsaib.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["api.cu", "prep.cu", "score_select.cu", "row_select.cu", "dcp.cu",
            "block_select.cu", "no_alloc.cu", "attend_api.cu", "attend.cu", "attend_tc.cu", "pages.cu",
            "append.cu", "tree.cu"]
@@ -31,12 +34,33 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(HERE, "..", "include", "indexer.h"))
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
+def _marshal_command(nvcc: str, obj: str) -> list[str]:
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    return ["g++", "-std=c++17", "-O2", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+            "-isystem", sysconfig.get_path("include"), "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj]
+
+
+def _link_marshal(obj: str) -> None:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libsaib.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}",
+                    "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,--allow-shlib-undefined"],
+                   check=True)
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -54,6 +78,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    marshal = os.path.join(objdir, "marshal.o")
+    procs.append(("marshal.cpp", subprocess.Popen(_marshal_command(nvcc, marshal), stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -62,10 +89,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    _link_marshal(marshal)
     return LIB
 
 

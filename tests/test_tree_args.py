@@ -221,8 +221,7 @@ def test_binding_commit_refusals():
 def test_token_pools_of_strided_caches():
     """Head-major caches, halves of one array, whole tokens: what the binding makes of them."""
     def entries(*pools):
-        raw, n, _ = binding._token_pools("test", pools)
-        return [binding._TOKEN_POOL_BYTES.unpack_from(raw, i * binding._TOKEN_POOL_BYTES.size)[1:] for i in range(n)]
+        return binding._native().token_pools(pools)
 
     plain = torch.zeros((3, 64, 2, 64), dtype=BF)
     heads = torch.zeros((3, 2, 64, 64), dtype=BF).transpose(1, 2)
