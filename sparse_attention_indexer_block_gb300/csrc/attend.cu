@@ -60,6 +60,7 @@ __device__ __forceinline__ int entry_request(const int32_t* req_entry, int n, in
 // units, in the order request, kv head, entry, are cut into `grid` ranges of
 // equal cost. A cut inside a unit's overhead leaves the unit whole to the CTA
 // that begins there.
+template <bool kTree>
 __device__ int4 cut_at(const AttendParams& p, int c) {
   const int64_t all = p.entry_cost[p.req_entry[p.num_reqs]] * p.num_kv_heads;
   const int64_t pos = cut_position(all, cutters(p, all, 0), c);
@@ -79,7 +80,8 @@ __device__ int4 cut_at(const AttendParams& p, int c) {
     const int32_t mid = (a + b + 1) >> 1;
     if (p.entry_cost[mid] <= at) a = mid; else b = mid - 1;
   }
-  const int32_t off = static_cast<int32_t>(at - p.entry_cost[a]) - p.unit_overhead;
+  int32_t off = static_cast<int32_t>(at - p.entry_cost[a]) - p.unit_overhead;
+  if (kTree && off > 0) off /= tile_cost<kTree>(p, request_shape(p, lo, false), a - e0);
   return make_int4(a - e0, head, off > 0 ? off : 0, lo);
 }
 
@@ -114,14 +116,16 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
     int64_t cost = 0;
     if (e < entries) {
       const int b = entry_request(p.req_entry, p.num_reqs, e);
-      cost = unit_tiles<kTree>(p, request_shape(p, b, false), e - p.req_entry[b]).count + p.unit_overhead;
+      const ReqShape r = request_shape(p, b, false);
+      const int32_t u = e - p.req_entry[b];
+      cost = unit_tiles<kTree>(p, r, u).count * tile_cost<kTree>(p, r, u) + p.unit_overhead;
     }
     const int64_t incl = carry + block_scan<kPlanThreads>(cost, sums, &total);
     if (e < entries) p.entry_cost[e + 1] = incl;
     carry += total;
   }
   __syncthreads();
-  for (int c = threadIdx.x; c <= p.grid; c += kPlanThreads) p.bound[c] = cut_at(p, c);
+  for (int c = threadIdx.x; c <= p.grid; c += kPlanThreads) p.bound[c] = cut_at<kTree>(p, c);
 }
 
 // ---------------------------------------------------------------------------

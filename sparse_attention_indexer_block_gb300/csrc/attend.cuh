@@ -54,13 +54,14 @@ struct AttendParams {
   float2* part_ml;                 // [2 * grid, rows] their maximum and sum
   int32_t max_entries;
   int32_t self_plan;               // the CTAs work `bound` out for themselves
-  int32_t min_cost;                // least work of a CTA, in tiles
+  int32_t min_cost;                // least work of a CTA (a tile: 1, of a tree tile_cost)
   int32_t cluster;                 // row-block kernel: blocks that share a unit; 0: a plan cuts
   int32_t cluster_entries;         // trees: clusters of a request's kv head
+  int32_t tile_cost, narrow_cost;  // trees: what a tile costs, and one of a unit of at most 128 rows
   int32_t grid;                    // CTAs of the row-block launch
   int32_t rows;                    // query rows of a unit
   int32_t tile_log2;               // keys of a tile
-  int32_t unit_overhead;           // tiles of streaming that a unit's start and end cost
+  int32_t unit_overhead;           // what a unit's start and end cost, in the same measure
   uint32_t* dev_error;
   uint64_t wait_ns;
   // a tree's: the new tokens that each of them sees (bit j of a row's words: new token j of its
@@ -131,6 +132,13 @@ __device__ __forceinline__ UnitTiles unit_tiles(const AttendParams& p, const Req
   t.skip = start - t.first;
   t.count = end - t.skip;
   return t;
+}
+
+// What a tile of entry u costs a CTA.
+template <bool kTree>
+__device__ __forceinline__ int32_t tile_cost(const AttendParams& p, const ReqShape& r, int32_t u) {
+  if (!kTree) return 1;
+  return r.nq * p.group - u * p.rows > 128 ? p.tile_cost : p.narrow_cost;
 }
 
 // A piece: tiles [t0, t1) of a unit.
@@ -423,15 +431,16 @@ __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost
   int32_t head = static_cast<int32_t>(quotient(rest, one));
   int64_t off = rest - head * one;
   const ReqShape r = request_shape(p, lo, false);
-  int32_t u = 0, tiles;
+  int32_t u = 0, tiles, of_tile;
   for (;; ++u) {
+    of_tile = tile_cost<kTree>(p, r, u);
     tiles = unit_tiles<kTree>(p, r, u).count;
-    if (off < tiles + p.unit_overhead) break;
-    off -= tiles + p.unit_overhead;
+    if (off < tiles * of_tile + p.unit_overhead) break;
+    off -= tiles * of_tile + p.unit_overhead;
   }
   // a cut near a unit's end moves there (by at most a sixteenth of a CTA's work)
-  int32_t t = static_cast<int32_t>(max(off - p.unit_overhead, int64_t{0}));
-  const int64_t near = quotient(all, n) / 16;
+  int32_t t = static_cast<int32_t>(max(off - p.unit_overhead, int64_t{0})) / of_tile;
+  const int64_t near = quotient(all, n) / 16 / of_tile;
   if (t <= near) t = 0;
   if (t > 0 && tiles - t <= near) {
     t = 0;
@@ -466,7 +475,8 @@ __device__ void self_plan(const AttendParams& p, int cta, int64_t* cost, int64_t
     if (b < p.num_reqs) {
       const ReqShape r = request_shape(p, b, cta == 0);
       const int32_t e = request_entries(p, r);
-      for (int32_t i = 0; i < e; ++i) n += unit_tiles<kTree>(p, r, i).count + p.unit_overhead;
+      for (int32_t i = 0; i < e; ++i)
+        n += unit_tiles<kTree>(p, r, i).count * tile_cost<kTree>(p, r, i) + p.unit_overhead;
       n += static_cast<int64_t>(e) << kEntryShift;
     }
     const int64_t incl = carry + block_scan<kThreads>(n, sums, &total);

@@ -188,6 +188,7 @@ void set_variant(AttendParams* p, const Variant& v) {
   p->grid = v.grid;
   p->unit_overhead = v.overhead;
   p->min_cost = v.min_cost;
+  p->tile_cost = p->narrow_cost = 1;
 }
 
 idx_status place_workspace(AttendParams* p, const idx_attend* a, const Variant& v) {
@@ -272,6 +273,15 @@ idx_status attend_new_tokens(const idx_attend* a, const Tree* tree, void* stream
   const Variant v = tc ? tc_variant() : few;
   const int64_t tiles = tiles_of(v);
   if ((st = place_workspace(&p, a, v)) != IDX_OK) return st;
+  if (tc && tree && a->head_dim == 64) {
+    // At D = 64 a tile takes 1.21 us with two slots and 0.87 with one (at D = 128 the keys' bytes
+    // bound both). 24 requests of 40 to 130 nodes with a window of 2048, 24/8 heads: the last CTA
+    // ends at 55 us instead of the mean's 47 when all tiles count alike.
+    p.tile_cost = 4;
+    p.narrow_cost = 3;
+    p.unit_overhead *= 4;
+    p.min_cost *= 4;
+  }
   // The chunk kernel's blocks plan for themselves when there is little work: a launch less is 4 us
   // less of the host's time, which is what such calls take (100 tokens of a first prompt: 33 us a
   // call, then 29; on the device 256 tokens 20.9, then 15.7). The cuts of the planning kernel are
