@@ -91,13 +91,19 @@ int cluster_blocks(int64_t units, int64_t tiles, int64_t slack, int64_t most, co
   return units * c <= v.grid && one <= most && one <= tiles * units / v.grid + slack ? c : 0;
 }
 
-// The same for a tree of several blocks of rows, each a cluster's: against the chunk kernel's plan,
-// units and join.
-constexpr int64_t kClusterEntries = 4;
-int tree_cluster_blocks(int64_t units, int64_t tiles, const Variant& v) {
+// The same for trees of up to kClusterEntries blocks of rows, a cluster for each, against the chunk
+// kernel: a cluster's block takes 5.5 us and 1 a tile, the chunk kernel with its plan and join some
+// 17 and, with all of the keys cut evenly over the device, 1.5 (D = 64: 0.9) a tile of 128 keys.
+// us, chunk kernel / clusters, D = 128, 8 kv heads: one tree of 32 rows over 1000 keys 16.2 / 8.2,
+// 8000: 32.0 / 21.1; of 96 rows over 2000 20.1 / 14.6, 8000: 32.6 / 36.8; four of 64 over 1000:
+// 18.7 / 15.2, 2000: 20.8 / 22.6; D = 64, one of 32 over 8000: 26.0 / 12.7, four of 64: 27.7 / 34.8.
+// (Of 72 such sizes the rule picks the slower side twice, by 7 %.)
+constexpr int64_t kClusterEntries = 8;
+int tree_cluster_blocks(int64_t units, int64_t pairs, int64_t tiles, int head_dim, const Variant& v) {
   int c = kMostCluster;
   while (c > 1 && (units * c > v.grid || c >= 2 * tiles)) c /= 2;
-  return units * c <= v.grid && (tiles + c - 1) / c <= 8 ? c : 0;
+  const int64_t wide = head_dim == 64 ? 9 * tiles : 15 * tiles / 2;  // tenths of us of a chunk unit
+  return units * c <= v.grid && (tiles + c - 1) / c <= 12 + pairs * wide / (10 * device_sm_count()) ? c : 0;
 }
 
 constexpr int64_t kLittleTiles = 12;  // a block's
@@ -255,7 +261,7 @@ idx_status attend_new_tokens(const idx_attend* a, const Tree* tree, void* stream
   if (entries <= (tree ? kClusterEntries : 1)) {
     const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads * entries;
     p.cluster = entries == 1 ? cluster_blocks(units, tiles_of(few), 10, 16, few)
-                             : tree_cluster_blocks(units, tiles_of(few), few);
+                             : tree_cluster_blocks(units, units / entries, tiles_of(few), a->head_dim, few);
     if (p.cluster) {
       p.grid = static_cast<int32_t>(units * p.cluster);
       p.cluster_entries = static_cast<int32_t>(entries);
