@@ -618,3 +618,96 @@ def test_speculative_steps():
             assert torch.equal(k[pg, at % PAGE], k1.view(-1, kv, dim)[:len(h)])
             assert torch.equal(v[pg, at % PAGE], v1.view(-1, kv, dim)[:len(h)])
             assert torch.equal(index.view(pages, PAGE, 68)[pg, at % PAGE], i1.view(-1, 68)[:len(h)])
+
+
+def test_step_in_a_graph_follows_its_inputs():
+    """Plan, append, attention and commit captured once and replayed on other trees, tokens and tables."""
+    heads, kv, dim, reqs, q = 8, 2, 64, 3, 24
+    g = torch.Generator(device=DEV).manual_seed(3)
+    pages = 30
+    k = torch.randn((pages, PAGE, kv, dim), generator=g, device=DEV).to(FP)
+    v = torch.randn((pages, PAGE, kv, dim), generator=g, device=DEV).to(FP)
+    angle = torch.rand((2000, dim // 2), generator=g, device=DEV) * 6.2832
+    rotary = torch.cat([angle.cos(), angle.sin()], 1)
+    table, lens = torch.zeros((reqs, 10), dtype=torch.int32, device=DEV), _i32([0] * reqs)
+    start, refs, err = _i32([0, q, 2 * q, 3 * q]), _i32([0] * pages), _i32([0])
+    parents, accepted = _i32([0] * (reqs * q)), torch.full((reqs, 6), -1, dtype=torch.int32, device=DEV)
+    slots = torch.zeros(reqs * q, dtype=torch.int64, device=DEV)
+    x = [torch.zeros((reqs * q, n, dim), dtype=FP, device=DEV) for n in (heads, kv, kv)]
+
+    def step():
+        masks, positions, _ = saib.indexer_plan_tree(parents, lens, start, q, window=70, sinks=2, dev_error=err)
+        turned = saib.indexer_append_kv(x[1], x[2], k, v, slots, q=x[0], positions=positions, rotary=rotary,
+                                        interleaved=True, dev_error=err)
+        out, lse = saib.indexer_attend_tree(turned, k, v, table, lens, start, masks, q, positions=positions, window=70,
+                                            sinks=2, dev_error=err)
+        saib.indexer_commit_tree([k, v], table, lens, start, accepted, ref_counts=refs, dev_error=err)
+        return out, lse
+
+    def fill(seed):
+        rng = random.Random(seed)
+        kl = [q + rng.randrange(0, 400) for _ in range(reqs)]
+        trees = _trees([q] * reqs, seed)
+        parents.copy_(_i32([p for t in trees for p in t]))
+        table.copy_(torch.randperm(pages, generator=g, device=DEV).view(reqs, 10))
+        refs.fill_(1)
+        lens.copy_(_i32(kl))
+        slots.copy_(torch.cat([table[b].long()[(n - q + torch.arange(q, device=DEV)) // PAGE] * PAGE
+                               + (n - q + torch.arange(q, device=DEV)) % PAGE for b, n in enumerate(kl)]))
+        for t in x:
+            t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+        accepted.fill_(-1)
+        for b, t in enumerate(trees):
+            chain = _chains(t)[-1][::-1][:6]
+            accepted[b, :len(chain)] = _i32(chain)
+
+    state = [k, v, lens, refs]
+    fill(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    fill(2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (3, 4):
+        fill(seed)
+        before = [t.clone() for t in state]
+        graph.replay()
+        torch.cuda.synchronize()
+        after = [t.clone() for t in state]
+        for t, old in zip(state, before):
+            t.copy_(old)
+        want = step()
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        for t, a in zip(state, after):
+            assert torch.equal(t, a)
+
+
+def test_streams_as_objects_and_handles():
+    c = Caches([8], [100], seed=20)
+    want = c.expected([[0, 7]])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    masks = [saib.indexer_plan_tree(_i32([-1] * 8), _i32([100]), c.start, 8, stream=s)[0]
+             for s in (None, side, side.cuda_stream, torch.cuda.current_stream().cuda_stream)]
+    c.commit([[0, 7]], stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(m, masks[0]) for m in masks)
+    c.check(want)
+
+
+def test_tree_of_a_batch_whose_hint_is_smaller_than_its_trees():
+    """Units past those the hint asks for, in clusters and without, of a long and a short table."""
+    for width in (0, 3000):
+        b = TreeBatch([2, 50, 9], [400, 300, 20], 8, 2, 128, BF, seed=21)
+        if width:
+            wide = torch.full((3, width), -1, dtype=torch.int32, device=DEV)
+            wide[:, :b.width] = b.table
+            b.table = wide
+        for hint in (1, 2, 9, 50):
+            b.check(b.attend_tree(max_query_len=hint), b.reference_tree())
