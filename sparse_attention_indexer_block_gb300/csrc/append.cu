@@ -9,6 +9,7 @@ namespace saib {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kManyHeads = 5;  // heads of a lane
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -18,7 +19,8 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 struct AppendParams {
   idx_append a;
-  int32_t splits;  // blocks that share a token
+  int32_t splits;       // blocks that share a token, or
+  int32_t tokens_log2;  // tokens that share a block
 };
 
 template <typename T>
@@ -52,27 +54,35 @@ __device__ __forceinline__ void turn(uint4* x, uint4* y, const float (&c)[8], co
   }
 }
 
-// A token's heads (its queries', keys', values') go to the lanes' groups of D / 16, a lane holding
+// A token's heads (its queries', keys', values') go round its groups of D / 16 lanes, a lane holding
 // two 16-byte chunks of a head: the two halves of eight pairs, whose angles it reads once for all
-// its heads. The first heads are asked for before the token's slot and position are there, three a
-// lane at a time. Bound by HBM: 16011 tokens of 64/8 heads of 64 50.0 us, 6.6 TB/s (two heads at a
-// time 51.3, four 52.9; after slot and position 55.6).
+// its heads. A token has a part of a block, a block, or several of them. The first heads are asked
+// for before the token's slot and position are there (16011 tokens of 64/8 heads of 64: 51.3 us
+// instead of 55.6), three a lane at a time (50.0; four 52.9). Bound by HBM: 49.4 us, 6.7 TB/s.
 template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kUnits = D / 16, kGroups = kThreads / kUnits, kAtOnce = 3;
+  constexpr int kUnits = D / 16, kGroups = kThreads / kUnits, kGroupsLog2 = D == 64 ? 5 : 4, kAtOnce = 3;
+  static_assert(kGroups == 1 << kGroupsLog2, "groups");
   const idx_append& a = p.a;
   pdl_wait();
   pdl_trigger();
-  const int token = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-  const int unit = threadIdx.x % kUnits;
-  const int step = kGroups * p.splits;
+  const int unit = threadIdx.x % kUnits, groups = kGroups >> p.tokens_log2;  // of a token
+  const int group = threadIdx.x / kUnits & (groups - 1);
+  int block = blockIdx.x, split = 0;
+  if (p.splits > 1) {
+    block = blockIdx.x / p.splits;
+    split = blockIdx.x - block * p.splits;
+  }
+  const int64_t t =
+      (static_cast<int64_t>(block) << p.tokens_log2) + (threadIdx.x / kUnits >> (kGroupsLog2 - p.tokens_log2));
+  if (t >= a.num_tokens) return;
+  const int step = groups * p.splits;
   const int queries = a.rotary && a.q ? a.num_heads : 0;
   const int keys = queries + a.num_kv_heads, heads = keys + a.num_kv_heads;
   const bool turned = a.rotary && unit < a.rotary_dim / 16;
   // the lane's chunks of a rotated head (of others: 2 unit and the next)
   const int c0 = turned && !kInterleaved ? unit : 2 * unit;
   const int c1 = turned && !kInterleaved ? unit + a.rotary_dim / 16 : 2 * unit + 1;
-  const int64_t t = token;
   const T* const q = static_cast<const T*>(a.q) + t * a.q_stride_token;
   const T* const k = static_cast<const T*>(a.k) + t * a.k_stride_token;
   const T* const v = static_cast<const T*>(a.v) + t * a.v_stride_token;
@@ -89,11 +99,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       y[i] = *(reinterpret_cast<const uint4*>(from) + (h < keys ? c1 : 2 * unit + 1));
     }
   };
-  int h0 = split * kGroups + threadIdx.x / kUnits;
+  int h0 = split * groups + group;
   load(h0);
   int64_t slot = a.slot_mapping[t];
   int64_t pos = a.rotary ? a.positions[t] : 0;
-  const bool first = threadIdx.x == 0 && split == 0;
+  const bool first = unit == 0 && group == 0 && split == 0;
   float c[8], s[8];
   if (a.rotary) {
     const int64_t in = min(max(pos, int64_t{0}), a.num_positions - 1);
@@ -138,7 +148,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 template <typename T, int D>
 idx_status launch_append(const AppendParams& p, cudaStream_t s) {
   const auto kernel = p.a.interleaved ? append_kernel<T, D, true> : append_kernel<T, D, false>;
-  return cuda_status(launch_pdl(kernel, static_cast<unsigned>(p.a.num_tokens) * p.splits, kThreads, 0, s, p));
+  const unsigned blocks = (static_cast<unsigned>(p.a.num_tokens) + (1u << p.tokens_log2) - 1) >> p.tokens_log2;
+  return cuda_status(launch_pdl(kernel, blocks * p.splits, kThreads, 0, s, p));
 }
 
 // ---------------------------------------------------------------------------
@@ -316,15 +327,19 @@ idx_status indexer_append_kv(const idx_append* a, void* stream) {
       !stride_ok(a->v_cache_stride_token, kPageTokens, true) ||
       !stride_ok(a->v_cache_stride_head, kv, true))
     return IDX_ERR_INVALID_ARG;
-  AppendParams p{*a, 1};
+  AppendParams p{*a, 1, 0};
   if (!rotate) p.a.rotary_dim = p.a.interleaved = 0;
   const int heads = (queries ? a->num_heads : 0) + 2 * a->num_kv_heads;
   const int groups = kThreads / (a->head_dim / 16);
   const int rounds = (heads + groups - 1) / groups;  // of a block alone
   // few tokens: a block a round, up to 16 blocks an SM (544 tokens of 64/8 heads of 128: 4.8 us, up
-  // to 8 5.7)
+  // to 8 5.7); many: so many tokens a block that a lane has some heads (us, one token a block / here:
+  // 16011 of 64/8 heads of 64 52.8 / 49.4, 14903 of 16/8 of 128 47.1 / 38.8, 11394 of 9/3 of 64
+  // 22.0 / 10.7; three heads a lane: 49.3, 39.5, 10.1, eight: 50.8, 38.8, 9.8)
   const int64_t room = int64_t{16} * device_sm_count() / a->num_tokens;
   p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(rounds, room)));
+  if (room < 1)
+    while (groups >> p.tokens_log2 > 1 && heads < kManyHeads * (groups >> p.tokens_log2)) ++p.tokens_log2;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->dtype == IDX_FP16)
     return a->head_dim == 64 ? launch_append<__half, 64>(p, s) : launch_append<__half, 128>(p, s);
