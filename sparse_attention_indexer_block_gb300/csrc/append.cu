@@ -332,11 +332,11 @@ idx_status indexer_append_kv(const idx_append* a, void* stream) {
   const int heads = (queries ? a->num_heads : 0) + 2 * a->num_kv_heads;
   const int groups = kThreads / (a->head_dim / 16);
   const int rounds = (heads + groups - 1) / groups;  // of a block alone
-  // few tokens: a block a round, up to 16 blocks an SM (544 tokens of 64/8 heads of 128: 4.8 us, up
-  // to 8 5.7); many: so many tokens a block that a lane has some heads (us, one token a block / here:
+  // few tokens: a block a round, up to 12 blocks an SM (576 tokens of 64/8 heads of 128: 5.1 us
+  // interleaved, 4.7 not; 8 blocks: 5.5, 4.5; 16: 5.3, 5.4); many: so many tokens a block that a lane has some heads (us, one token a block / here:
   // 16011 of 64/8 heads of 64 52.8 / 49.4, 14903 of 16/8 of 128 47.1 / 38.8, 11394 of 9/3 of 64
   // 22.0 / 10.7; three heads a lane: 49.3, 39.5, 10.1, eight: 50.8, 38.8, 9.8)
-  const int64_t room = int64_t{16} * device_sm_count() / a->num_tokens;
+  const int64_t room = int64_t{12} * device_sm_count() / a->num_tokens;
   p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(rounds, room)));
   if (room < 1)
     while (groups >> p.tokens_log2 > 1 && heads < kManyHeads * (groups >> p.tokens_log2)) ++p.tokens_log2;
