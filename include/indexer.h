@@ -817,7 +817,8 @@ idx_status indexer_plan_tree(const int32_t* parents, const int32_t* seq_lens,
  * multiples of 4). K or V [pages, 64, kv heads, dim]: one piece of all heads where
  * they are contiguous, else one per head. An fp8 index cache is two such pools
  * (128 bytes a token from the page's beginning, 4 bytes from byte 8192), an MXFP4
- * one is one (68 bytes). */
+ * one is one (68 bytes). Caches of one entry a token only: no compressed or
+ * key-sharded ones. */
 typedef struct idx_token_pool {
   void* base;
   int64_t page_stride, token_stride, piece_stride;
@@ -836,7 +837,8 @@ typedef struct idx_token_pool {
  * without sets IDX_DEV_BAD_REF and stays at 0). A page outside the pools sets
  * IDX_DEV_BAD_BLOCK, its moves or references are left out; lengths outside the
  * table, or L < Q, set IDX_DEV_BAD_LEN and leave the request as it is. The pages
- * of the new tokens belong to one row each.
+ * of the new tokens belong to one row each, and the pools do not overlap (the same
+ * one twice is IDX_ERR_INVALID_ARG).
  */
 idx_status indexer_commit_tree(const idx_token_pool* pools, int32_t num_pools, int64_t num_pages,
                                const int32_t* block_table, int64_t bt_stride, int32_t bt_width,

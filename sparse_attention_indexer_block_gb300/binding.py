@@ -927,7 +927,8 @@ def indexer_commit_tree(pools, block_table, seq_lens, query_start_loc, accepted,
                         dev_error=None, stream=None):
     """Keeps every request's accepted nodes (accepted int32 [requests, n]: ascending, then -1) of its
     tree of new tokens and drops the others: in every pool (tensors [pages, 64, ...] of keys or
-    values, uint8 index caches [pages, 8448] or [pages, 4352]) their tokens move to the tree's first
-    places, seq_lens becomes L - Q + accepted nodes, and the pages that a row no longer holds lose a
-    reference in ref_counts (int32 [pages]), all in place. Rows of block_table are the requests."""
+    values, uint8 index caches [pages, 8448] or [pages, 4352], none twice) their tokens move to the
+    tree's first places, seq_lens becomes L - Q + accepted nodes, and the pages that a row no longer
+    holds lose a reference in ref_counts (int32 [pages]), all in place. Rows of block_table are the
+    requests."""
     _native().commit_tree(pools, block_table, seq_lens, query_start_loc, accepted, ref_counts, dev_error, stream)

@@ -1,6 +1,8 @@
 // Trees of drafted tokens: what they ask of attention, and the accepted path
 // kept in the caches.
 #include <algorithm>
+#include <memory>
+#include <new>
 
 #include "internal.h"
 
@@ -269,6 +271,15 @@ __global__ void __launch_bounds__(kMoveThreads)
   if (first) p.seq_lens[b] = left;
 }
 
+// Whether two pools begin at the same place: moved twice, a token would end up where another's is.
+bool same_pool_twice(const idx_token_pool* pools, int32_t n) {
+  const std::unique_ptr<uintptr_t[]> at(n > 1 ? new (std::nothrow) uintptr_t[n] : nullptr);
+  if (!at) return false;
+  for (int32_t i = 0; i < n; ++i) at[i] = reinterpret_cast<uintptr_t>(pools[i].base);
+  std::sort(at.get(), at.get() + n);
+  return std::adjacent_find(at.get(), at.get() + n) != at.get() + n;
+}
+
 }  // namespace
 }  // namespace saib
 
@@ -324,6 +335,7 @@ idx_status indexer_commit_tree(const idx_token_pool* pools, int32_t num_pools, i
         static_cast<int64_t>(t.pieces) * t.piece_bytes > INT32_MAX)
       return IDX_ERR_INVALID_ARG;
   }
+  if (same_pool_twice(pools, num_pools)) return IDX_ERR_INVALID_ARG;
   if (num_reqs == 0) return IDX_OK;
   if (!block_table || !seq_lens || !query_start_loc || (max_accepted && !accepted) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) ||

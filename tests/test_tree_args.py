@@ -128,6 +128,8 @@ def test_commit_tree_refusals(lib):
                  dict(page_stride=-4), dict(page_stride=2), dict(token_stride=-4), dict(token_stride=6),
                  dict(piece_stride=-4), dict(piece_stride=2), dict(pieces=1 << 24, piece_bytes=1 << 10)):
         assert call(0, _token_pool(**over)) == INVALID, over
+    two = (binding.TokenPool * 2)(*_token_pool(), *_token_pool())
+    assert f(two, 2, *base[2:]) == INVALID                       # the same pool twice
     for at, value in ((0, None), (1, -1), (2, 0), (2, 1 << 31), (3, None), (4, 3), (5, 0), (6, -1), (7, None), (8, None),
                       (9, None), (10, 7), (11, -1), (3, FAKE + 2), (9, FAKE + 1), (12, FAKE + 2)):
         assert call(at, value) == INVALID, (at, value)
