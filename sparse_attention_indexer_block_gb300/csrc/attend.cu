@@ -795,35 +795,46 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_rows_kernel(const Atten
              i += p.cluster * (kWarps * 32)) {
           const int r = i / (D / 4), d = i % (D / 4) * 4;
           const uint32_t part_at = smem_u32(&s_part[r]), o_at = smem_u32(join + r * kPitch + d);
-          float bm[kMostCluster], bl[kMostCluster];
-          float4 bo[kMostCluster];
-#pragma unroll
-          for (int b = 0; b < kMostCluster; ++b) {
-            bm[b] = -INFINITY;
-            bl[b] = 0.f;
-            bo[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (b < p.cluster) {
-              const uint32_t at = cluster_addr(part_at, b);
-              bm[b] = cluster_load(at);
-              bl[b] = cluster_load(at + 4);
-              bo[b] = cluster_load4(cluster_addr(o_at, b));
-            }
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int b = 0; b < kMostCluster; ++b) mx = fmaxf(mx, bm[b]);
-          const float base = mx == -INFINITY ? 0.f : mx;
-          float sum = 0.f;
+          float mx = -INFINITY, sum = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          // (eight blocks at a time; a tree's cluster may have sixteen)
+          const auto add = [&](int b0) {
+            float bm[kMostCluster], bl[kMostCluster];
+            float4 bo[kMostCluster];
 #pragma unroll
-          for (int b = 0; b < kMostCluster; ++b) {
-            const float f = exp2_approx(bm[b] - base);
-            sum += f * bl[b];
-            v.x += f * bo[b].x;
-            v.y += f * bo[b].y;
-            v.z += f * bo[b].z;
-            v.w += f * bo[b].w;
-          }
+            for (int b = 0; b < kMostCluster; ++b) {
+              bm[b] = -INFINITY;
+              bl[b] = 0.f;
+              bo[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (b0 + b < p.cluster) {
+                const uint32_t at = cluster_addr(part_at, b0 + b);
+                bm[b] = cluster_load(at);
+                bl[b] = cluster_load(at + 4);
+                bo[b] = cluster_load4(cluster_addr(o_at, b0 + b));
+              }
+            }
+            float top = mx;
+#pragma unroll
+            for (int b = 0; b < kMostCluster; ++b) top = fmaxf(top, bm[b]);
+            const float base = top == -INFINITY ? 0.f : top;
+            if (b0) {
+              const float keep = exp2_approx(mx - base);
+              sum *= keep;
+              v = make_float4(v.x * keep, v.y * keep, v.z * keep, v.w * keep);
+            }
+            mx = top;
+#pragma unroll
+            for (int b = 0; b < kMostCluster; ++b) {
+              const float f = exp2_approx(bm[b] - base);
+              sum += f * bl[b];
+              v.x += f * bo[b].x;
+              v.y += f * bo[b].y;
+              v.z += f * bo[b].z;
+              v.w += f * bo[b].w;
+            }
+          };
+          add(0);
+          if (kTree && p.cluster > kMostCluster) add(kMostCluster);
           write_row(r, d, mx, sum, v);
         }
         cluster_sync();  // (the results are read before their memory is used again)
@@ -1175,7 +1186,9 @@ idx_status launch_cluster_as(const AttendParams& p, cudaStream_t s) {
   using C = RowsCfg<D, 1>;
   const auto kernel = attend_rows_kernel<T, D, 1, kSel, true, kTree>;
   static std::atomic<bool> configured[kMaxDevices];
-  const cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
+  cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
+  if (e == cudaSuccess && p.cluster > kMostCluster)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);

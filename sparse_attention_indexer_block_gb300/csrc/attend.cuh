@@ -461,6 +461,7 @@ __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost
 // (4 us).
 constexpr int kSelfPlanReqs = 512, kSelfPlanEntries = 8;
 constexpr int kMostCluster = 8;
+constexpr int kMostTreeCluster = 16;  // (more than eight is asked for at the launch)
 
 // The cuts at both ends of a CTA's range and its first request's shape, by its
 // kThreads threads; `cost` has room for num_reqs + 1. p.bound gets them too, for the join.

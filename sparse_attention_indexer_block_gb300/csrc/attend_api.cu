@@ -77,6 +77,13 @@ bool warp_per_list(const AttendParams& p, int head_dim, const Variant& v) {
   return warp_time < cta_time;
 }
 
+// Blocks of a cluster, as many as the device and the tiles have room for.
+int cluster_size(int64_t units, int64_t tiles, int widest, const Variant& v) {
+  int c = widest;
+  while (c > 1 && (units * c > v.grid || c >= 2 * tiles)) c /= 2;
+  return c;
+}
+
 // Blocks of a cluster that share each of `units` units of at most `tiles` tiles, with no plan, no
 // partial results in memory and no second launch; 0 where cutting all tiles evenly over the device
 // is faster. A block takes 0.9 us a tile and 4; the cut's blocks take fewer tiles, but 11 more (for a
@@ -84,26 +91,34 @@ bool warp_per_list(const AttendParams& p, int head_dim, const Variant& v) {
 // keys 11.5 / 6.2, 6000: 16.0 / 14.5, 12 000: 18.6 / 24.3; 16 of 1000: 19.1 / 13.3, of 3000: 40 /
 // 35; 4 tokens with lists of 512: 18.1 / 6.2, 32 with 2048: 37 / 32. `most` bounds a block's tiles
 // where lengths may differ, for only the cut evens them out.
-int cluster_blocks(int64_t units, int64_t tiles, int64_t slack, int64_t most, const Variant& v) {
-  int c = kMostCluster;
-  while (c > 1 && (units * c > v.grid || c >= 2 * tiles)) c /= 2;
+int cluster_blocks(int64_t units, int64_t tiles, int64_t slack, int64_t most, const Variant& v,
+                   int widest = kMostCluster) {
+  const int c = cluster_size(units, tiles, widest, v);
   const int64_t one = (tiles + c - 1) / c;
   return units * c <= v.grid && one <= most && one <= tiles * units / v.grid + slack ? c : 0;
 }
 
 // The same for trees of up to kClusterEntries blocks of rows, a cluster for each, against the chunk
 // kernel: a cluster's block takes 5.5 us and 1 a tile, the chunk kernel with its plan and join some
-// 17 and, with all of the keys cut evenly over the device, 1.5 (D = 64: 0.9) a tile of 128 keys.
-// us, chunk kernel / clusters, D = 128, 8 kv heads: one tree of 32 rows over 1000 keys 16.2 / 8.2,
-// 8000: 32.0 / 21.1; of 96 rows over 2000 20.1 / 14.6, 8000: 32.6 / 36.8; four of 64 over 1000:
-// 18.7 / 15.2, 2000: 20.8 / 22.6; D = 64, one of 32 over 8000: 26.0 / 12.7, four of 64: 27.7 / 34.8.
-// (Of 72 such sizes the rule picks the slower side twice, by 7 %.)
+// 16 and, with all of the keys cut evenly over the device, 1.5 (D = 64: 0.9) a tile of 128 keys.
+// us, chunk kernel / clusters, D = 128, 8 kv heads: one tree of 32 rows over 1000 keys 16.9 / 8.3,
+// 4000: 19.6 / 14.4; of 96 rows over 2000 19.7 / 14.6, 8000: 22.4 / 36.8; four of 64 over 1000:
+// 17.4 / 15.2, 2000: 19.3 / 22.6; eight of 32 over 2000: 25.3 / 22.8; D = 64, one of 32 over 8000:
+// 17.2 / 13.0, 16 000: 18.9 / 20.0.
 constexpr int64_t kClusterEntries = 8;
-int tree_cluster_blocks(int64_t units, int64_t pairs, int64_t tiles, int head_dim, const Variant& v) {
-  int c = kMostCluster;
-  while (c > 1 && (units * c > v.grid || c >= 2 * tiles)) c /= 2;
+
+// A tree's clusters have sixteen blocks where all run at once (one per GPC, of which there are eight)
+// and the tiles are many: 8 units of 4000 keys of 128 12.3 us with eight blocks, 11.4 with sixteen,
+// 8000: 18.5, 15.3, but 1000: 7.5, 8.1; 16 units of 4000: 14.1, 19.9.
+constexpr int kGpcs = 8;
+int tree_widest(int64_t units, int64_t tiles) {
+  return units <= kGpcs && tiles > 32 ? kMostTreeCluster : kMostCluster;
+}
+int tree_cluster_blocks(int64_t units, int64_t pairs, int64_t tiles, int head_dim, int widest,
+                        const Variant& v) {
+  const int c = cluster_size(units, tiles, widest, v);
   const int64_t wide = head_dim == 64 ? 9 * tiles : 15 * tiles / 2;  // tenths of us of a chunk unit
-  return units * c <= v.grid && (tiles + c - 1) / c <= 12 + pairs * wide / (10 * device_sm_count()) ? c : 0;
+  return units * c <= v.grid && (tiles + c - 1) / c <= 10 + pairs * wide / (10 * device_sm_count()) ? c : 0;
 }
 
 constexpr int64_t kLittleTiles = 12;  // a block's
@@ -260,8 +275,10 @@ idx_status attend_new_tokens(const idx_attend* a, const Tree* tree, void* stream
   const int64_t entries = (longest * p.group + few.rows - 1) / few.rows;
   if (entries <= (tree ? kClusterEntries : 1)) {
     const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads * entries;
-    p.cluster = entries == 1 ? cluster_blocks(units, tiles_of(few), 10, 16, few)
-                             : tree_cluster_blocks(units, units / entries, tiles_of(few), a->head_dim, few);
+    const int64_t tiles = tiles_of(few);
+    const int widest = tree ? tree_widest(units, tiles) : kMostCluster;
+    p.cluster = entries == 1 ? cluster_blocks(units, tiles, tree ? 8 : 10, 16, few, widest)
+                             : tree_cluster_blocks(units, units / entries, tiles, a->head_dim, widest, few);
     if (p.cluster) {
       p.grid = static_cast<int32_t>(units * p.cluster);
       p.cluster_entries = static_cast<int32_t>(entries);

@@ -854,11 +854,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Join of a tree's units that several CTAs share. Block (c, y): 32 rows of the unit whose first piece
-// ends CTA c's range, a thread per row and 32 of its values; only cuts inside a unit leave work. The
-// pieces are joined in the order of the CTAs, so the result does not depend on timing. Bound by
-// latency: the cuts, then the request's lengths and two pieces side by side.
-template <typename T, int D>
-__global__ void __launch_bounds__(D) attend_join_kernel(const __grid_constant__ AttendParams p) {
+// ends CTA c's range, a thread per row and 16 of its values; only cuts inside a unit leave work. The
+// pieces are joined in the order of the CTAs, so the result does not depend on timing, the loads of
+// kAtOnce of them side by side: two where units have few pieces (so that more blocks fit an SM; 64
+// requests of up to 4000 keys 96.5 us, with four 98.0), eight where they may have many (one of
+// 40 000 keys, 12 pieces a CTA's cut: 35 us, piece by piece 87). Bound by latency: the cuts, then the
+// request's lengths and the first pieces.
+template <typename T, int D, int kAtOnce>
+__global__ void __launch_bounds__(2 * D) attend_join_kernel(const __grid_constant__ AttendParams p) {
   const int c = blockIdx.x, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
   const int r = blockIdx.y * 32 + lane;
   constexpr int kTop = static_cast<int>(kTopWeightTc<T>);
@@ -872,17 +875,51 @@ __global__ void __launch_bounds__(D) attend_join_kernel(const __grid_constant__ 
     return make_int4(__shfl_sync(0xffffffffu, a.x, 0), __shfl_sync(0xffffffffu, a.y, 0),
                      __shfl_sync(0xffffffffu, a.z, 0), __shfl_sync(0xffffffffu, a.w, 0));
   };
-  struct Part {
-    float2 ml;
-    float4 v[8];
-  };
-  const auto load = [&](int64_t piece, Part* x) {
-    x->ml = p.part_ml[piece * p.rows + r];
+  float m = -INFINITY, l = 0.f;
+  float4 v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x->v[i] = reinterpret_cast<const float4*>(p.part_o)[part_chunk<D, true>(p, piece, r, part * 8 + i)];
+  for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // pieces 2 (c0 + bit), of the bits that are set, and piece `lead` before them
+  const auto join = [&](int64_t lead, int c0, uint32_t bits) {
+    while (lead >= 0 || bits) {
+      float2 ml[kAtOnce];
+      float4 x[kAtOnce][4];
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        ml[e] = make_float2(-INFINITY, 0.f);
+        if (lead < 0 && !bits) continue;
+        int64_t piece = lead;
+        if (lead < 0) {
+          piece = 2 * static_cast<int64_t>(c0 + __ffs(bits) - 1);
+          bits &= bits - 1;
+        }
+        lead = -1;
+        ml[e] = p.part_ml[piece * p.rows + r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[e][i] = reinterpret_cast<const float4*>(p.part_o)[part_chunk<D, true>(p, piece, r, part * 4 + i)];
+      }
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) top = fmaxf(top, ml[e].x);
+      const float base = top == -INFINITY ? 0.f : top, keep = exp2_approx(m - base);
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = make_float4(v[i].x * keep, v[i].y * keep, v[i].z * keep, v[i].w * keep);
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        if (ml[e].x == -INFINITY) continue;  // (a row without keys there, or no piece)
+        const float f = exp2_approx(ml[e].x - base);
+        l += f * ml[e].y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = make_float4(v[i].x + f * x[e][i].x, v[i].y + f * x[e][i].y, v[i].z + f * x[e][i].z,
+                             v[i].w + f * x[e][i].w);
+      }
+    }
   };
-  Part sum, x;
   int4 next = make_int4(0, 0, 0, 0);
   int64_t token = 0;
   int head = 0, rows = 0;
@@ -891,10 +928,10 @@ __global__ void __launch_bounds__(D) attend_join_kernel(const __grid_constant__ 
     const int cc = c0 + lane;
     const int4 none = make_int4(-1, -1, 0, -1);
     const int4 a = cc <= p.grid ? p.bound[cc] : none, b = cc < p.grid ? p.bound[cc + 1] : none;
+    int64_t lead = -1;
     if (c0 == c + 1) {
       next = first(a);
       if (next.z == 0 || next.w >= p.num_reqs || (same(here, next) && here.z > 0)) return;
-      load(2 * static_cast<int64_t>(c) + 1, &sum);
       const ReqShape shape = request_shape(p, next.w, false);
       Piece u;
       u.q0 = shape.q0;
@@ -905,55 +942,42 @@ __global__ void __launch_bounds__(D) attend_join_kernel(const __grid_constant__ 
       if (blockIdx.y * 32 >= rows) return;
       int pos;
       row_place(p, u, r, &token, &head, &pos);
+      lead = 2 * static_cast<int64_t>(c) + 1;
     }
     const bool in = cc < p.grid && same(a, next) && a.z > 0;
     const uint32_t all = __ballot_sync(0xffffffffu, in);
-    uint32_t full = __ballot_sync(0xffffffffu, in && !(same(b, next) && b.z == a.z));
-    while (full) {
-      load(2 * static_cast<int64_t>(c0 + __ffs(full) - 1), &x);
-      full &= full - 1;
-      const float top = fmaxf(sum.ml.x, x.ml.x), base = top == -INFINITY ? 0.f : top;
-      const float keep = exp2_approx(sum.ml.x - base), add = exp2_approx(x.ml.x - base);
-      sum.ml = make_float2(top, sum.ml.y * keep + x.ml.y * add);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sum.v[i] = make_float4(sum.v[i].x * keep + x.v[i].x * add, sum.v[i].y * keep + x.v[i].y * add,
-                               sum.v[i].z * keep + x.v[i].z * add, sum.v[i].w * keep + x.v[i].w * add);
-    }
+    join(lead, c0, __ballot_sync(0xffffffffu, in && !(same(b, next) && b.z == a.z)));
     if (all != 0xffffffffu) break;
   }
-  const float inv = sum.ml.y == 0.f ? 0.f : 1.f / sum.ml.y;
+  if (r >= rows) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t at = token * p.num_heads + head;
-  uint4 w[4];
+  // (16 values of a row are a sector)
+  uint4* const out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * D) + part * 2;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = sum.v[2 * i], g = sum.v[2 * i + 1];
-    w[i] = make_uint4(pack2<T>(f.x * inv, f.y * inv), pack2<T>(f.z * inv, f.w * inv),
-                      pack2<T>(g.x * inv, g.y * inv), pack2<T>(g.z * inv, g.w * inv));
+  for (int i = 0; i < 2; ++i) {
+    const float4 f = v[2 * i], g = v[2 * i + 1];
+    out[i] = make_uint4(pack2<T>(f.x * inv, f.y * inv), pack2<T>(f.z * inv, f.w * inv),
+                        pack2<T>(g.x * inv, g.y * inv), pack2<T>(g.z * inv, g.w * inv));
   }
-  transpose4(w, lane);
-  uint4* const out = reinterpret_cast<uint4*>(p.out);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int from = (lane & ~3) + i;
-    const int64_t row = __shfl_sync(0xffffffffu, at, from);
-    if (r - lane + from < rows) out[row * (D / 8) + part * 4 + (lane & 3)] = w[i];
-  }
-  if (part == 0 && r < rows && p.lse) p.lse[at] = row_lse<kTop>(sum.ml.x, sum.ml.y);
+  if (part == 0 && p.lse) p.lse[at] = row_lse<kTop>(m, l);
 }
 
 template <typename T, int D>
 idx_status launch_join_as(const AttendParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid, kRowsTc / 32);
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(2 * D);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p));
+  // (max_entries is a bound: the units may be fewer)
+  const bool many = int64_t{p.max_entries} * p.num_kv_heads < p.grid / 4;
+  return cuda_status(cudaLaunchKernelEx(
+      &cfg, many ? attend_join_kernel<T, D, 8> : attend_join_kernel<T, D, 2>, p));
 }
 
 // Map of a cache: [64 tokens of a page][64 of the head_dim values] boxes of one
