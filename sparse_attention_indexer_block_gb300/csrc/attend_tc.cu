@@ -981,7 +981,9 @@ idx_status launch_join_as(const AttendParams& p, cudaStream_t s) {
 }
 
 // Map of a cache: [64 tokens of a page][64 of the head_dim values] boxes of one
-// head and page.
+// head and page. What a box asks of L2 is no more than a head's row: 256 bytes at D = 64
+// bring in the next head's, which has often gone when its turn comes (43 requests of 4194 keys, 8
+// kv heads: 539 MB read instead of 369, 96 us instead of 78).
 bool encode_map(CUtensorMap* map, const void* base, bool half, int head_dim, int64_t tok,
                 int64_t head, int64_t page, int64_t heads, int64_t pages) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -1007,7 +1009,8 @@ bool encode_map(CUtensorMap* map, const void* base, bool half, int head_dim, int
   return encode(map,
                 half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                 const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_SWIZZLE_128B,
+                head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
