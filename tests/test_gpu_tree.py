@@ -711,3 +711,50 @@ def test_tree_of_a_batch_whose_hint_is_smaller_than_its_trees():
             b.table = wide
         for hint in (1, 2, 9, 50):
             b.check(b.attend_tree(max_query_len=hint), b.reference_tree())
+
+
+def test_trees_on_two_streams_at_once():
+    """Two batches side by side, each with its own outputs and what the call allocates: as one after the other."""
+    batches = [TreeBatch([20, 40, 9], [6000, 300, 9000], 16, 2, 128, BF, seed=30),
+               TreeBatch([8], [3000], 16, 4, 64, FP, seed=31), TreeBatch([60] * 4, [2000] * 4, 12, 4, 64, FP, seed=32)]
+    want = [b.attend_tree() for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in batches]
+    for _ in range(20):
+        for b, s, g in zip(batches, streams, got):
+            g.append(saib.indexer_attend_tree(b.q, b.k, b.v, b.table, b.lens, b.start, b.masks, max(b.ql), stream=s))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)
+
+
+def test_tree_without_lse_through_the_c_entry():
+    import ctypes as C
+
+    from sparse_attention_indexer_block_gb300 import binding
+    for ql, kl in (([8], [500]), ([50, 3], [20000, 90])):
+        b = TreeBatch(ql, kl, 8, 2, 128, BF, seed=33)
+        want = b.attend_tree()
+        out, ws = torch.empty_like(b.q), saib.attend_workspace(b.rows, len(ql), 8, 2, 128)
+        a = binding.Attend(q=b.q.data_ptr(), k=b.k.data_ptr(), v=b.v.data_ptr(), block_table=b.table.data_ptr(),
+                           seq_lens=b.lens.data_ptr(), query_start_loc=b.start.data_ptr(), out=out.data_ptr(),
+                           workspace=ws.data_ptr(), workspace_bytes=ws.numel(), q_stride_token=b.q.stride(0),
+                           q_stride_head=b.q.stride(1), num_pages=b.k.shape[0], bt_stride=b.table.stride(0),
+                           bt_width=b.table.shape[1], num_reqs=len(ql), num_tokens=b.rows, num_heads=8, num_kv_heads=2,
+                           head_dim=128, dtype=0, max_query_len=max(ql), scale=128 ** -0.5,
+                           **{f"{c}_stride_{d}": t.stride(i) for c, t in (("k", b.k), ("v", b.v))
+                              for i, d in enumerate(("page", "token", "head"))})
+        st = saib.load().indexer_attend_tree(C.byref(a), b.masks.data_ptr(), b.words, b.words, None,
+                                             torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == 0 and torch.equal(out, want[0])
+
+
+@pytest.mark.parametrize("kl,ql,heads,kv,dim", [([4500], [8], 32, 8, 128), ([9000, 5000], [4, 8], 8, 2, 128),
+                                                ([12000], [16], 8, 1, 64), ([7000], [1], 16, 4, 64)])
+def test_tree_in_clusters_of_sixteen(kl, ql, heads, kv, dim):
+    b = TreeBatch(ql, kl, heads, kv, dim, BF, seed=34)
+    b.check(b.attend_tree(), b.reference_tree())
+    b.check(b.attend_tree(window=6000, sinks=5), b.reference_tree(6000, 5))
