@@ -240,7 +240,7 @@ def _places(case):
         n = min(case["tokens"] - len(out), _spread(rng, 1, 4096))
         at = rng.randrange(max(1, case["far"] - n))
         step = rng.choice([1, 1, 2])
-        out += [min(at + i // step, case["far"] - 1) for i in range(n)]
+        out += [at + i // step for i in range(n)]
     return out
 
 
