@@ -884,10 +884,12 @@ __global__ void __launch_bounds__(2 * D) attend_join_kernel(const __grid_constan
     while (lead >= 0 || bits) {
       float2 ml[kAtOnce];
       float4 x[kAtOnce][4];
+      int n = 0;  // pieces that there are
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e) {
         ml[e] = make_float2(-INFINITY, 0.f);
         if (lead < 0 && !bits) continue;
+        n = e + 1;
         int64_t piece = lead;
         if (lead < 0) {
           piece = 2 * static_cast<int64_t>(c0 + __ffs(bits) - 1);
@@ -910,7 +912,9 @@ __global__ void __launch_bounds__(2 * D) attend_join_kernel(const __grid_constan
         v[i] = make_float4(v[i].x * keep, v[i].y * keep, v[i].z * keep, v[i].w * keep);
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e) {
-        if (ml[e].x == -INFINITY) continue;  // (a row without keys there, or no piece)
+        // (a row without keys there adds zeros; one of NaN scores alone, whose maximum is that of no
+        // key too, has a NaN sum and makes the row NaN)
+        if (e >= n) continue;
         const float f = exp2_approx(ml[e].x - base);
         l += f * ml[e].y;
 #pragma unroll
