@@ -248,7 +248,9 @@ __global__ void __launch_bounds__(kMoveThreads)
     if (n < kMoves) break;
     __syncthreads();
   }
+  // every thread has read the length (a block alone whose lists are empty has met no barrier yet)
   if (p.blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else __syncthreads();
   if (rank != 0 || !p.last) return;
   if (!ok) {
     if (first) set_error(p.err, IDX_DEV_BAD_LEN);
