@@ -1181,28 +1181,55 @@ idx_status launch_rows_as(const AttendParams& p, cudaStream_t s) {
   return cuda_status(launch_pdl(kernel, p.grid, kWarps * 32, C::kSmem, s, p));
 }
 
-template <typename T, int D, bool kSel, bool kTree>
-idx_status launch_cluster_as(const AttendParams& p, cudaStream_t s) {
-  using C = RowsCfg<D, 1>;
-  const auto kernel = attend_rows_kernel<T, D, 1, kSel, true, kTree>;
-  static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = allow_smem<C::kSmem, 0>(kernel, configured);
-  if (e == cudaSuccess && p.cluster > kMostCluster)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return cuda_status(e);
+// A launch of clusters of `cluster` blocks; attr has room for two.
+template <typename T, int D>
+cudaLaunchConfig_t cluster_config(int grid, int cluster, cudaLaunchAttribute* attr, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = RowsCfg<D, 1>::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
+  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  return cfg;
+}
+
+template <typename T, int D, bool kSel, bool kTree>
+idx_status launch_cluster_as(const AttendParams& p, cudaStream_t s) {
+  const auto kernel = attend_rows_kernel<T, D, 1, kSel, true, kTree>;
+  static std::atomic<bool> configured[kMaxDevices];
+  const cudaError_t e = allow_smem<RowsCfg<D, 1>::kSmem, 0>(kernel, configured);
+  if (e != cudaSuccess) return cuda_status(e);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = cluster_config<T, D>(p.grid, p.cluster, attr, s);
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+// Allows a tree's clusters of kMostTreeCluster blocks, and asks how many the current device runs at once.
+template <typename T, int D>
+int wide_clusters_as() {
+  const auto kernel = attend_rows_kernel<T, D, 1, false, true, true>;
+  static std::atomic<int> cached[kMaxDevices];  // one more than the answer; 0: not asked yet
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < kMaxDevices) {
+    const int c = cached[dev].load(std::memory_order_acquire);
+    if (c > 0) return c - 1;
+  }
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = cluster_config<T, D>(kMostTreeCluster, kMostTreeCluster, attr, nullptr);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D, 1>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    n = 0;
+    cudaGetLastError();  // (a device without room for one is no error of the call)
+  }
+  if (dev < kMaxDevices) cached[dev].store(n + 1, std::memory_order_release);
+  return n;
 }
 
 template <typename T, int D>
@@ -1247,6 +1274,11 @@ idx_status launch_combine_as(const AttendParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+int attend_wide_clusters(int head_dim, bool half) {
+  if (half) return head_dim == 64 ? wide_clusters_as<__half, 64>() : wide_clusters_as<__half, 128>();
+  return head_dim == 64 ? wide_clusters_as<__nv_bfloat16, 64>() : wide_clusters_as<__nv_bfloat16, 128>();
+}
 
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s) {
   return cuda_status(launch_pdl(p.masks ? attend_plan_kernel<true> : attend_plan_kernel<false>, 1,

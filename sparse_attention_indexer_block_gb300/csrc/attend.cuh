@@ -461,7 +461,7 @@ __device__ inline int4 cut_at_request(const AttendParams& p, const int64_t* cost
 // (4 us).
 constexpr int kSelfPlanReqs = 512, kSelfPlanEntries = 8;
 constexpr int kMostCluster = 8;
-constexpr int kMostTreeCluster = 16;  // (more than eight is asked for at the launch)
+constexpr int kMostTreeCluster = 16;  // (more than eight where the device has room for them)
 
 // The cuts at both ends of a CTA's range and its first request's shape, by its
 // kThreads threads; `cost` has room for num_reqs + 1. p.bound gets them too, for the join.
@@ -515,6 +515,10 @@ inline cudaError_t allow_smem(Kernel* kernel, std::atomic<bool>* configured) {
   if (e == cudaSuccess && cached) configured[dev].store(true, std::memory_order_release);
   return e;
 }
+
+// Clusters of kMostTreeCluster blocks of a tree's row-block kernel that the current device runs at once
+// (0: none can be placed).
+int attend_wide_clusters(int head_dim, bool half);
 
 // Launchers.
 idx_status launch_attend_plan(const AttendParams& p, cudaStream_t s);

@@ -107,12 +107,13 @@ int cluster_blocks(int64_t units, int64_t tiles, int64_t slack, int64_t most, co
 // 17.2 / 13.0, 16 000: 18.9 / 20.0.
 constexpr int64_t kClusterEntries = 8;
 
-// A tree's clusters have sixteen blocks where all run at once (one per GPC, of which there are eight)
-// and the tiles are many: 8 units of 4000 keys of 128 12.3 us with eight blocks, 11.4 with sixteen,
-// 8000: 18.5, 15.3, but 1000: 7.5, 8.1; 16 units of 4000: 14.1, 19.9.
+// A tree's clusters have sixteen blocks where all run at once (one per GPC, of which there are eight, and
+// as many as the device says it has room for) and the tiles are many: 8 units of 4000 keys of 128 12.3 us
+// with eight blocks, 11.4 with sixteen, 8000: 18.5, 15.3, but 1000: 7.5, 8.1; 16 units of 4000: 14.1, 19.9.
 constexpr int kGpcs = 8;
-int tree_widest(int64_t units, int64_t tiles) {
-  return units <= kGpcs && tiles > 32 ? kMostTreeCluster : kMostCluster;
+int tree_widest(int64_t units, int64_t tiles, int head_dim, bool half) {
+  return units <= kGpcs && tiles > 32 && units <= attend_wide_clusters(head_dim, half) ? kMostTreeCluster
+                                                                                       : kMostCluster;
 }
 int tree_cluster_blocks(int64_t units, int64_t pairs, int64_t tiles, int head_dim, int widest,
                         const Variant& v) {
@@ -276,7 +277,7 @@ idx_status attend_new_tokens(const idx_attend* a, const Tree* tree, void* stream
   if (entries <= (tree ? kClusterEntries : 1)) {
     const int64_t units = static_cast<int64_t>(a->num_reqs) * p.num_kv_heads * entries;
     const int64_t tiles = tiles_of(few);
-    const int widest = tree ? tree_widest(units, tiles) : kMostCluster;
+    const int widest = tree ? tree_widest(units, tiles, a->head_dim, half) : kMostCluster;
     p.cluster = entries == 1 ? cluster_blocks(units, tiles, tree ? 8 : 10, 16, few, widest)
                              : tree_cluster_blocks(units, units / entries, tiles, a->head_dim, widest, few);
     if (p.cluster) {
