@@ -11,6 +11,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -151,17 +152,29 @@ class On {
   cudaStream_t stream_ = nullptr;
 };
 
+// Lets go of the interpreter's lock: an allocation may wait for the device, and so may a launch.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+  const at::TensorOptions options = at::TensorOptions().dtype(type).device(like.device());
+  const Unlocked unlocked;
+  return at::empty(shape, options);
 }
 
 // Runs a function of the library without the interpreter's lock.
 template <typename F>
 idx_status unlocked(const F& f) {
-  PyThreadState* s = PyEval_SaveThread();
-  const idx_status st = f();
-  PyEval_RestoreThread(s);
-  return st;
+  const Unlocked unlocked;
+  return f();
 }
 
 void check(idx_status st) {
@@ -175,10 +188,12 @@ PyObject* result(PyObject* given, const Tensor& made) {
   return given;
 }
 
-// Calls f and turns what it throws into Python exceptions.
+// Calls f and turns what it throws into Python exceptions (what torch throws into torch's own:
+// OutOfMemoryError among them).
 template <typename F>
 PyObject* guarded(const char* name, Py_ssize_t n, Py_ssize_t want, const F& f) {
   if (n != want) return PyErr_Format(PyExc_TypeError, "%s: %zd arguments, not %zd", name, n, want);
+  HANDLE_TH_ERRORS
   try {
     return f();
   } catch (const Refusal& r) {
@@ -188,10 +203,9 @@ PyObject* guarded(const char* name, Py_ssize_t n, Py_ssize_t want, const F& f) {
       Py_DECREF(e);
     }
   } catch (const PythonError&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 int32_t type_code(const Tensor& t, const char* what) {
