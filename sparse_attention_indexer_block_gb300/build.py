@@ -18,6 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsaib.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
+OBJECTS = os.path.join(HERE, "_build")
+STAMP = os.path.join(OBJECTS, "marshal.txt")  # what _marshal.so was built for
 SOURCES = ["api.cu", "prep.cu", "score_select.cu", "row_select.cu", "dcp.cu",
            "block_select.cu", "no_alloc.cu", "attend_api.cu", "attend.cu", "attend_tc.cu", "pages.cu",
            "append.cu", "tree.cu"]
@@ -33,12 +35,22 @@ def _nvcc() -> str:
     return cand
 
 
+def _made_for() -> str:
+    """What the marshalling module is built for: its objects' layouts are this Python's and this torch's."""
+    import torch
+
+    return f"{sysconfig.get_config_var('EXT_SUFFIX')} torch {torch.__version__} cxx11 {int(torch.compiled_with_cxx11_abi())}"
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL) or not os.path.exists(STAMP):
         return True
+    with open(STAMP) as f:
+        if f.read() != _made_for():
+            return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "indexer.h"))
+    deps += [os.path.join(HERE, "..", "include", "indexer.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
@@ -61,24 +73,25 @@ def _link_marshal(obj: str) -> None:
                     "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,--allow-shlib-undefined"],
                    check=True)
     os.replace(tmp, MARSHAL)
+    with open(STAMP, "w") as f:
+        f.write(_made_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     nvcc = _nvcc()
-    objdir = os.path.join(HERE, "_build")
-    os.makedirs(objdir, exist_ok=True)
+    os.makedirs(OBJECTS, exist_ok=True)
     procs = []
     objs = []
     for src in SOURCES:
-        obj = os.path.join(objdir, src.replace(".cu", ".o"))
+        obj = os.path.join(OBJECTS, src.replace(".cu", ".o"))
         objs.append(obj)
         cmd = [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    marshal = os.path.join(objdir, "marshal.o")
+    marshal = os.path.join(OBJECTS, "marshal.o")
     procs.append(("marshal.cpp", subprocess.Popen(_marshal_command(nvcc, marshal), stdout=subprocess.PIPE,
                                                   stderr=subprocess.STDOUT)))
     failed = []
