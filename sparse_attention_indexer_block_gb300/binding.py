@@ -166,6 +166,7 @@ def load(path: str = LIB_PATH):
             fn.argtypes = args
         from . import _marshal as marshal
         marshal.set_error_class(IndexerError)
+        marshal.bind(lib._handle)
         global _marshal
         _marshal = marshal
         _lib = lib

@@ -69,9 +69,8 @@ def _link_marshal(obj: str) -> None:
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libsaib.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}",
-                    "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,--allow-shlib-undefined"],
-                   check=True)
+    subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+                    "-lc10", "-ldl", "-Wl,--allow-shlib-undefined"], check=True)
     os.replace(tmp, MARSHAL)
     with open(STAMP, "w") as f:
         f.write(_made_for())

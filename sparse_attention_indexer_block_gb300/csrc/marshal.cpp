@@ -14,9 +14,12 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <dlfcn.h>
+
 #include <cmath>
 #include <initializer_list>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/indexer.h"
@@ -26,6 +29,20 @@ namespace {
 using at::Tensor;
 
 PyObject* g_error = nullptr;  // IndexerError
+
+// The functions of the library that the binding has loaded.
+struct Library {
+  decltype(&indexer_attend_paged) attend_paged;
+  decltype(&indexer_attend_selected) attend_selected;
+  decltype(&indexer_attend_tree) attend_tree;
+  decltype(&indexer_attend_workspace_bytes) attend_workspace_bytes;
+  decltype(&indexer_append_kv) append_kv;
+  decltype(&indexer_insert_keys_mxfp4) insert_keys_mxfp4;
+  decltype(&indexer_plan_tree) plan_tree;
+  decltype(&indexer_commit_tree) commit_tree;
+  decltype(&indexer_last_cuda_error) last_cuda_error;
+};
+Library g_lib = {};
 
 struct Refusal {
   idx_status status;
@@ -178,7 +195,7 @@ idx_status unlocked(const F& f) {
 }
 
 void check(idx_status st) {
-  if (st != IDX_OK) throw Refusal{st, st == IDX_ERR_CUDA ? indexer_last_cuda_error() : ""};
+  if (st != IDX_OK) throw Refusal{st, st == IDX_ERR_CUDA ? g_lib.last_cuda_error() : ""};
 }
 
 // A new reference to a result: the caller's own object, or a new tensor's.
@@ -320,9 +337,9 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       c.workspace = at;
       c.workspace_bytes = bytes;
       return unlocked([&] {
-        return form == kPaged      ? indexer_attend_paged(&c, on.stream())
-               : form == kSelected ? indexer_attend_selected(&c, on.stream())
-                                   : indexer_attend_tree(&c, at_of<const int32_t>(masks), mask_stride,
+        return form == kPaged      ? g_lib.attend_paged(&c, on.stream())
+               : form == kSelected ? g_lib.attend_selected(&c, on.stream())
+                                   : g_lib.attend_tree(&c, at_of<const int32_t>(masks), mask_stride,
                                                          static_cast<int32_t>(words),
                                                          at_of<const int32_t>(positions), on.stream());
       });
@@ -335,7 +352,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if ((form == kSelected ? tokens : reqs) * kv_heads <= kFewUnits) st = run(nullptr, 0);
       if (st == IDX_ERR_WORKSPACE) {
         size_t bytes = 0;
-        check(indexer_attend_workspace_bytes(c.num_tokens, c.num_reqs, c.num_heads, c.num_kv_heads, c.head_dim,
+        check(g_lib.attend_workspace_bytes(c.num_tokens, c.num_reqs, c.num_heads, c.num_kv_heads, c.head_dim,
                                              &bytes));
         const Tensor made = fresh({static_cast<int64_t>(bytes)}, at::kByte, q);
         st = run(made.data_ptr(), bytes);
@@ -445,7 +462,7 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c.num_tokens = static_cast<int32_t>(tokens);
     c.num_kv_heads = static_cast<int32_t>(kv_heads);
     c.head_dim = static_cast<int32_t>(dim);
-    check(unlocked([&] { return indexer_append_kv(&c, on.stream()); }));
+    check(unlocked([&] { return g_lib.append_kv(&c, on.stream()); }));
     if (!q) Py_RETURN_NONE;
     return result(a[9], made);
   });
@@ -469,7 +486,7 @@ PyObject* insert_keys_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int index = need_device({&k, &slots, &cache, values, error});
     const On on(index, a[5]);
     check(unlocked([&] {
-      return indexer_insert_keys_mxfp4(k.data_ptr(), tokens > 1 ? k.stride(0) : dim, at_of<const int64_t>(slots),
+      return g_lib.insert_keys_mxfp4(k.data_ptr(), tokens > 1 ? k.stride(0) : dim, at_of<const int64_t>(slots),
                                        tokens, static_cast<int32_t>(dim), at_of<uint8_t>(cache), cache.size(0),
                                        at_of<void>(values), at_of<uint32_t>(error), on.stream());
     }));
@@ -513,7 +530,7 @@ PyObject* plan_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor made_paths = paths || !width ? Tensor() : fresh({tokens, width}, at::kInt, parents);
     int32_t* const path = width ? at_of<int32_t>(paths ? *paths : made_paths) : nullptr;
     check(unlocked([&] {
-      return indexer_plan_tree(at_of<const int32_t>(parents), at_of<const int32_t>(lens),
+      return g_lib.plan_tree(at_of<const int32_t>(parents), at_of<const int32_t>(lens),
                                at_of<const int32_t>(start), static_cast<int32_t>(reqs),
                                static_cast<int32_t>(tokens), window, sinks,
                                at_of<int32_t>(masks ? *masks : made_masks), static_cast<int32_t>(words),
@@ -624,7 +641,7 @@ PyObject* commit_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!items[i].is_cuda() || items[i].get_device() != index) refuse("tensors are on different devices");
     const On on(index, a[7]);
     check(unlocked([&] {
-      return indexer_commit_tree(pools.data(), static_cast<int32_t>(pools.size()), pages,
+      return g_lib.commit_tree(pools.data(), static_cast<int32_t>(pools.size()), pages,
                                  at_of<const int32_t>(table), bt_stride, static_cast<int32_t>(table.size(1)),
                                  static_cast<int32_t>(reqs), at_of<int32_t>(lens), at_of<const int32_t>(start),
                                  at_of<const int32_t>(accepted), stride, static_cast<int32_t>(accepted.size(1)),
@@ -655,6 +672,27 @@ PyObject* token_pools(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// bind(handle): takes the functions from a library that dlopen has returned.
+PyObject* bind(PyObject*, PyObject* handle) {
+  void* const lib = PyLong_AsVoidPtr(handle);
+  if (PyErr_Occurred()) return nullptr;
+  Library found;
+  const auto get = [&](auto* at, const char* name) -> bool {
+    *at = reinterpret_cast<std::remove_reference_t<decltype(*at)>>(dlsym(lib, name));
+    if (!*at) PyErr_Format(PyExc_RuntimeError, "the library does not export %s", name);
+    return *at != nullptr;
+  };
+  if (!get(&found.attend_paged, "indexer_attend_paged") || !get(&found.attend_selected, "indexer_attend_selected") ||
+      !get(&found.attend_tree, "indexer_attend_tree") ||
+      !get(&found.attend_workspace_bytes, "indexer_attend_workspace_bytes") ||
+      !get(&found.append_kv, "indexer_append_kv") ||
+      !get(&found.insert_keys_mxfp4, "indexer_insert_keys_mxfp4") || !get(&found.plan_tree, "indexer_plan_tree") ||
+      !get(&found.commit_tree, "indexer_commit_tree") || !get(&found.last_cuda_error, "indexer_last_cuda_error"))
+    return nullptr;
+  g_lib = found;
+  Py_RETURN_NONE;
+}
+
 PyObject* set_error_class(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XSETREF(g_error, cls);
@@ -673,6 +711,7 @@ PyMethodDef g_methods[] = {
     {"plan_tree", method(plan_tree), METH_FASTCALL, nullptr},
     {"commit_tree", method(commit_tree), METH_FASTCALL, nullptr},
     {"token_pools", method(token_pools), METH_FASTCALL, nullptr},
+    {"bind", bind, METH_O, nullptr},
     {"set_error_class", set_error_class, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -1,10 +1,16 @@
 """The build and the loading of the library and its marshalling module, on the CPU."""
 import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from sparse_attention_indexer_block_gb300 import build as libbuild
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
 
 @pytest.fixture(scope="module")
 def lib():
@@ -21,3 +27,35 @@ def test_a_build_is_stale_for_another_torch_or_recipe(lib, monkeypatch):
         m.setattr(os.path, "getmtime", lambda p: real(lib) + 10 if os.path.abspath(p) == recipe else real(p))
         assert libbuild._stale()
     assert not libbuild._stale()
+
+
+def _run(code, *args):
+    r = subprocess.run([sys.executable, "-c", code, *args], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+
+
+def test_every_call_uses_the_library_that_was_loaded(lib, tmp_path):
+    other = tmp_path / "libother.so"
+    shutil.copy(lib, other)
+    _run("""
+import sys
+import sparse_attention_indexer_block_gb300 as saib
+from sparse_attention_indexer_block_gb300 import binding
+saib.load(sys.argv[1])
+assert saib.indexer_status_string(0) == "ok"
+try:
+    saib.indexer_attend_paged(*[None] * 6)
+    raise SystemExit("not refused")
+except saib.IndexerError:
+    pass
+maps = open("/proc/self/maps").read()
+assert sys.argv[1] in maps and "libsaib.so" not in maps
+""", str(other))
+
+
+def test_a_library_that_lacks_a_function_is_refused(lib):
+    import ctypes
+
+    from sparse_attention_indexer_block_gb300 import binding
+    with pytest.raises(RuntimeError, match="indexer_attend_paged"):
+        binding._native().bind(ctypes.CDLL(None)._handle)
