@@ -164,18 +164,23 @@ def load(path: str = LIB_PATH):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        from . import _marshal as marshal
-        marshal.set_error_class(IndexerError)
-        marshal.bind(lib._handle)
-        global _marshal
-        _marshal = marshal
         _lib = lib
         return lib
 
 
 def _native():
+    """The module of the calls of every layer, on the library that load() has loaded."""
+    global _marshal
     if _marshal is None:
-        load()
+        lib = load()
+        try:
+            from . import _marshal as marshal
+        except ImportError as e:
+            raise RuntimeError(f"the native marshalling is not built for this Python and torch ({e}); run "
+                               "sparse_attention_indexer_block_gb300.build.build()") from e
+        marshal.set_error_class(IndexerError)
+        marshal.bind(lib._handle)
+        _marshal = marshal
     return _marshal
 
 

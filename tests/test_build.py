@@ -53,9 +53,35 @@ assert sys.argv[1] in maps and "libsaib.so" not in maps
 """, str(other))
 
 
+def test_calls_that_pass_by_the_module_do_without_it(lib):
+    _run("""
+import sys
+sys.modules["sparse_attention_indexer_block_gb300._marshal"] = None
+import sparse_attention_indexer_block_gb300 as saib
+saib.load()
+assert saib.indexer_status_string(0) == "ok"
+try:
+    saib.indexer_attend_paged(*[None] * 6)
+    raise SystemExit("no error")
+except RuntimeError as e:
+    assert "not built" in str(e)
+""")
+
+
 def test_a_library_that_lacks_a_function_is_refused(lib):
     import ctypes
 
     from sparse_attention_indexer_block_gb300 import binding
     with pytest.raises(RuntimeError, match="indexer_attend_paged"):
         binding._native().bind(ctypes.CDLL(None)._handle)
+
+
+def test_a_build_without_the_module_leaves_the_library(lib, tmp_path, monkeypatch):
+    for name in ("LIB", "MARSHAL", "OBJECTS"):
+        monkeypatch.setattr(libbuild, name, str(tmp_path / name))
+    monkeypatch.setattr(libbuild, "SOURCES", ["no_alloc.cu"])
+    monkeypatch.setattr(libbuild, "_marshal_command", lambda nvcc, obj: ["false"])
+    monkeypatch.setattr(subprocess, "run", lambda cmd, **kw: open(cmd[cmd.index("-o") + 1], "w").close())
+    with pytest.raises(RuntimeError, match="marshal.cpp"):
+        libbuild.build(force=True)
+    assert (tmp_path / "LIB").exists() and not (tmp_path / "MARSHAL").exists()
