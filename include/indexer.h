@@ -626,7 +626,7 @@ typedef struct idx_attend {
   float scale;                    /* > 0 */
 } idx_attend;
 
-/* Bytes of workspace that either attention call needs, on the current CUDA
+/* Bytes of workspace that any of the attention calls needs, on the current CUDA
  * device, when none of its sizes is larger than these. Calls of few short units
  * (small decode steps) need none: a call with a null workspace of 0 bytes returns
  * IDX_ERR_WORKSPACE, before any work, when it does need one. */

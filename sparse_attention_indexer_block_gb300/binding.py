@@ -699,8 +699,8 @@ def _attend_workspace_bytes(device, *sizes):
 
 def attend_workspace(num_tokens: int, num_reqs: int, num_heads: int, num_kv_heads: int,
                      head_dim: int, device="cuda"):
-    """Workspace for indexer_attend_paged / indexer_attend_selected calls on that device, none of
-    whose sizes is larger than these."""
+    """Workspace for indexer_attend_paged / indexer_attend_selected / indexer_attend_tree calls on that
+    device, none of whose sizes is larger than these."""
     with torch.cuda.device(device):
         n = _attend_workspace_bytes(torch.cuda.current_device(), num_tokens, num_reqs, num_heads,
                                     num_kv_heads, head_dim)
